@@ -282,6 +282,108 @@ w8a8_status w8a8_gateup_swiglu_quant_packed(const uint16_t* x, const int8_t* w_g
                                             int8_t* q_packed, float* s_tok, void* workspace,
                                             size_t workspace_bytes, hipStream_t stream);
 
+/* ---- few tokens: projections with 4-bit weights ---------------------------------
+ * Single-token and small-batch decoding reads every weight for a handful of
+ * tokens, so the weight bytes are the time.  Here a weight is a code in [-8, 7]
+ * and each group of `group` consecutive columns (32, 64 or 128) of a row shares
+ * one bf16 scale: w[n][k] = code * scale.  Row-major form:
+ *   codes   uint8 [N, K / 2]: two codes a byte, the even column in the low half,
+ *           each stored as code + 8
+ *   scales  bf16 [N, K / group]
+ * Shapes: 0 <= N <= 2^30, K % 128 == 0, 128 <= K <= W8A8_MAX_K; `group` other than
+ * 32, 64 or 128 is W8A8_ERR_BAD_ARGUMENT. */
+
+/* Rows of w bf16 [N, K] -> codes and scales: scale = bf16(amax / 7) of the group,
+ * code = round-half-even(w / scale) clamped to +-7 (-8 is never produced); a group
+ * of zeros has scale 0 and codes 0. */
+w8a8_status w8a8_w4_quantize(const uint16_t* w, int64_t N, int64_t K, int group, uint8_t* codes,
+                             uint16_t* scales, hipStream_t stream);
+
+/* Packed form, rows rounded up to 16 (padding: codes 0, scales 0): blocks of 16
+ * rows x 128 columns, block (n / 16, k / 128) at byte
+ * ((n / 16) * (K / 128) + k / 128) * 1024.  Row r and column c of a block are in the
+ * 32-bit word at byte (16 * (c / 8 % 4) + r) * 16 + 4 * (c / 32): element j = c % 8
+ * at bit 4 * (j / 2) + 16 * (j % 2).  Scales: [N / 16][K / group][16].
+ * w8a8_w4_pack lays a weight out once, at load time. */
+size_t w8a8_w4_code_bytes(int64_t N, int64_t K);              /* 0 for N or K <= 0 */
+size_t w8a8_w4_scale_bytes(int64_t N, int64_t K, int group);  /* 0 also for a bad group */
+w8a8_status w8a8_w4_pack(const uint8_t* codes, const uint16_t* scales, int64_t N, int64_t K, int group,
+                         uint8_t* codes_packed, uint16_t* scales_packed, hipStream_t stream);
+
+/* y[m][n] = bf16( sum over groups of scale * sum(x * code) + bias[n] ), fp32 sums,
+ * one rounding.  x bf16 [M, K], bias bf16 [N] or NULL, y bf16 [M, N].  N % 8 == 0,
+ * 0 <= M <= W8A8_W4_MAX_M.  Made for M up to 64, where one pass over the weight
+ * serves every token; larger M is computed 64 tokens at a time.  A token's
+ * result does not depend on the others in the call. */
+#define W8A8_W4_MAX_M (1 << 20)
+w8a8_status w8a8_w4_linear(const uint16_t* x, const uint8_t* codes_packed, const uint16_t* scales_packed,
+                           const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K, int group,
+                           hipStream_t stream);
+
+/* ---- few tokens: a paged cache of keys and values in 8 bits ---------------------
+ * Pages of `page` tokens (16, 32, 64 or 128) for `heads` cache heads of `dim` values
+ * (64 or 128):
+ *   k_codes, v_codes  int8 [pages, heads, page, dim]
+ *   k_scale, v_scale  fp32 [pages, heads]: value = code * scale of its page and head
+ *   table             int32 [seqs, width]: the page of each block of a sequence
+ *   lens              int32 [seqs]: tokens a sequence holds, those of the newest
+ *                     append included
+ * Token p of a sequence is row p % page of page table[p / page].  A negative
+ * length counts as 0, one past width * page as width * page.  Table entries
+ * outside [0, pages) name no page: append drops the tokens that fall there, read
+ * gives zeros, attention sees no keys there.  Which pages are whose is the
+ * caller's: sequences may share pages that are only read, but two sequences of one
+ * append must not write to the same page.
+ * Limits: seqs <= W8A8_KV_MAX_SEQS, heads and q_heads <= W8A8_KV_MAX_HEADS, tokens <=
+ * W8A8_KV_MAX_TOKENS, width * page <= W8A8_KV_MAX_LENGTH, pages < 2^31. */
+#define W8A8_KV_MAX_SEQS (1 << 20)
+#define W8A8_KV_MAX_HEADS 1024
+#define W8A8_KV_MAX_TOKENS (1 << 20)
+#define W8A8_KV_MAX_LENGTH (1 << 30)
+
+/* The last `tokens` tokens of every sequence, rows k and v [seqs * tokens] of
+ * [heads, dim] bf16 values, rows ldk and ldv elements apart (>= heads * dim, a
+ * multiple of 8: slices of a wider projection), go to positions lens - tokens ..
+ * lens - 1; those at negative positions are dropped.  For each page and head that
+ * receives some: scale = max(old scale if the page holds earlier tokens of the
+ * sequence, amax / 127 of the new values), held codes become
+ * round-half-even(code * (old / new scale)), new ones round-half-even(x / scale).
+ * Filling a page in one call rounds each value once; token by token, a page's
+ * earlier codes are rounded again whenever a larger value arrives (each time by
+ * at most half a step of the new scale). */
+w8a8_status w8a8_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, int8_t* k_codes,
+                           float* k_scale, int8_t* v_codes, float* v_scale, int64_t pages, const int32_t* table,
+                           int64_t width, const int32_t* lens, int64_t seqs, int64_t tokens, int64_t heads,
+                           int64_t dim, int64_t page, hipStream_t stream);
+
+/* The sequences as bf16: k, v [seqs, length, heads, dim] = bf16(code * scale), zeros
+ * from a sequence's length on. */
+w8a8_status w8a8_kv_read(const int8_t* k_codes, const float* k_scale, const int8_t* v_codes, const float* v_scale,
+                         int64_t pages, const int32_t* table, int64_t width, const int32_t* lens, int64_t seqs,
+                         int64_t length, int64_t heads, int64_t dim, int64_t page, uint16_t* k, uint16_t* v,
+                         hipStream_t stream);
+
+/* Attention of the last `tokens` tokens of every sequence over what it holds:
+ * query i is at position p = lens - tokens + i and sees keys 0 .. p,
+ *   y = sum_j exp(scale * q.k_j - max) v_j / sum_j exp(scale * q.k_j - max);
+ * a query that sees no key (p < 0, an empty sequence) gives zeros.  q: rows
+ * [seqs * tokens] of [q_heads, dim] bf16, ldq elements apart (>= q_heads * dim, a
+ * multiple of 8); q_heads % heads == 0, query head a reads cache head
+ * a / (q_heads / heads).  y bf16 [seqs, tokens, q_heads, dim], dense.  scale is
+ * finite (usually dim^-0.5; W8A8_ERR_BAD_ARGUMENT otherwise).
+ * Sequences are cut into pieces when there are too few queries to fill the GPU;
+ * the pieces' partial results go through the workspace
+ * (w8a8_kv_attention_workspace_bytes, which may be 0: then it may be NULL; 0 also
+ * for arguments that the call refuses).  The cut depends on the shapes, not on
+ * lens' values, and results do not vary from run to run. */
+size_t w8a8_kv_attention_workspace_bytes(int64_t seqs, int64_t tokens, int64_t q_heads, int64_t heads, int64_t dim,
+                                         int64_t page, int64_t width);
+w8a8_status w8a8_kv_attention(const uint16_t* q, int64_t ldq, const int8_t* k_codes, const float* k_scale,
+                              const int8_t* v_codes, const float* v_scale, int64_t pages, const int32_t* table,
+                              int64_t width, const int32_t* lens, int64_t seqs, int64_t tokens, int64_t q_heads,
+                              int64_t heads, int64_t dim, int64_t page, float scale, uint16_t* y, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

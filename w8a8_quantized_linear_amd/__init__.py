@@ -17,7 +17,7 @@ from __future__ import annotations
 
 import ctypes
 from pathlib import Path
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -30,6 +30,8 @@ __all__ = [
     "w8a8_gemm_dequant_packed", "w8a8_gemm_swiglu_packed", "w8a8_fp8_gemm_dequant_packed",
     "w8a8_swiglu", "swiglu_quant_workspace_bytes", "w8a8_gateup_swiglu_quant_packed",
     "w8a8_gemm_i32_packed", "swiglu_quant_h", "w8a8_linear_packed_noalloc", "NOALLOC_MAX_WORKSPACE",
+    "w8a8_w4_quantize", "w8a8_w4_pack", "w8a8_w4_linear", "w4_code_bytes", "w4_scale_bytes", "KVCache", "kv_cache",
+    "w8a8_kv_append", "w8a8_kv_read", "w8a8_kv_attention", "kv_attention_workspace_bytes",
 ]
 
 LIB_PATH = Path(__file__).resolve().parent / "libw8a8.so"
@@ -40,6 +42,7 @@ if not LIB_PATH.exists():
 
 _lib = ctypes.CDLL(str(LIB_PATH))
 _P, _I64, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+_F = ctypes.c_float
 _SIGS = {
     "w8a8_status_string": (ctypes.c_char_p, [_I]),
     "w8a8_workspace_bytes": (_SZ, [_I64, _I64]),
@@ -67,6 +70,15 @@ _SIGS = {
     "w8a8_swiglu_quant_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "w8a8_linear_packed_noalloc": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P]),
     "w8a8_gateup_swiglu_quant_packed": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _P, _P, _P, _SZ, _P]),
+    "w8a8_w4_code_bytes": (_SZ, [_I64, _I64]),
+    "w8a8_w4_scale_bytes": (_SZ, [_I64, _I64, _I]),
+    "w8a8_w4_quantize": (_I, [_P, _I64, _I64, _I, _P, _P, _P]),
+    "w8a8_w4_pack": (_I, [_P, _P, _I64, _I64, _I, _P, _P, _P]),
+    "w8a8_w4_linear": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P]),
+    "w8a8_kv_append": (_I, [_P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P] + [_I64] * 5 + [_P]),
+    "w8a8_kv_read": (_I, [_P, _P, _P, _P, _I64, _P, _I64, _P] + [_I64] * 5 + [_P, _P, _P]),
+    "w8a8_kv_attention_workspace_bytes": (_SZ, [_I64] * 7),
+    "w8a8_kv_attention": (_I, [_P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P] + [_I64] * 6 + [_F, _P, _P, _SZ, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -470,3 +482,167 @@ def w8a8_gateup_swiglu_quant_packed(x, w_gateup_packed, N, s_ch, bias=None, rot_
                                                 ws.numel() * ws.element_size(), _stream()),
            "w8a8_gateup_swiglu_quant_packed")
     return q, s
+
+
+# ------------------------------------ few tokens: 4-bit weights --------------
+def w4_code_bytes(N: int, K: int) -> int:
+    return int(_lib.w8a8_w4_code_bytes(N, K))
+
+
+def w4_scale_bytes(N: int, K: int, group: int) -> int:
+    return int(_lib.w8a8_w4_scale_bytes(N, K, group))
+
+
+def w8a8_w4_quantize(w: torch.Tensor, group: int = 128):
+    """w bf16 [N, K] -> (codes uint8 [N, K / 2], scales bf16 [N, K / group]): 4-bit codes, one
+    scale for each row and group of 32, 64 or 128 columns."""
+    _want(w, torch.bfloat16, "w", 2)
+    N, K = w.shape
+    if group not in (32, 64, 128):
+        raise ValueError(f"group: expected 32, 64 or 128, got {group}")
+    codes = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
+    scales = torch.empty((N, K // group), dtype=torch.bfloat16, device=w.device)
+    _check(_lib.w8a8_w4_quantize(_ptr(w), N, K, group, _ptr(codes), _ptr(scales), _stream()), "w8a8_w4_quantize")
+    return codes, scales
+
+
+def w8a8_w4_pack(codes: torch.Tensor, scales: torch.Tensor):
+    """Row-major codes uint8 [N, K / 2] and scales bf16 [N, K / group] -> the packed layout that
+    w8a8_w4_linear reads: (flat uint8 codes, flat bf16 scales).  Once, at load time."""
+    _want(codes, torch.uint8, "codes", 2)
+    _want(scales, torch.bfloat16, "scales", 2)
+    N, K = codes.shape[0], 2 * codes.shape[1]
+    if scales.shape[0] != N or scales.shape[1] == 0 or K % scales.shape[1]:
+        raise ValueError("codes and scales disagree")
+    group = K // scales.shape[1]
+    cp = torch.empty((max(w4_code_bytes(N, K), 1),), dtype=torch.uint8, device=codes.device)
+    sp = torch.empty((max(w4_scale_bytes(N, K, group) // 2, 1),), dtype=torch.bfloat16, device=codes.device)
+    _check(_lib.w8a8_w4_pack(_ptr(codes), _ptr(scales), N, K, group, _ptr(cp), _ptr(sp), _stream()), "w8a8_w4_pack")
+    return cp, sp
+
+
+def w8a8_w4_linear(x, codes_packed, scales_packed, N: int, group: int, bias=None, out=None):
+    """y bf16 [M, N] = x bf16 [M, K] . w^T + bias with the 4-bit weight [N, K] in the packed layout
+    (w8a8_w4_pack)."""
+    _want(x, torch.bfloat16, "x", 2)
+    _want(codes_packed, torch.uint8, "codes_packed", 1)
+    _want(scales_packed, torch.bfloat16, "scales_packed", 1)
+    M, K = x.shape
+    if group not in (32, 64, 128):
+        raise ValueError(f"group: expected 32, 64 or 128, got {group}")
+    rows = -(-N // 16) * 16
+    if codes_packed.numel() < rows * (K // 2) or scales_packed.numel() < rows * (K // group):
+        raise ValueError("packed weight is smaller than [N, K] needs")
+    if bias is not None:
+        _want(bias, torch.bfloat16, "bias", 1)
+        if bias.shape[0] != N:
+            raise ValueError("bias length must equal N")
+    y = _out(out, torch.bfloat16, M * N, "out", x.device, shape=(M, N))
+    _check(_lib.w8a8_w4_linear(_ptr(x), _ptr(codes_packed), _ptr(scales_packed), _ptr(bias), _ptr(y), M, N, K, group,
+                               _stream()), "w8a8_w4_linear")
+    return y
+
+
+# --------------------------- few tokens: a paged 8-bit cache and attention ---
+class KVCache(NamedTuple):
+    """Pages of keys and values: codes int8 [pages, heads, page, dim], scales fp32 [pages, heads]."""
+    k_codes: torch.Tensor
+    v_codes: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def kv_cache(pages: int, heads: int, page: int, dim: int, device=None) -> KVCache:
+    """An empty cache of `pages` pages of `page` tokens (16, 32, 64 or 128) on the current device."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    codes = [torch.empty((pages, heads, page, dim), dtype=torch.int8, device=device) for _ in range(2)]
+    scales = [torch.empty((pages, heads), dtype=torch.float32, device=device) for _ in range(2)]
+    return KVCache(*codes, *scales)
+
+
+def _cache_args(cache: KVCache, table: torch.Tensor, lens: torch.Tensor):
+    """Checks a cache with its table and lengths: (pages, heads, page, dim, seqs, width)."""
+    _want(cache.k_codes, torch.int8, "cache.k_codes", 4)
+    _want(cache.v_codes, torch.int8, "cache.v_codes", 4)
+    _want(cache.k_scale, torch.float32, "cache.k_scale", 2)
+    _want(cache.v_scale, torch.float32, "cache.v_scale", 2)
+    _want(table, torch.int32, "table", 2)
+    _want(lens, torch.int32, "lens", 1)
+    shape = cache.k_codes.shape
+    if cache.v_codes.shape != shape or cache.k_scale.shape != shape[:2] or cache.v_scale.shape != shape[:2]:
+        raise ValueError("the cache's tensors disagree on pages, heads, page or dim")
+    if table.shape[0] != lens.shape[0]:
+        raise ValueError("table and lens disagree on the number of sequences")
+    pages, heads, page, dim = shape
+    return pages, heads, page, dim, table.shape[0], table.shape[1]
+
+
+def _token_rows(t: torch.Tensor, name: str, seqs: int, dim: int) -> int:
+    """Checks bf16 [seqs, tokens, heads, dim] whose tokens are rows a fixed distance apart, heads and
+    dim dense within a row (a slice of a wider projection is fine); returns that distance."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 4 or t.shape[0] != seqs or t.shape[3] != dim:
+        raise ValueError(f"{name}: expected [{seqs}, tokens, heads, {dim}], got {tuple(t.shape)}")
+    _device_ok(t, name)
+    tokens, heads = t.shape[1], t.shape[2]
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1 or (heads > 1 and s2 != dim):
+        raise ValueError(f"{name}: heads and dim must be dense within a token's row")
+    if tokens > 1:
+        if seqs > 1 and s0 != tokens * s1:
+            raise ValueError(f"{name}: tokens must be a fixed distance apart across sequences")
+        return s1
+    return s0 if seqs > 1 else heads * dim
+
+
+def w8a8_kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor) -> None:
+    """Writes new tokens k, v bf16 [seqs, tokens, heads, dim] into the cache, in place: they become positions
+    lens - tokens .. lens - 1 of their sequences (lens int32 [seqs] counts them), in the pages that
+    table int32 [seqs, width] names."""
+    pages, heads, page, dim, seqs, width = _cache_args(cache, table, lens)
+    ldk, ldv = _token_rows(k, "k", seqs, dim), _token_rows(v, "v", seqs, dim)
+    if k.shape != v.shape or k.shape[2] != heads:
+        raise ValueError("k, v and the cache disagree on tokens or heads")
+    _check(_lib.w8a8_kv_append(_ptr(k), ldk, _ptr(v), ldv, _ptr(cache.k_codes), _ptr(cache.k_scale), _ptr(cache.v_codes),
+                               _ptr(cache.v_scale), pages, _ptr(table), width, _ptr(lens), seqs, k.shape[1], heads, dim,
+                               page, _stream()), "w8a8_kv_append")
+
+
+def w8a8_kv_read(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, length: int, out=None):
+    """The sequences' first `length` positions as bf16 (k, v), each [seqs, length, heads, dim]; zeros from a
+    sequence's length on."""
+    pages, heads, page, dim, seqs, width = _cache_args(cache, table, lens)
+    k0, v0 = out if out is not None else (None, None)
+    shape = (seqs, length, heads, dim)
+    n = seqs * length * heads * dim
+    k = _out(k0, torch.bfloat16, n, "k", table.device, shape=shape)
+    v = _out(v0, torch.bfloat16, n, "v", table.device, shape=shape)
+    _check(_lib.w8a8_kv_read(_ptr(cache.k_codes), _ptr(cache.k_scale), _ptr(cache.v_codes), _ptr(cache.v_scale), pages,
+                             _ptr(table), width, _ptr(lens), seqs, length, heads, dim, page, _ptr(k), _ptr(v), _stream()),
+           "w8a8_kv_read")
+    return k, v
+
+
+def kv_attention_workspace_bytes(seqs: int, tokens: int, q_heads: int, heads: int, dim: int, page: int, width: int) -> int:
+    return int(_lib.w8a8_kv_attention_workspace_bytes(seqs, tokens, q_heads, heads, dim, page, width))
+
+
+def w8a8_kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor,
+                      scale: Optional[float] = None, workspace=None, out=None):
+    """y bf16 [seqs, tokens, q_heads, dim]: attention of each sequence's last `tokens` tokens, q bf16
+    [seqs, tokens, q_heads, dim], over what the cache holds of it, causal among themselves (append their keys
+    and values first).  scale defaults to dim^-0.5.  Queries that see no key give zeros."""
+    pages, heads, page, dim, seqs, width = _cache_args(cache, table, lens)
+    ldq = _token_rows(q, "q", seqs, dim)
+    tokens, q_heads = q.shape[1], q.shape[2]
+    need = kv_attention_workspace_bytes(seqs, tokens, q_heads, heads, dim, page, width)
+    ws = _workspace(workspace, need, q.device) if need or workspace is not None else None
+    y = _out(out, torch.bfloat16, seqs * tokens * q_heads * dim, "out", q.device, shape=(seqs, tokens, q_heads, dim))
+    _check(_lib.w8a8_kv_attention(_ptr(q), ldq, _ptr(cache.k_codes), _ptr(cache.k_scale), _ptr(cache.v_codes),
+                                  _ptr(cache.v_scale), pages, _ptr(table), width, _ptr(lens), seqs, tokens, q_heads, heads,
+                                  dim, page, dim ** -0.5 if scale is None else scale, _ptr(y), _ptr(ws),
+                                  0 if ws is None else ws.numel() * ws.element_size(), _stream()), "w8a8_kv_attention")
+    return y

@@ -14,8 +14,14 @@ constexpr int kMaxDevices = 64;
 // 0 = unknown, 1 = gfx950, 2 = other
 std::atomic<int> g_arch_ok[kMaxDevices];
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-size_t align256(size_t v) { return (v + 255u) & ~size_t(255u); }
+using w8a8::align256;
+using w8a8::aligned16;
+using w8a8::check_device;
+using w8a8::launched;
+
+}  // namespace
+
+namespace w8a8 {
 
 w8a8_status check_device() {
   int dev = -1;
@@ -37,7 +43,9 @@ w8a8_status check_device() {
   return state == 1 ? W8A8_OK : W8A8_ERR_UNSUPPORTED_DEVICE;
 }
 
-w8a8_status launched(hipError_t e) { return e == hipSuccess ? W8A8_OK : W8A8_ERR_LAUNCH; }
+}  // namespace w8a8
+
+namespace {
 
 // Shape rules shared by the GEMM entry points.
 w8a8_status check_gemm_shape(int64_t M, int64_t N, int64_t K) {

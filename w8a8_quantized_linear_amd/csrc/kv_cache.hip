@@ -1,0 +1,165 @@
+// A paged cache of keys and values in 8 bits: new tokens in, sequences back out.
+//
+// Layout.  A page holds `page` tokens of every head: int8 codes [pages][heads][page][dim] and one fp32 scale
+// for each page and head, for keys and for values.  Token p of a sequence is row p % page of the page that
+// the sequence's table names at p / page.
+//
+// What append computes, for each page and head that new tokens fall into: s = max(s_old, amax / 127), where
+// amax is the largest magnitude among the new values there and s_old is the page's scale if it holds tokens
+// of this sequence from before (0 if not); the codes held are moved to the new scale, c = RNE(c * (s_old / s)),
+// and the new ones are RNE(x / s), the library's per-token rule with the scale of a block.  All steps are
+// single fp32 operations, so the codes are the same on every run and machine.
+//
+// Bound: memory traffic (2 bytes read and 1 written per new value) and, for single tokens, latency.
+#include "epilogue_math.h"
+#include "internal.h"
+#include "quant_math.h"
+
+namespace w8a8 {
+namespace {
+
+using namespace qm;
+typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
+
+// The page of a sequence's block, or -1 where the table names none that exists.
+__device__ __forceinline__ int64_t page_of(const KvCache& c, int64_t seq, int64_t block) {
+  if (block >= c.width) return -1;
+  const int32_t id = c.table[seq * c.width + block];
+  return id >= 0 && id < c.pages ? id : -1;
+}
+
+// A sequence's length, and what of it its table row can address.
+__device__ __forceinline__ int64_t len_of(const KvCache& c, int64_t seq) { return max(c.lens[seq], 0); }
+__device__ __forceinline__ int64_t held_of(const KvCache& c, int64_t seq) { return min(len_of(c, seq), c.width * c.page); }
+
+// One workgroup per (sequence, touched block, head, keys or values): it alone reads and writes that block's
+// codes and scale.  A thread holds up to 8 pieces of 8 values.
+template <int DIM>
+__global__ void __launch_bounds__(256)
+kv_append_kernel(KvCache c, const uint16_t* __restrict__ k, int64_t ldk, const uint16_t* __restrict__ v, int64_t ldv,
+                 int64_t tokens, int64_t touched) {
+  constexpr int kPieces = 128 * DIM / 8 / 256;   // of the largest page
+  __shared__ float wave_max[4];
+  int64_t at = blockIdx.x;
+  const bool values = at & 1;
+  at >>= 1;
+  const int head = (int)(at % c.heads);
+  at /= c.heads;
+  const int64_t seq = at / touched, held = held_of(c, seq), first = len_of(c, seq) - tokens;
+  const int64_t block = max<int64_t>(first, 0) / c.page + at % touched, start = block * c.page;
+  if (start >= held) return;
+  const int64_t id = page_of(c, seq, block);
+  if (id < 0) return;
+  const uint16_t* src = (values ? v + seq * tokens * ldv : k + seq * tokens * ldk) + head * DIM;
+  const int64_t ld = values ? ldv : ldk;
+  const int64_t base = id * c.heads + head;
+  int8_t* dst = (values ? c.v_codes : c.k_codes) + base * c.page * DIM;
+  float* scale = (values ? c.v_scale : c.k_scale) + base;
+  const int rows = (int)min<int64_t>(c.page, held - start);         // rows of the block in use
+  const int old_rows = (int)min<int64_t>(max<int64_t>(first - start, 0), rows);   // from before
+
+  u32x4 raw[kPieces];
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int piece = i * 256 + threadIdx.x, row = piece / (DIM / 8);
+    raw[i] = u32x4{0, 0, 0, 0};
+    if (row >= old_rows && row < rows) {
+      raw[i] = *reinterpret_cast<const u32x4*>(src + (start + row - first) * ld + piece % (DIM / 8) * 8);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(bf16lo(raw[i][j])), fabsf(bf16hi(raw[i][j]))));
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) amax = fmaxf(amax, __shfl_xor(amax, d));
+  if ((threadIdx.x & 63) == 0) wave_max[threadIdx.x >> 6] = amax;
+  const float s_old = old_rows ? *scale : 0.0f;
+  __syncthreads();
+  amax = fmaxf(fmaxf(wave_max[0], wave_max[1]), fmaxf(wave_max[2], wave_max[3]));
+  const float s = fmaxf(s_old, amax / 127.0f);      // IEEE division
+  const QuotientScale qs = quotient_scale(s);
+  const bool grew = s > s_old && old_rows;
+  const float ratio = grew ? s_old / s : 1.0f;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int piece = i * 256 + threadIdx.x, row = piece / (DIM / 8);
+    if (row >= rows) continue;
+    u32x2_t* out = reinterpret_cast<u32x2_t*>(dst + piece * 8);
+    if (row >= old_rows) {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[2 * j] = bf16lo(raw[i][j]) * qs.pre;
+        x[2 * j + 1] = bf16hi(raw[i][j]) * qs.pre;
+      }
+      *out = u32x2_t{int8_codes4(x[0], x[1], x[2], x[3], qs.s, qs.r), int8_codes4(x[4], x[5], x[6], x[7], qs.s, qs.r)};
+    } else if (grew) {
+      u32x2_t w = *out;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t word = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float code = (float)(int8_t)(w[j] >> (8 * e));
+          word |= ((uint32_t)(int)rintf(code * ratio) & 0xffu) << (8 * e);
+        }
+        w[j] = word;
+      }
+      *out = w;
+    }
+  }
+  if (threadIdx.x == 0) *scale = s;                  // every thread has read s_old (barrier above)
+}
+
+// k, v [seqs][length][heads][dim] bf16: one thread per 8 values of both.
+template <int DIM>
+__global__ void __launch_bounds__(256)
+kv_read_kernel(KvCache c, int64_t length, int64_t pieces, uint16_t* __restrict__ k, uint16_t* __restrict__ v) {
+  const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (j >= pieces) return;
+  const int d = (int)(j % (DIM / 8)) * 8;
+  const int64_t row = j / (DIM / 8), head = row % c.heads, pos = row / c.heads % length, seq = row / c.heads / length;
+  const int64_t id = pos < held_of(c, seq) ? page_of(c, seq, pos / c.page) : -1;
+  u32x4 out[2] = {u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
+  if (id >= 0) {
+    const int64_t base = id * c.heads + head, code = (base * c.page + pos % c.page) * DIM + d;
+    const u32x2_t w[2] = {*reinterpret_cast<const u32x2_t*>(c.k_codes + code), *reinterpret_cast<const u32x2_t*>(c.v_codes + code)};
+    const float s[2] = {c.k_scale[base], c.v_scale[base]};
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t b = w[t][i / 2] >> (16 * (i % 2));
+        out[t][i] = bf16x2_rne((float)(int8_t)b * s[t], (float)(int8_t)(b >> 8) * s[t]);
+      }
+  }
+  *reinterpret_cast<u32x4*>(k + j * 8) = out[0];
+  *reinterpret_cast<u32x4*>(v + j * 8) = out[1];
+}
+
+}  // namespace
+
+hipError_t launch_kv_append(const KvCache& c, const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                            int64_t seqs, int64_t tokens, hipStream_t stream) {
+  const int64_t touched = (tokens + c.page - 2) / c.page + 1;
+  const int64_t blocks = seqs * touched * c.heads * 2;
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  if (c.dim == 64)
+    hipLaunchKernelGGL((kv_append_kernel<64>), dim3((unsigned)blocks), dim3(256), 0, stream, c, k, ldk, v, ldv, tokens, touched);
+  else
+    hipLaunchKernelGGL((kv_append_kernel<128>), dim3((unsigned)blocks), dim3(256), 0, stream, c, k, ldk, v, ldv, tokens, touched);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_read(const KvCache& c, int64_t seqs, int64_t length, uint16_t* k, uint16_t* v,
+                          hipStream_t stream) {
+  const int64_t pieces = seqs * length * c.heads * (c.dim / 8), blocks = (pieces + 255) / 256;
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  if (c.dim == 64)
+    hipLaunchKernelGGL((kv_read_kernel<64>), dim3((unsigned)blocks), dim3(256), 0, stream, c, length, pieces, k, v);
+  else
+    hipLaunchKernelGGL((kv_read_kernel<128>), dim3((unsigned)blocks), dim3(256), 0, stream, c, length, pieces, k, v);
+  return hipGetLastError();
+}
+
+}  // namespace w8a8
