@@ -35,12 +35,13 @@ __all__ = [
 ]
 
 LIB_PATH = Path(__file__).resolve().parent / "libw8a8.so"
-if not LIB_PATH.exists():
+if not LIB_PATH.exists() or not LIB_PATH.with_name("_binding.so").exists():
     raise ImportError(
-        f"{LIB_PATH} is not built; run `python w8a8_quantized_linear_amd/build.py` "
+        f"{LIB_PATH} or _binding.so beside it is not built; run `python w8a8_quantized_linear_amd/build.py` "
         "(hipcc, gfx950) first -- there is no non-HIP fallback")
 
 _lib = ctypes.CDLL(str(LIB_PATH))
+from . import _binding  # noqa: E402  (the calls for few tokens, which cost less than ctypes' marshalling)
 _P, _I64, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 _F = ctypes.c_float
 _SIGS = {
@@ -103,6 +104,11 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream():
     return torch.cuda.current_stream().cuda_stream
+
+
+# torch's current device and its current stream as plain numbers: what torch.cuda.current_device() and
+# current_stream().cuda_stream give, without building a Stream object for each call
+_raw_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _device_ok(t: torch.Tensor, name: str) -> None:
@@ -524,23 +530,8 @@ def w8a8_w4_pack(codes: torch.Tensor, scales: torch.Tensor):
 def w8a8_w4_linear(x, codes_packed, scales_packed, N: int, group: int, bias=None, out=None):
     """y bf16 [M, N] = x bf16 [M, K] . w^T + bias with the 4-bit weight [N, K] in the packed layout
     (w8a8_w4_pack)."""
-    _want(x, torch.bfloat16, "x", 2)
-    _want(codes_packed, torch.uint8, "codes_packed", 1)
-    _want(scales_packed, torch.bfloat16, "scales_packed", 1)
-    M, K = x.shape
-    if group not in (32, 64, 128):
-        raise ValueError(f"group: expected 32, 64 or 128, got {group}")
-    rows = -(-N // 16) * 16
-    if codes_packed.numel() < rows * (K // 2) or scales_packed.numel() < rows * (K // group):
-        raise ValueError("packed weight is smaller than [N, K] needs")
-    if bias is not None:
-        _want(bias, torch.bfloat16, "bias", 1)
-        if bias.shape[0] != N:
-            raise ValueError("bias length must equal N")
-    y = _out(out, torch.bfloat16, M * N, "out", x.device, shape=(M, N))
-    _check(_lib.w8a8_w4_linear(_ptr(x), _ptr(codes_packed), _ptr(scales_packed), _ptr(bias), _ptr(y), M, N, K, group,
-                               _stream()), "w8a8_w4_linear")
-    return y
+    y = _binding.w4_linear(x, codes_packed, scales_packed, N, group, bias, out, _raw_stream(_raw_device()))
+    return y if type(y) is not int else _check(y, "w8a8_w4_linear")
 
 
 # --------------------------- few tokens: a paged 8-bit cache and attention ---
@@ -560,70 +551,19 @@ def kv_cache(pages: int, heads: int, page: int, dim: int, device=None) -> KVCach
     return KVCache(*codes, *scales)
 
 
-def _cache_args(cache: KVCache, table: torch.Tensor, lens: torch.Tensor):
-    """Checks a cache with its table and lengths: (pages, heads, page, dim, seqs, width)."""
-    _want(cache.k_codes, torch.int8, "cache.k_codes", 4)
-    _want(cache.v_codes, torch.int8, "cache.v_codes", 4)
-    _want(cache.k_scale, torch.float32, "cache.k_scale", 2)
-    _want(cache.v_scale, torch.float32, "cache.v_scale", 2)
-    _want(table, torch.int32, "table", 2)
-    _want(lens, torch.int32, "lens", 1)
-    shape = cache.k_codes.shape
-    if cache.v_codes.shape != shape or cache.k_scale.shape != shape[:2] or cache.v_scale.shape != shape[:2]:
-        raise ValueError("the cache's tensors disagree on pages, heads, page or dim")
-    if table.shape[0] != lens.shape[0]:
-        raise ValueError("table and lens disagree on the number of sequences")
-    pages, heads, page, dim = shape
-    return pages, heads, page, dim, table.shape[0], table.shape[1]
-
-
-def _token_rows(t: torch.Tensor, name: str, seqs: int, dim: int) -> int:
-    """Checks bf16 [seqs, tokens, heads, dim] whose tokens are rows a fixed distance apart, heads and
-    dim dense within a row (a slice of a wider projection is fine); returns that distance."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 4 or t.shape[0] != seqs or t.shape[3] != dim:
-        raise ValueError(f"{name}: expected [{seqs}, tokens, heads, {dim}], got {tuple(t.shape)}")
-    _device_ok(t, name)
-    tokens, heads = t.shape[1], t.shape[2]
-    s0, s1, s2, s3 = t.stride()
-    if s3 != 1 or (heads > 1 and s2 != dim):
-        raise ValueError(f"{name}: heads and dim must be dense within a token's row")
-    if tokens > 1:
-        if seqs > 1 and s0 != tokens * s1:
-            raise ValueError(f"{name}: tokens must be a fixed distance apart across sequences")
-        return s1
-    return s0 if seqs > 1 else heads * dim
-
-
 def w8a8_kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor) -> None:
-    """Writes new tokens k, v bf16 [seqs, tokens, heads, dim] into the cache, in place: they become positions
-    lens - tokens .. lens - 1 of their sequences (lens int32 [seqs] counts them), in the pages that
-    table int32 [seqs, width] names."""
-    pages, heads, page, dim, seqs, width = _cache_args(cache, table, lens)
-    ldk, ldv = _token_rows(k, "k", seqs, dim), _token_rows(v, "v", seqs, dim)
-    if k.shape != v.shape or k.shape[2] != heads:
-        raise ValueError("k, v and the cache disagree on tokens or heads")
-    _check(_lib.w8a8_kv_append(_ptr(k), ldk, _ptr(v), ldv, _ptr(cache.k_codes), _ptr(cache.k_scale), _ptr(cache.v_codes),
-                               _ptr(cache.v_scale), pages, _ptr(table), width, _ptr(lens), seqs, k.shape[1], heads, dim,
-                               page, _stream()), "w8a8_kv_append")
+    """Writes new tokens k, v bf16 [seqs, tokens, heads, dim] (dense rows a fixed distance apart: slices of a wider
+    projection are fine) into the cache, in place: they become positions lens - tokens .. lens - 1 of their sequences
+    (lens int32 [seqs] counts them), in the pages that table int32 [seqs, width] names."""
+    _check(_binding.kv_append(k, v, cache, table, lens, _raw_stream(_raw_device())), "w8a8_kv_append")
 
 
 def w8a8_kv_read(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, length: int, out=None):
     """The sequences' first `length` positions as bf16 (k, v), each [seqs, length, heads, dim]; zeros from a
     sequence's length on."""
-    pages, heads, page, dim, seqs, width = _cache_args(cache, table, lens)
-    k0, v0 = out if out is not None else (None, None)
-    shape = (seqs, length, heads, dim)
-    n = seqs * length * heads * dim
-    k = _out(k0, torch.bfloat16, n, "k", table.device, shape=shape)
-    v = _out(v0, torch.bfloat16, n, "v", table.device, shape=shape)
-    _check(_lib.w8a8_kv_read(_ptr(cache.k_codes), _ptr(cache.k_scale), _ptr(cache.v_codes), _ptr(cache.v_scale), pages,
-                             _ptr(table), width, _ptr(lens), seqs, length, heads, dim, page, _ptr(k), _ptr(v), _stream()),
-           "w8a8_kv_read")
-    return k, v
+    k, v = out if out is not None else (None, None)
+    kv = _binding.kv_read(cache, table, lens, length, k, v, _raw_stream(_raw_device()))
+    return kv if type(kv) is not int else _check(kv, "w8a8_kv_read")
 
 
 def kv_attention_workspace_bytes(seqs: int, tokens: int, q_heads: int, heads: int, dim: int, page: int, width: int) -> int:
@@ -635,14 +575,5 @@ def w8a8_kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens
     """y bf16 [seqs, tokens, q_heads, dim]: attention of each sequence's last `tokens` tokens, q bf16
     [seqs, tokens, q_heads, dim], over what the cache holds of it, causal among themselves (append their keys
     and values first).  scale defaults to dim^-0.5.  Queries that see no key give zeros."""
-    pages, heads, page, dim, seqs, width = _cache_args(cache, table, lens)
-    ldq = _token_rows(q, "q", seqs, dim)
-    tokens, q_heads = q.shape[1], q.shape[2]
-    need = kv_attention_workspace_bytes(seqs, tokens, q_heads, heads, dim, page, width)
-    ws = _workspace(workspace, need, q.device) if need or workspace is not None else None
-    y = _out(out, torch.bfloat16, seqs * tokens * q_heads * dim, "out", q.device, shape=(seqs, tokens, q_heads, dim))
-    _check(_lib.w8a8_kv_attention(_ptr(q), ldq, _ptr(cache.k_codes), _ptr(cache.k_scale), _ptr(cache.v_codes),
-                                  _ptr(cache.v_scale), pages, _ptr(table), width, _ptr(lens), seqs, tokens, q_heads, heads,
-                                  dim, page, dim ** -0.5 if scale is None else scale, _ptr(y), _ptr(ws),
-                                  0 if ws is None else ws.numel() * ws.element_size(), _stream()), "w8a8_kv_attention")
-    return y
+    y = _binding.kv_attention(q, cache, table, lens, scale, workspace, out, _raw_stream(_raw_device()))
+    return y if type(y) is not int else _check(y, "w8a8_kv_attention")

@@ -1,4 +1,5 @@
-"""Build ``libw8a8.so`` (the C-ABI library) for gfx950 with hipcc, in-tree.
+"""Build ``libw8a8.so`` (the C-ABI library) for gfx950 with hipcc, and the compiled
+part of its Python binding with the host compiler, in-tree.
 
     python w8a8_quantized_linear_amd/build.py
 
@@ -20,9 +21,11 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 LIB = PKG / "libw8a8.so"
+BINDING = PKG / "_binding.so"      # the compiled part of the Python binding (needs torch's headers)
 BUILD_DIR = PKG / "_build"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CXX = os.environ.get("CXX", "g++")
 ARCH = "gfx950"
 SOURCES = ["quantize.hip", "gemm.hip", "swiglu.hip", "short.hip", "scratch.hip", "api.cpp",
            "w4.hip", "kv_cache.hip", "attention.hip", "decode_api.cpp"]
@@ -76,13 +79,41 @@ def _link(objs, out: Path) -> Path:
     return out
 
 
+def _compile_binding() -> Path:
+    import sysconfig
+    from torch.utils.cpp_extension import include_paths
+    obj = BUILD_DIR / "binding.o"
+    obj.unlink(missing_ok=True)
+    includes = [*include_paths(), "/opt/rocm/include", sysconfig.get_paths()["include"], str(INCLUDE)]
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-Wall", "-DUSE_ROCM", "-D__HIP_PLATFORM_AMD__",
+           *(f"-isystem{i}" for i in includes[:-1]), f"-I{INCLUDE}", "-c", str(CSRC / "binding.cpp"), "-o", str(obj)]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{CXX} failed for binding.cpp:\n{res.stderr}")
+    return obj
+
+
+def _link_binding(obj: Path) -> None:
+    from torch.utils.cpp_extension import TORCH_LIB_PATH
+    tmp = BINDING.with_suffix(".so.tmp")
+    cmd = [CXX, "-shared", str(obj), f"-L{PKG}", "-l:libw8a8.so", f"-L{TORCH_LIB_PATH}", "-lc10", "-lc10_hip", "-ltorch_cpu",
+           "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{TORCH_LIB_PATH}", "-o", str(tmp)]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"link failed:\n{res.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build() -> Path:
-    """Build libw8a8.so (the library) and probe/libw8a8_probe.so (measurement aids)."""
+    """Build libw8a8.so (the library), _binding.so (the compiled part of its Python binding) and
+    probe/libw8a8_probe.so (measurement aids)."""
     BUILD_DIR.mkdir(exist_ok=True)
     jobs = [(src, CSRC, "") for src in SOURCES] + [(src, PROBE_DIR, "probe_") for src in PROBE_SOURCES]
-    with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
+    with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(lambda j: _compile(*j), jobs))
     _link(objs[:len(SOURCES)], LIB)
+    _link_binding(binding.result())
     _link(objs[len(SOURCES):], PROBE_LIB)
     return LIB
 
