@@ -28,7 +28,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CXX = os.environ.get("CXX", "g++")
 ARCH = "gfx950"
 SOURCES = ["quantize.hip", "gemm.hip", "swiglu.hip", "short.hip", "scratch.hip", "api.cpp",
-           "w4.hip", "kv_cache.hip", "attention.hip", "decode_api.cpp"]
+           "w4.hip", "kv_cache.hip", "attention.hip", "attention_prompt.hip", "decode_api.cpp"]
 # Per-source flags.  The quantizer's fp64 matrix instructions (the rotation's
 # cross-quarter transform) take the VGPR form: their results feed vector
 # instructions, and results in accumulation registers would cost two copies per

@@ -12,31 +12,20 @@
 // Maximum, sum and output are fp32.
 #include <algorithm>
 
-#include "epilogue_math.h"
-#include "internal.h"
+#include "attention_math.h"
 
 namespace w8a8 {
 namespace {
 
-typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+using namespace kva;
 
 constexpr int kWaves = 4;
 constexpr int kTile = 32;                       // tokens of a wave's step: two MFMA tiles of 16
 constexpr int kSegment = 2048;                  // tokens whose page entries are in LDS at once
 constexpr int kEntries = kSegment / 16;         // pages of a segment at the smallest page
 constexpr int kStep = kWaves * kTile;           // pieces of a sequence are whole steps of a workgroup
-
-// Tokens of each of the `splits` pieces of a sequence.
-__device__ __forceinline__ int piece_of(int held, int splits) {
-  return ((held + splits - 1) / splits + kStep - 1) / kStep * kStep;
-}
-
+static_assert(kPiece % kStep == 0, "pieces are whole steps");
 constexpr int kProbExp = 14;                    // probabilities are rounded below 2^14 (f16 ends at 2^16)
-
 
 // The largest of the four lanes l, l ^ 16, l ^ 32, l ^ 48.
 __device__ __forceinline__ float max_quarters(float v) {
@@ -48,26 +37,9 @@ __device__ __forceinline__ float sum_quarters(float v) {
   return v + __shfl_xor(v, 32);
 }
 
-// Two bytes holding code + 128 in the low bytes of 16-bit halves -> two f16 codes: with 0x64 above it a byte u
-// is the f16 1024 + u, and 1152 less is the code, exactly.
-__device__ __forceinline__ uint32_t f16_codes(uint32_t halves) {
-  const f16x2 v = __builtin_bit_cast(f16x2, halves | 0x64006400u) - f16x2{(_Float16)1152.0f, (_Float16)1152.0f};
-  return __builtin_bit_cast(uint32_t, v);
-}
-
-__device__ __forceinline__ uint32_t f16_pair(float a, float b) {
-  return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
-}
-
 struct Entry {
   int32_t id;        // page, -1: none
   float k, v;        // its scales
-};
-
-// Partial results of a row's pieces: unnormalised outputs [DIM], then maximum and sum.
-struct Partial {
-  float* out;
-  float* stat;
 };
 
 // One workgroup: 16 * NB query rows (tokens x the heads that share a cache head) against one piece of a
@@ -118,7 +90,7 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
         for (int j = 0; j < 4; ++j) top = max(top, max((raw[cc][u][j] << 16) & 0x7fffffffu, raw[cc][u][j] & 0x7fff0000u));
       }
     top = __float_as_uint(max_quarters(__uint_as_float(top)));
-    const int up = min(134 - (int)(top >> 23), 126);      // the row's largest value lands in [2^7, 2^8)
+    const int up = query_exp(top);
     const float by = ldexpf(1.0f, up);
     qs[n] = ldexpf(scale * 1.44269504088896341f, -up);
 #pragma unroll
@@ -161,7 +133,7 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
     v_top = fmaxf(v_top, __shfl_xor(v_top, 4));
     v_top = fmaxf(v_top, __shfl_xor(v_top, 8));
     v_top = max_quarters(v_top);
-    const int seg_exp = max((int)(__float_as_uint(v_top) >> 23) - 126, -112);   // v_top < 2^seg_exp; 2^(14 + 112) is finite
+    const int seg_exp = scale_exp(v_top);
     if (seg_exp > v_exp) {
 #pragma unroll
       for (int n = 0; n < NB; ++n)
@@ -202,9 +174,9 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
             u32x4 a;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const uint32_t word = kraw[u][cc][2 * half + j] ^ 0x80808080u;
-              a[2 * j] = f16_codes(__builtin_amdgcn_perm(0, word, 0x0c010c00u));
-              a[2 * j + 1] = f16_codes(__builtin_amdgcn_perm(0, word, 0x0c030c02u));
+              uint32_t two[2];
+              f16_word(kraw[u][cc][2 * half + j], two);
+              a[2 * j] = two[0], a[2 * j + 1] = two[1];
             }
 #pragma unroll
             for (int n = 0; n < NB; ++n)
@@ -354,7 +326,9 @@ kv_combine_kernel(int rows, int heads, int group, int splits, uint16_t* __restri
   *reinterpret_cast<u32x2*>(dst) = u32x2{bf16x2_rne(o[0] * inv, o[1] * inv), bf16x2_rne(o[2] * inv, o[3] * inv)};
 }
 
+// Blocks of 16 rows of a workgroup; rows past 64 take the prompt form.
 int blocks_of(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+bool prompt_rows(int64_t rows) { return rows > 64; }
 
 template <int DIM, int NB>
 hipError_t launch(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs, int64_t tokens, int group, float scale,
@@ -364,31 +338,43 @@ hipError_t launch(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
   hipLaunchKernelGGL((kv_attention_kernel<DIM, NB>), dim3((unsigned)blocks), dim3(256), 0, stream, c, q, ldq, (int)tokens, group,
                      scale, (int)splits, (int)tiles, y, part);
-  hipError_t e = hipGetLastError();
+  return hipGetLastError();
+}
+
+template <int DIM>
+hipError_t launch_all(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs, int64_t tokens, int group, float scale,
+                      int64_t splits, uint16_t* y, Partial part, hipStream_t stream) {
+  const int64_t rows = tokens * group, all = seqs * c.heads * rows;
+  hipError_t e;
+  if (prompt_rows(rows)) e = launch_prompt<DIM>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
+  else if (blocks_of(rows) == 1) e = launch<DIM, 1>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
+  else if (blocks_of(rows) == 2) e = launch<DIM, 2>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
+  else e = launch<DIM, 4>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
   if (e != hipSuccess || splits == 1) return e;
-  const int64_t all = seqs * c.heads * rows;
   hipLaunchKernelGGL((kv_combine_kernel<DIM>), dim3((unsigned)all), dim3(256), 0, stream, (int)rows, c.heads, group, (int)splits,
                      y, part);
   return hipGetLastError();
 }
 
-template <int DIM>
-hipError_t launch_rows(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs, int64_t tokens, int group, float scale,
-                       int64_t splits, uint16_t* y, Partial part, hipStream_t stream) {
-  switch (blocks_of(tokens * group)) {
-    case 1: return launch<DIM, 1>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
-    case 2: return launch<DIM, 2>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
-    default: return launch<DIM, 4>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
-  }
-}
-
 }  // namespace
 
-// Workgroups enough for two or more on each of the 256 CUs, but no piece of a full table below one step.
 int64_t kv_attention_splits(int64_t seqs, int64_t tokens, int q_heads, int heads, int page, int64_t width) {
-  const int64_t rows = tokens * (q_heads / heads), tile = 16 * blocks_of(rows);
-  const int64_t one = seqs * heads * ((rows + tile - 1) / tile);
-  const int64_t most = (width * page + kStep - 1) / kStep;
+  const int64_t rows = tokens * (q_heads / heads);
+  const int64_t most = (width * page + kPiece - 1) / kPiece;
+  if (prompt_rows(rows)) {
+    // one workgroup fits a CU: the cut that leaves the fewest rounds of 256, a piece more costing a twentieth
+    // (its partial results pass through memory)
+    const int64_t one = seqs * heads * ((rows + kPromptRows - 1) / kPromptRows);
+    int64_t best = 1;
+    double least = 0.0;
+    for (int64_t s = 1; s <= std::min<int64_t>(8, most); ++s) {
+      const double cost = (double)((one * s + 255) / 256) / (double)s * (1.0 + 0.05 * (double)(s - 1));
+      if (s == 1 || cost < least) best = s, least = cost;
+    }
+    return best;
+  }
+  // workgroups enough for four on each of the 256 CUs, but no piece of a full table below one step
+  const int64_t tile = 16 * blocks_of(rows), one = seqs * heads * ((rows + tile - 1) / tile);
   return std::max<int64_t>(1, std::min<int64_t>((1024 + one - 1) / one, most));
 }
 
@@ -401,8 +387,8 @@ hipError_t launch_kv_attention(const KvCache& c, const uint16_t* q, int64_t ldq,
     part.stat = part.out + seqs * tokens * q_heads * splits * c.dim;
   }
   const int group = q_heads / c.heads;
-  return c.dim == 64 ? launch_rows<64>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream)
-                     : launch_rows<128>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
+  return c.dim == 64 ? launch_all<64>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream)
+                     : launch_all<128>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
 }
 
 }  // namespace w8a8

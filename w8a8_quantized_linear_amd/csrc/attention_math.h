@@ -1,0 +1,62 @@
+// What the two forms of attention over the paged 8-bit cache share: types, the codes' conversion, the cut of a
+// sequence into pieces, and where the pieces leave their partial results.
+#pragma once
+
+#include "epilogue_math.h"
+#include "internal.h"
+
+namespace w8a8 {
+namespace kva {
+
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kPiece = 128;                     // pieces of a sequence are whole multiples of this
+
+// Tokens of each of the `splits` pieces of a sequence.
+__host__ __device__ __forceinline__ int piece_of(int held, int splits) {
+  return ((held + splits - 1) / splits + kPiece - 1) / kPiece * kPiece;
+}
+
+// Two bytes holding code + 128 in the low bytes of 16-bit halves -> two f16 codes: with 0x64 above it a byte u
+// is the f16 1024 + u, and 1152 less is the code, exactly.
+__device__ __forceinline__ uint32_t f16_codes(uint32_t halves) {
+  const f16x2 v = __builtin_bit_cast(f16x2, halves | 0x64006400u) - f16x2{(_Float16)1152.0f, (_Float16)1152.0f};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+__device__ __forceinline__ uint32_t f16_pair(float a, float b) {
+  return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+}
+
+// Four codes in memory order -> f16, two per word.
+__device__ __forceinline__ void f16_word(uint32_t word, uint32_t* two) {
+  word ^= 0x80808080u;
+  two[0] = f16_codes(__builtin_amdgcn_perm(0, word, 0x0c010c00u));
+  two[1] = f16_codes(__builtin_amdgcn_perm(0, word, 0x0c030c02u));
+}
+
+// The power of two that brings a row of queries whose largest magnitude has these bits into [2^7, 2^8).
+__device__ __forceinline__ int query_exp(uint32_t top_bits) { return min(134 - (int)(top_bits >> 23), 126); }
+
+// The least e (at least -112) with s < 2^e, for a scale s >= 0.
+__device__ __forceinline__ int scale_exp(float s) { return max((int)(__float_as_uint(s) >> 23) - 126, -112); }
+
+// Partial results of a row's pieces, for each row and piece: unnormalised outputs [dim], and maximum and sum.
+struct Partial {
+  float* out;
+  float* stat;
+};
+
+// Prompt form (attention_prompt.hip): 256 query rows a workgroup.
+constexpr int kPromptRows = 256;
+template <int DIM>
+hipError_t launch_prompt(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs, int64_t tokens, int group,
+                         float scale, int64_t splits, uint16_t* y, Partial part, hipStream_t stream);
+
+}  // namespace kva
+}  // namespace w8a8

@@ -1,0 +1,320 @@
+// Attention over the paged 8-bit cache for many query rows: prompts and pieces of prompts.
+//
+// The mathematics is that of attention.hip.  Here the products bound the time, not the cache's bytes, so a
+// workgroup turns each 64 tokens of codes into f16 once, in LDS, for 256 query rows (8 waves of 32): keys
+// [token][dim], values transposed [dim][token].  Per wave and tile the matrix core needs 1,024 cycles
+// (dim 128), the softmax of 64 x 32 scores about 900 vector cycles, the conversions 200, and the operands'
+// reads from LDS a quarter of the CU's 1,024: two waves on each SIMD overlap one's products with the other's
+// softmax.
+//   S^T = K Q^T  (MFMA 32x32x16 f16): lane 32 h + r holds row r, tokens 8 (i / 4) + 4 h + i % 4 of a 32-token
+//   block in register i, which is the second operand of O^T += V^T P^T as it stands, if the tokens of a
+//   16-token step are taken in the order 4 h + j, 8 + 4 h + j (j < 4) for each half h: the order in which
+//   the values are written to LDS.
+// The values' scale goes into the exponent, p' = 2^(s - max + log2(scale) - e), so it costs nothing per element;
+// the sum of p' over a page is divided by the scale again.  A page whose values have scale zero (or subnormal: taken
+// for zero) counts as one of scale 2^(e-1) with codes of zero.  The running maximum moves only when a row's score passes it by more than
+// 2^8 (the probabilities stay below 2^15), which spares most tiles the rescaling of the outputs.
+#include "attention_math.h"
+
+namespace w8a8 {
+namespace kva {
+namespace {
+
+constexpr int kTile = 64;                       // tokens
+constexpr int kSubs = kTile / 16;               // 16-token runs: no page boundary falls inside one
+constexpr int kWaves = kPromptRows / 32;
+constexpr int kThreads = 64 * kWaves;
+constexpr float kLazy = 8.0f;                   // log2 of how far scores may pass the running maximum
+constexpr int kProbExp = 7;                     // p' < 2^(kLazy + kProbExp), f16 ends at 2^16
+
+struct Run {
+  float k;           // the keys' scale
+  float v;           // the values' scale, 0 where they are all zeros, -1 where the table names no page
+  float v_log;       // log2 of it
+  float v_inv;       // 1 / it
+};
+
+// The larger of lanes l and l ^ 32.
+__device__ __forceinline__ float max_halves(float v) { return fmaxf(v, __shfl_xor(v, 32)); }
+
+template <int DIM>
+__global__ void __launch_bounds__(kThreads)
+kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tokens, int group, float scale, int splits,
+                 int row_tiles, int total, uint16_t* __restrict__ y, Partial part) {
+  constexpr int KS = DIM / 16;                  // MFMA steps of a key
+  constexpr int DB = DIM / 32;                  // output blocks
+  constexpr int KCH = DIM / 8;                  // 16-byte chunks of an f16 key row
+  constexpr int KP = kTile * DIM / 16 / 256;    // 16-byte pieces of codes per thread of the keys' half
+  __shared__ __attribute__((aligned(16))) u32x4 k_lds[2][kTile * KCH];
+  __shared__ __attribute__((aligned(16))) u32x4 v_lds[2][DIM * (kTile / 8)];
+  __shared__ Run runs[2][kSubs];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int h = lane >> 5, r = lane & 31;
+  // consecutive items to one XCD (workgroups go round the 8 XCDs), so that those of one sequence and head share an L2
+  const int xcd = blockIdx.x % 8, slot = blockIdx.x / 8;
+  int at = xcd * (total / 8) + min(xcd, total % 8) + slot;
+  const int split = at % splits;
+  at /= splits;
+  const int tile = row_tiles - 1 - at % row_tiles;          // the longest first
+  at /= row_tiles;
+  const int head = at % c.heads, page_log = __builtin_ctz(c.page);
+  const int64_t seq = at / c.heads;
+  const int rows = tokens * group, row0 = tile * kPromptRows + 32 * wave;
+  const int len = max(c.lens[seq], 0), held = min(len, (int)c.width << page_log), piece = piece_of(held, splits);
+  const int first_pos = len - tokens;
+  const int tile_last = min((tile + 1) * kPromptRows, rows) - 1;
+  const int begin = min(split * piece, held), end = min(min(begin + piece, held), first_pos + tile_last / group + 1);
+  const int row = min(row0 + r, rows - 1), last_key = first_pos + row / group;
+  // this wave's keys: none if it has no rows; every row sees those before `all_seen`
+  const int wave_end = row0 < rows ? min(end, first_pos + min(row0 + 31, rows - 1) / group + 1) : 0;
+  const int all_seen = min(end, first_pos + row0 / group + 1);
+
+  // ---- queries ----
+  u32x4 qf[KS];
+  float qs;
+  {
+    const uint16_t* src = q + (seq * tokens + row / group) * ldq + (head * group + row % group) * DIM + 8 * h;
+    uint32_t top = 0;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      qf[s] = *reinterpret_cast<const u32x4*>(src + 16 * s);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = max(top, max((qf[s][j] << 16) & 0x7fffffffu, qf[s][j] & 0x7fff0000u));
+    }
+    top = __float_as_uint(max_halves(__uint_as_float(top)));
+    const int up = query_exp(top);
+    const float by = ldexpf(scale < 0.0f ? -1.0f : 1.0f, up);      // scores are scaled by what is not negative
+    qs = ldexpf(fabsf(scale) * 1.44269504088896341f, -up);
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        qf[s][j] = f16_pair(__uint_as_float(qf[s][j] << 16) * by, __uint_as_float(qf[s][j] & 0xffff0000u) * by);
+  }
+
+  // ---- staging: waves 0 .. 3 the values, 4 .. 7 the keys ----
+  const bool keys = wave >= 4;
+  const int st = tid & 255;
+  const int v_quad = st % (DIM / 4), v_half = st / (DIM / 4) % 2, v_sub = st / (DIM / 2);      // v_sub >= kSubs: none
+  const int64_t head_base = (int64_t)head * c.page * DIM;
+  const int64_t page_bytes = (int64_t)c.heads * c.page * DIM;
+  const int32_t* table = c.table + seq * c.width;
+  int32_t ids[2];                               // pages of the next tile's runs that this thread stages
+  u32x4 raw[2];                                 // its codes
+  float run_scale[2];
+  // the run of 16 tokens behind piece i of this thread
+  auto sub_of = [&](int i) { return keys ? (i * 256 + st) / (DIM / 16) / 16 : min(v_sub, kSubs - 1); };
+  auto load_ids = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < KP; ++i) ids[i] = table[min((t0 + 16 * sub_of(i)) >> page_log, (int)c.width - 1)];
+  };
+  auto load_codes = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < KP; ++i) {
+      const int t = t0 + 16 * sub_of(i);
+      const bool real = ids[i] >= 0 && ids[i] < c.pages && t < end;
+      const int64_t id = real ? ids[i] : 0;
+      const int64_t base = id * page_bytes + head_base + (int64_t)(t & (c.page - 1)) * DIM;
+      if (keys) {
+        const int p = i * 256 + st;
+        raw[i] = *reinterpret_cast<const u32x4*>(c.k_codes + base + (p / (DIM / 16) % 16) * DIM + p % (DIM / 16) * 16);
+        run_scale[i] = real ? c.k_scale[id * c.heads + head] : 0.0f;
+      } else if (i == 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          raw[j / 4][j % 4] = *reinterpret_cast<const uint32_t*>(c.v_codes + base + (4 * v_half + j % 4 + 8 * (j / 4)) * DIM + 4 * v_quad);
+        run_scale[0] = real ? c.v_scale[id * c.heads + head] : -1.0f;
+      }
+    }
+  };
+  auto store = [&](int buf) {
+    if (keys) {
+#pragma unroll
+      for (int i = 0; i < KP; ++i) {
+        const int p = i * 256 + st, t = p / (DIM / 16), ch = 2 * (p % (DIM / 16));
+        u32x4 lo, hi;
+        uint32_t two[2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f16_word(raw[i][j], two);
+          if (j < 2) lo[2 * j] = two[0], lo[2 * j + 1] = two[1];
+          else hi[2 * j - 4] = two[0], hi[2 * j - 3] = two[1];
+        }
+        k_lds[buf][t * KCH + (ch ^ (t & (KCH - 1)))] = lo;
+        k_lds[buf][t * KCH + ((ch + 1) ^ (t & (KCH - 1)))] = hi;
+        if (p % (DIM / 16) == 0 && t % 16 == 0) runs[buf][t / 16].k = run_scale[i];
+      }
+    } else if (v_sub < kSubs) {
+      const int ch = 2 * v_sub + v_half;
+      const bool zeros = !(run_scale[0] >= 0x1p-126f);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const uint32_t pick = 0x0c000c00u | (4 + b) << 16 | b;
+        u32x4 a;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          a[j] = f16_codes(__builtin_amdgcn_perm(raw[j / 2][2 * (j % 2) + 1] ^ 0x80808080u, raw[j / 2][2 * (j % 2)] ^ 0x80808080u, pick));
+        const int d = 4 * v_quad + b;
+        v_lds[buf][d * (kTile / 8) + (ch ^ ((d ^ (d >> 2)) & 7))] = zeros ? u32x4{0, 0, 0, 0} : a;
+      }
+      if (v_quad == 0 && v_half == 0) {
+        runs[buf][v_sub].v = zeros && run_scale[0] != -1.0f ? 0.0f : run_scale[0];
+        runs[buf][v_sub].v_log = __log2f(run_scale[0]);
+        runs[buf][v_sub].v_inv = 1.0f / run_scale[0];
+      }
+    }
+  };
+
+  f32x16 out[DB];
+#pragma unroll
+  for (int b = 0; b < DB; ++b)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) out[b][i] = 0.0f;
+  float top = -INFINITY, sum = 0.0f;
+  int v_exp = -112;
+
+  if (begin < end) {
+    load_ids(begin);
+    load_codes(begin);
+    load_ids(begin + kTile);
+    store(0);
+    __syncthreads();
+  }
+  for (int t0 = begin, buf = 0; t0 < end; t0 += kTile, buf ^= 1) {
+    const bool more = t0 + kTile < end;
+    if (more) {
+      load_codes(t0 + kTile);
+      load_ids(t0 + 2 * kTile);
+    }
+    if (t0 < wave_end) {
+      f32x16 s[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const int t = 32 * b + r;
+          const u32x4 a = k_lds[buf][t * KCH + ((2 * k + h) ^ (t & (KCH - 1)))];
+          s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, qf[k]), s[b], 0, 0, 0);
+        }
+      }
+      Run run[kSubs];
+      float factor[kSubs];
+      bool whole = t0 + kTile <= all_seen;
+      int tile_exp = -112;
+#pragma unroll
+      for (int u = 0; u < kSubs; ++u) {
+        run[u] = runs[buf][u];
+        factor[u] = run[u].k * qs;
+        whole = whole && run[u].v >= 0.0f;
+        tile_exp = max(tile_exp, run[u].v > 0.0f ? scale_exp(run[u].v) : -112);
+      }
+      if (!__builtin_amdgcn_readfirstlane(whole)) {             // some row does not see some token
+#pragma unroll
+        for (int u = 0; u < kSubs; ++u) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int key = t0 + 16 * u + 8 * (i / 4) + 4 * h + i % 4;
+            const bool seen = key < end && key <= last_key && run[u].v >= 0.0f;
+            s[u / 2][8 * (u % 2) + i] = seen ? s[u / 2][8 * (u % 2) + i] * factor[u] : -INFINITY;
+          }
+          factor[u] = 1.0f;
+        }
+      }
+      float m = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < kSubs; ++u) {
+        float mu = s[u / 2][8 * (u % 2)];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) mu = fmaxf(mu, s[u / 2][8 * (u % 2) + i]);
+        m = fmaxf(m, mu * factor[u]);
+      }
+      m = max_halves(m);
+      tile_exp = __builtin_amdgcn_readfirstlane(tile_exp);
+      if (__any(m > top + kLazy) || tile_exp > v_exp) {
+        const float next = fmaxf(m, top), ref = next == -INFINITY ? 0.0f : next;
+        const int exp = max(tile_exp, v_exp);
+        const float by = __builtin_amdgcn_exp2f(top - ref);
+        sum *= by;
+        const float scaled = ldexpf(by, v_exp - exp);
+#pragma unroll
+        for (int b = 0; b < DB; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) out[b][i] *= scaled;
+        top = next;
+        v_exp = exp;
+      }
+      const float ref = top == -INFINITY ? 0.0f : top;
+      u32x4 p[kSubs];
+#pragma unroll
+      for (int u = 0; u < kSubs; ++u) {
+        const bool scaled = run[u].v > 0.0f;
+        const float off = (scaled ? run[u].v_log + (float)(kProbExp - v_exp) : (float)(kProbExp - 1)) - ref;
+        float add = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u / 2][8 * (u % 2) + i], factor[u], off));
+          const float b = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u / 2][8 * (u % 2) + i + 1], factor[u], off));
+          add += a + b;
+          p[u][i / 2] = f16_pair(a, b);
+        }
+        sum = __builtin_fmaf(add, scaled ? ldexpf(run[u].v_inv, v_exp - kProbExp) : ldexpf(1.0f, 1 - kProbExp), sum);
+      }
+#pragma unroll
+      for (int b = 0; b < DB; ++b)
+#pragma unroll
+        for (int u = 0; u < kSubs; ++u) {
+          const int d = 32 * b + r;
+          const u32x4 a = v_lds[buf][d * (kTile / 8) + ((2 * u + h) ^ ((d ^ (d >> 2)) & 7))];
+          out[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, p[u]), out[b], 0, 0, 0);
+        }
+    }
+    if (more) store(buf ^ 1);
+    __syncthreads();
+  }
+
+  // ---- outputs: register i of block b is dim 32 b + 8 (i / 4) + 4 h + i % 4 ----
+  sum += __shfl_xor(sum, 32);
+  if (row0 + r >= rows) return;
+  const float back = ldexpf(1.0f, v_exp - kProbExp);
+  const float by = splits == 1 ? (sum > 0.0f ? back / sum : 0.0f) : back;
+  const int64_t index = ((seq * c.heads + head) * rows + row) * splits + split;
+  uint16_t* dst = y + ((seq * tokens + row / group) * c.heads * group + head * group + row % group) * DIM;
+#pragma unroll
+  for (int b = 0; b < DB; ++b)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int d = 32 * b + 2 * i + 4 * h;
+      const f32x4 o = {out[b][i] * by, out[b][i + 1] * by, out[b][i + 2] * by, out[b][i + 3] * by};
+      if (splits == 1)
+        *reinterpret_cast<u32x2*>(dst + d) = u32x2{bf16x2_rne(o[0], o[1]), bf16x2_rne(o[2], o[3])};
+      else if (top != -INFINITY)
+        *reinterpret_cast<f32x4*>(part.out + index * DIM + d) = o;
+    }
+  if (splits > 1 && h == 0) {
+    part.stat[2 * index] = top;
+    part.stat[2 * index + 1] = sum;
+  }
+}
+
+}  // namespace
+
+template <int DIM>
+hipError_t launch_prompt(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs, int64_t tokens, int group,
+                         float scale, int64_t splits, uint16_t* y, Partial part, hipStream_t stream) {
+  const int64_t tiles = (tokens * group + kPromptRows - 1) / kPromptRows, total = seqs * c.heads * tiles * splits;
+  if (total > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((kv_prompt_kernel<DIM>), dim3((unsigned)total), dim3(kThreads), 0, stream, c, q, ldq, (int)tokens, group,
+                     scale, (int)splits, (int)tiles, (int)total, y, part);
+  return hipGetLastError();
+}
+
+template hipError_t launch_prompt<64>(const KvCache&, const uint16_t*, int64_t, int64_t, int64_t, int, float, int64_t,
+                                      uint16_t*, Partial, hipStream_t);
+template hipError_t launch_prompt<128>(const KvCache&, const uint16_t*, int64_t, int64_t, int64_t, int, float, int64_t,
+                                       uint16_t*, Partial, hipStream_t);
+
+}  // namespace kva
+}  // namespace w8a8
