@@ -305,7 +305,7 @@ w8a8_status w8a8_w4_quantize(const uint16_t* w, int64_t N, int64_t K, int group,
  * 32-bit word at byte (16 * (c / 8 % 4) + r) * 16 + 4 * (c / 32): element j = c % 8
  * at bit 4 * (j / 2) + 16 * (j % 2).  Scales: [N / 16][K / group][16].
  * w8a8_w4_pack lays a weight out once, at load time. */
-size_t w8a8_w4_code_bytes(int64_t N, int64_t K);              /* 0 for N or K <= 0 */
+size_t w8a8_w4_code_bytes(int64_t N, int64_t K);              /* 0 outside the limits */
 size_t w8a8_w4_scale_bytes(int64_t N, int64_t K, int group);  /* 0 also for a bad group */
 w8a8_status w8a8_w4_pack(const uint8_t* codes, const uint16_t* scales, int64_t N, int64_t K, int group,
                          uint8_t* codes_packed, uint16_t* scales_packed, hipStream_t stream);
@@ -314,11 +314,14 @@ w8a8_status w8a8_w4_pack(const uint8_t* codes, const uint16_t* scales, int64_t N
  * one rounding.  x bf16 [M, K], bias bf16 [N] or NULL, y bf16 [M, N].  N % 8 == 0,
  * 0 <= M <= W8A8_W4_MAX_M.  Made for M up to 64, where one pass over the weight
  * serves every token; larger M is computed 64 tokens at a time.  A token's
- * result does not depend on the others in the call. */
+ * result does not depend on the others in the call, nor on their number.  The
+ * workspace holds fp32 partial sums where K is long and N small, so that K is cut;
+ * w8a8_w4_workspace_bytes is 0, and workspace may be NULL, where it is not. */
 #define W8A8_W4_MAX_M (1 << 20)
+size_t w8a8_w4_workspace_bytes(int64_t M, int64_t N, int64_t K);
 w8a8_status w8a8_w4_linear(const uint16_t* x, const uint8_t* codes_packed, const uint16_t* scales_packed,
                            const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K, int group,
-                           hipStream_t stream);
+                           void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* ---- few tokens: a paged cache of keys and values in 8 bits ---------------------
  * Pages of `page` tokens (16, 32, 64 or 128) for `heads` cache heads of `dim` values

@@ -30,7 +30,10 @@ int main() {
   for (int64_t m : ends)
     for (int64_t n : ends)
       for (int64_t k : ends) {
-        seen += w8a8_w4_linear(u16, u8, u16, u16, u16, m, n, k, 32, nullptr) == DEV;
+        seen += w8a8_w4_linear(u16, u8, u16, u16, u16, m, n, k, 32, a, SIZE_MAX, nullptr) == DEV;
+        (void)w8a8_w4_workspace_bytes(m, n, k);
+        (void)w8a8_w4_code_bytes(n, k);
+        (void)w8a8_w4_scale_bytes(n, k, 32);
         seen += w8a8_w4_quantize(u16, n, k, 64, u8, u16, nullptr) == DEV;
         seen += w8a8_w4_pack(u8, u16, n, k, 128, u8, u16, nullptr) == DEV;
         for (int64_t w : ends) {
@@ -44,8 +47,8 @@ int main() {
         }
       }
   EXPECT(seen > 0, 1);
-  EXPECT(w8a8_w4_linear(u16, u8, u16, nullptr, u16, 1, 16, 256, 64, nullptr), DEV);
-  EXPECT(w8a8_w4_linear(u16, u8, u16, nullptr, u16, 1, 12, 256, 64, nullptr), W8A8_ERR_BAD_SHAPE);
+  EXPECT(w8a8_w4_linear(u16, u8, u16, nullptr, u16, 1, 16, 256, 64, a, 4096, nullptr), DEV);
+  EXPECT(w8a8_w4_linear(u16, u8, u16, nullptr, u16, 1, 12, 256, 64, a, 4096, nullptr), W8A8_ERR_BAD_SHAPE);
   if (failures == 0) std::printf("all argument checks as expected\n");
   return failures ? 1 : 0;
 }

@@ -11,9 +11,10 @@ hipError_t launch_w4_pack(const uint8_t*, const uint16_t*, int64_t, int64_t, int
   return hipErrorInvalidValue;
 }
 hipError_t launch_w4_linear(const uint16_t*, const uint8_t*, const uint16_t*, const uint16_t*, uint16_t*, int64_t,
-                            int64_t, int64_t, int, hipStream_t) {
+                            int64_t, int64_t, int, void*, hipStream_t) {
   return hipErrorInvalidValue;
 }
+int w4_splits(int64_t, int64_t) { return 3; }
 hipError_t launch_kv_append(const KvCache&, const uint16_t*, int64_t, const uint16_t*, int64_t, int64_t, int64_t,
                             hipStream_t) {
   return hipErrorInvalidValue;

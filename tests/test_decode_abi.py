@@ -21,7 +21,8 @@ def lib():
         "w8a8_w4_scale_bytes": (SZ, [I64, I64, I]),
         "w8a8_w4_quantize": (I, [P, I64, I64, I, P, P, P]),
         "w8a8_w4_pack": (I, [P, P, I64, I64, I, P, P, P]),
-        "w8a8_w4_linear": (I, [P, P, P, P, P, I64, I64, I64, I, P]),
+        "w8a8_w4_workspace_bytes": (SZ, [I64, I64, I64]),
+        "w8a8_w4_linear": (I, [P, P, P, P, P, I64, I64, I64, I, P, SZ, P]),
         "w8a8_kv_append": (I, [P, I64, P, I64, P, P, P, P, I64, P, I64, P] + [I64] * 5 + [P]),
         "w8a8_kv_read": (I, [P, P, P, P, I64, P, I64, P] + [I64] * 5 + [P, P, P]),
         "w8a8_kv_attention_workspace_bytes": (SZ, [I64] * 7),
@@ -45,22 +46,30 @@ def test_sizes(lib):
 
 
 def test_w4_refusals(lib):
-    f = lib.w8a8_w4_linear
-    assert f(A, A, A, None, A, -1, 16, 256, 64, None) == SHAPE
-    assert f(A, A, A, None, A, (1 << 20) + 1, 16, 256, 64, None) == SHAPE
-    assert f(A, A, A, None, A, 1, 12, 256, 64, None) == SHAPE
-    assert f(A, A, A, None, A, 1, 0, 256, 64, None) == SHAPE
-    assert f(A, A, A, None, A, 1, 16, 192, 64, None) == SHAPE
-    assert f(A, A, A, None, A, 1, 16, 131072 + 128, 64, None) == SHAPE
-    assert f(A, A, A, None, A, 1, 16, 256, 16, None) == BADARG
-    assert f(None, None, None, None, None, 0, 16, 256, 64, None) == OK
+    def f(x, w, s, b, y, m, n, k, group, ws=A, ws_bytes=1 << 30):
+        return lib.w8a8_w4_linear(x, w, s, b, y, m, n, k, group, ws, ws_bytes, None)
+
+    assert f(A, A, A, None, A, -1, 16, 256, 64) == SHAPE
+    assert f(A, A, A, None, A, (1 << 20) + 1, 16, 256, 64) == SHAPE
+    assert f(A, A, A, None, A, 1, 12, 256, 64) == SHAPE
+    assert f(A, A, A, None, A, 1, 0, 256, 64) == SHAPE
+    assert f(A, A, A, None, A, 1, 16, 192, 64) == SHAPE
+    assert f(A, A, A, None, A, 1, 16, 131072 + 128, 64) == SHAPE
+    assert f(A, A, A, None, A, 1, 16, 256, 16) == BADARG
+    assert f(None, None, None, None, None, 0, 16, 256, 64) == OK
     for i in (0, 1, 2, 4):
         p = [A, A, A, None, A]
         p[i] = None
-        assert f(*p, 1, 16, 256, 64, None) == NULLP
+        assert f(*p, 1, 16, 256, 64) == NULLP
         p[i] = U
-        assert f(*p, 1, 16, 256, 64, None) == MISALIGNED
-    assert f(A, A, A, U, A, 1, 16, 256, 64, None) == MISALIGNED
+        assert f(*p, 1, 16, 256, 64) == MISALIGNED
+    assert f(A, A, A, U, A, 1, 16, 256, 64) == MISALIGNED
+    need = lib.w8a8_w4_workspace_bytes(5, 1024, 16384)           # a long, narrow weight: K is cut
+    assert need >= 2 * 5 * 1024 * 4 and need % 256 == 0
+    assert f(A, A, A, None, A, 5, 1024, 16384, 64, A, need - 1) == BADARG
+    assert f(A, A, A, None, A, 5, 1024, 16384, 64, None, need) == NULLP
+    assert f(A, A, A, None, A, 5, 1024, 16384, 64, U, need) == MISALIGNED
+    assert lib.w8a8_w4_workspace_bytes(5, 1024, 1024) == 0 and lib.w8a8_w4_workspace_bytes(0, 1024, 16384) == 0
     for g in (lambda n, k, grp, p=A: lib.w8a8_w4_quantize(p, n, k, grp, A, A, None),
               lambda n, k, grp, p=A: lib.w8a8_w4_pack(A, A, n, k, grp, p, A, None)):
         assert g(-1, 256, 64) == SHAPE and g(8, 192, 64) == SHAPE and g(8, 256, 7) == BADARG
@@ -128,7 +137,7 @@ def test_valid_calls_without_a_gpu(lib):
     import torch
     if torch.cuda.is_available():
         pytest.skip("a GPU is present; covered by the GPU tests")
-    assert lib.w8a8_w4_linear(A, A, A, A, A, 1, 16, 256, 64, None) == DEVICE
+    assert lib.w8a8_w4_linear(A, A, A, A, A, 1, 16, 256, 64, None, 0, None) == DEVICE       # no workspace needed
     assert lib.w8a8_w4_quantize(A, 8, 256, 64, A, A, None) == DEVICE and lib.w8a8_w4_pack(A, A, 8, 256, 64, A, A, None) == DEVICE
     assert append(lib) == DEVICE and attend(lib) == DEVICE and read(lib) == DEVICE
     assert attend(lib, ws=None, ws_bytes=0, width=1) == DEVICE                # no workspace needed

@@ -70,12 +70,12 @@ def test_shapes(lib, N, K):
     run(lib, 3, N, K, 32 if K % 256 else 128, True, seed=N + K, full_range=True)
 
 
-@pytest.mark.parametrize("M,N,K,group", ((1, 1024, 1024, 128), (5, 5120, 17408, 32), (64, 5120, 5120, 64), (1, 17408, 5120, 128)))
+@pytest.mark.parametrize("M,N,K,group", ((1, 1024, 1024, 128), (5, 5120, 17408, 32), (64, 5120, 5120, 64), (1, 17408, 5120, 128), (16, 12288, 512, 32), (40, 264, 12544, 128)))
 def test_projection_sizes(lib, M, N, K, group):
     run(lib, M, N, K, group, True, seed=7)
 
 
-@pytest.mark.parametrize("N,K,group", ((40, 256, 32), (1024, 1024, 128), (520, 2176, 64)))
+@pytest.mark.parametrize("N,K,group", ((40, 256, 32), (1024, 1024, 128), (520, 2176, 64), (104, 16384, 32), (8264, 640, 128)))
 def test_a_token_alone_and_in_a_batch(lib, N, K, group):
     """Bit for bit the same, whichever form of the kernel the batch runs."""
     y, (x, cp, sp, b) = run(lib, 70, N, K, group, True, seed=3)

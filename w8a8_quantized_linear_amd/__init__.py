@@ -30,7 +30,8 @@ __all__ = [
     "w8a8_gemm_dequant_packed", "w8a8_gemm_swiglu_packed", "w8a8_fp8_gemm_dequant_packed",
     "w8a8_swiglu", "swiglu_quant_workspace_bytes", "w8a8_gateup_swiglu_quant_packed",
     "w8a8_gemm_i32_packed", "swiglu_quant_h", "w8a8_linear_packed_noalloc", "NOALLOC_MAX_WORKSPACE",
-    "w8a8_w4_quantize", "w8a8_w4_pack", "w8a8_w4_linear", "w4_code_bytes", "w4_scale_bytes", "KVCache", "kv_cache",
+    "w8a8_w4_quantize", "w8a8_w4_pack", "w8a8_w4_linear", "w4_code_bytes", "w4_scale_bytes",
+    "w4_workspace_bytes", "KVCache", "kv_cache",
     "w8a8_kv_append", "w8a8_kv_read", "w8a8_kv_attention", "kv_attention_workspace_bytes",
 ]
 
@@ -43,7 +44,6 @@ if not LIB_PATH.exists() or not LIB_PATH.with_name("_binding.so").exists():
 _lib = ctypes.CDLL(str(LIB_PATH))
 from . import _binding  # noqa: E402  (the calls for few tokens, which cost less than ctypes' marshalling)
 _P, _I64, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
-_F = ctypes.c_float
 _SIGS = {
     "w8a8_status_string": (ctypes.c_char_p, [_I]),
     "w8a8_workspace_bytes": (_SZ, [_I64, _I64]),
@@ -75,11 +75,8 @@ _SIGS = {
     "w8a8_w4_scale_bytes": (_SZ, [_I64, _I64, _I]),
     "w8a8_w4_quantize": (_I, [_P, _I64, _I64, _I, _P, _P, _P]),
     "w8a8_w4_pack": (_I, [_P, _P, _I64, _I64, _I, _P, _P, _P]),
-    "w8a8_w4_linear": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P]),
-    "w8a8_kv_append": (_I, [_P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P] + [_I64] * 5 + [_P]),
-    "w8a8_kv_read": (_I, [_P, _P, _P, _P, _I64, _P, _I64, _P] + [_I64] * 5 + [_P, _P, _P]),
+    "w8a8_w4_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "w8a8_kv_attention_workspace_bytes": (_SZ, [_I64] * 7),
-    "w8a8_kv_attention": (_I, [_P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P] + [_I64] * 6 + [_F, _P, _P, _SZ, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -527,10 +524,14 @@ def w8a8_w4_pack(codes: torch.Tensor, scales: torch.Tensor):
     return cp, sp
 
 
-def w8a8_w4_linear(x, codes_packed, scales_packed, N: int, group: int, bias=None, out=None):
+def w4_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_lib.w8a8_w4_workspace_bytes(M, N, K))
+
+
+def w8a8_w4_linear(x, codes_packed, scales_packed, N: int, group: int, bias=None, workspace=None, out=None):
     """y bf16 [M, N] = x bf16 [M, K] . w^T + bias with the 4-bit weight [N, K] in the packed layout
-    (w8a8_w4_pack)."""
-    y = _binding.w4_linear(x, codes_packed, scales_packed, N, group, bias, out, _raw_stream(_raw_device()))
+    (w8a8_w4_pack).  A token's result does not depend on the others in the call."""
+    y = _binding.w4_linear(x, codes_packed, scales_packed, N, group, bias, workspace, out, _raw_stream(_raw_device()))
     return y if type(y) is not int else _check(y, "w8a8_w4_linear")
 
 

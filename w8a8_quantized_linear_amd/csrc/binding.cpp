@@ -138,10 +138,26 @@ bool expect(Py_ssize_t got, Py_ssize_t wanted) {
   return got == wanted;
 }
 
-// (x, codes_packed, scales_packed, N, group, bias, out, stream)
+// The caller's workspace of at least `need` bytes, or a new one if any is needed.
+at::Tensor workspace(PyObject* o, size_t need, int device) {
+  if (o == Py_None) {
+    if (!need) return at::Tensor();
+    return at::empty({(int64_t)need}, at::TensorOptions().dtype(at::kByte).device(at::Device(at::kCUDA, (c10::DeviceIndex)device)));
+  }
+  const at::Tensor& t = tensor(o, "workspace");
+  check_device(t, "workspace", device);
+  if (!t.is_contiguous()) fail(PyExc_ValueError, "workspace: must be contiguous");
+  if (t.nbytes() < need)
+    fail(PyExc_ValueError, "workspace: needs " + std::to_string(need) + " bytes, has " + std::to_string(t.nbytes()));
+  return t;
+}
+void* ptr_of(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+size_t bytes_of(const at::Tensor& t) { return t.defined() ? t.nbytes() : 0; }
+
+// (x, codes_packed, scales_packed, N, group, bias, workspace, out, stream)
 PyObject* w4_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (!expect(n, 8)) return nullptr;
+  if (!expect(n, 9)) return nullptr;
   try {
     const int device = c10::hip::current_device();
     const at::Tensor& x = want(a[0], at::kBFloat16, "x", 2, device);
@@ -160,10 +176,12 @@ PyObject* w4_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (b.size(0) != N) fail(PyExc_ValueError, "bias length must equal N");
       bias = bf16(b);
     }
-    const at::Tensor y = output(a[6], "out", {M, N}, device);
+    const at::Tensor ws = workspace(a[6], w8a8_w4_workspace_bytes(M, N, K), device);
+    const at::Tensor y = output(a[7], "out", {M, N}, device);
     w8a8_status st;
     Py_BEGIN_ALLOW_THREADS
-    st = w8a8_w4_linear(bf16(x), static_cast<const uint8_t*>(w.data_ptr()), bf16(s), bias, bf16(y), M, N, K, (int)group, stream_of(a[7]));
+    st = w8a8_w4_linear(bf16(x), static_cast<const uint8_t*>(w.data_ptr()), bf16(s), bias, bf16(y), M, N, K, (int)group, ptr_of(ws),
+                        bytes_of(ws), stream_of(a[8]));
     Py_END_ALLOW_THREADS
     return result(st, y);
   } catch (const PythonError&) {
@@ -236,22 +254,13 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (scale == -1.0 && PyErr_Occurred()) return nullptr;
     }
     const size_t need = w8a8_kv_attention_workspace_bytes(c.seqs, tokens, q_heads, c.heads, c.dim, c.page, c.width);
-    at::Tensor ws;
-    if (a[5] != Py_None) {
-      ws = tensor(a[5], "workspace");
-      check_device(ws, "workspace", c.device);
-      if (!ws.is_contiguous()) fail(PyExc_ValueError, "workspace: must be contiguous");
-      if (ws.nbytes() < need)
-        fail(PyExc_ValueError, "workspace: needs " + std::to_string(need) + " bytes, has " + std::to_string(ws.nbytes()));
-    } else if (need) {
-      ws = at::empty({(int64_t)need}, q.options().dtype(at::kByte));
-    }
+    const at::Tensor ws = workspace(a[5], need, c.device);
     const at::Tensor y = output(a[6], "out", {c.seqs, tokens, q_heads, c.dim}, c.device);
     w8a8_status st;
     Py_BEGIN_ALLOW_THREADS
     st = w8a8_kv_attention(bf16(q), ldq, c.k_codes(), c.k_scale(), c.v_codes(), c.v_scale(), c.pages, c.table_ptr(), c.width,
                            c.lens_ptr(), c.seqs, tokens, q_heads, c.heads, c.dim, c.page, (float)scale, bf16(y),
-                           ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, stream_of(a[7]));
+                           ptr_of(ws), bytes_of(ws), stream_of(a[7]));
     Py_END_ALLOW_THREADS
     return result(st, y);
   } catch (const PythonError&) {

@@ -37,13 +37,19 @@ bool ld_ok(int64_t ld, int64_t least) { return ld >= least && ld % 8 == 0 && ld 
 extern "C" {
 
 size_t w8a8_w4_code_bytes(int64_t N, int64_t K) {
-  if (N <= 0 || K <= 0) return 0;
+  if (N <= 0 || K <= 0 || N > kMaxRows || K > W8A8_MAX_K) return 0;
   return (size_t)((N + 15) / 16 * 16) * (size_t)(K / 2);
 }
 
 size_t w8a8_w4_scale_bytes(int64_t N, int64_t K, int group) {
-  if (N <= 0 || K <= 0 || !group_ok(group)) return 0;
+  if (N <= 0 || K <= 0 || N > kMaxRows || K > W8A8_MAX_K || !group_ok(group)) return 0;
   return (size_t)((N + 15) / 16 * 16) * (size_t)(K / group) * sizeof(uint16_t);
+}
+
+size_t w8a8_w4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0 || M > W8A8_W4_MAX_M || N > kMaxRows || K > W8A8_MAX_K) return 0;
+  const int splits = w8a8::w4_splits(N, K);
+  return splits == 1 ? 0 : align256((size_t)splits * (size_t)M * (size_t)N * sizeof(float));
 }
 
 w8a8_status w8a8_w4_quantize(const uint16_t* w, int64_t N, int64_t K, int group, uint8_t* codes, uint16_t* scales,
@@ -71,16 +77,19 @@ w8a8_status w8a8_w4_pack(const uint8_t* codes, const uint16_t* scales, int64_t N
 
 w8a8_status w8a8_w4_linear(const uint16_t* x, const uint8_t* codes_packed, const uint16_t* scales_packed,
                            const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K, int group,
-                           hipStream_t stream) {
+                           void* workspace, size_t workspace_bytes, hipStream_t stream) {
   w8a8_status st = check_w4_shape(N, K, group);
   if (st != W8A8_OK) return st;
   if (M < 0 || M > W8A8_W4_MAX_M || N < 1 || N % 8 != 0) return W8A8_ERR_BAD_SHAPE;
   if (M == 0) return W8A8_OK;
-  if (!x || !codes_packed || !scales_packed || !y) return W8A8_ERR_NULL_POINTER;
-  if (!aligned16(x) || !aligned16(codes_packed) || !aligned16(scales_packed) || !aligned16(y) || (bias && !aligned16(bias)))
+  const size_t need = w8a8_w4_workspace_bytes(M, N, K);
+  if (workspace_bytes < need) return W8A8_ERR_BAD_ARGUMENT;
+  if (!x || !codes_packed || !scales_packed || !y || (need && !workspace)) return W8A8_ERR_NULL_POINTER;
+  if (!aligned16(x) || !aligned16(codes_packed) || !aligned16(scales_packed) || !aligned16(y) || (bias && !aligned16(bias)) ||
+      (need && !aligned16(workspace)))
     return W8A8_ERR_MISALIGNED;
   if ((st = check_device()) != W8A8_OK) return st;
-  return launched(w8a8::launch_w4_linear(x, codes_packed, scales_packed, bias, y, M, N, K, group, stream));
+  return launched(w8a8::launch_w4_linear(x, codes_packed, scales_packed, bias, y, M, N, K, group, workspace, stream));
 }
 
 w8a8_status w8a8_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, int8_t* k_codes,

@@ -70,7 +70,8 @@ hipError_t launch_w4_pack(const uint8_t* codes, const uint16_t* scales, int64_t 
                           uint8_t* codes_packed, uint16_t* scales_packed, hipStream_t stream);
 hipError_t launch_w4_linear(const uint16_t* x, const uint8_t* codes_packed, const uint16_t* scales_packed,
                             const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K, int group,
-                            hipStream_t stream);
+                            void* workspace, hipStream_t stream);
+int w4_splits(int64_t N, int64_t K);   // parts of K whose fp32 sums [splits][M][N] the workspace holds (1: none)
 
 // A paged cache of int8 codes as the kernels see it (pointers of w8a8.h's cache
 // arguments): code pages [pages][heads][page][dim], scales [pages][heads].

@@ -82,133 +82,350 @@ w4_pack_scales_kernel(const uint16_t* __restrict__ scales, int64_t N, int64_t gr
 }
 
 // ---- the projection --------------------------------------------------------------
+// K is cut into kSegs * splits runs of 128-column blocks, run j from blocks * j / runs on; `splits` follows from N
+// and K alone.  Every form below sums a run block by block and group by group and then adds the runs in order
+// (those of a split first, then the splits), so an output does not depend on which form computed it.
+constexpr int kSegs = 8;
+__device__ __forceinline__ int run_begin(int blocks, int run, int runs) {
+  return (int)((unsigned)(blocks * run) / (unsigned)runs);
+}
+
 // Eight nibbles of a packed word -> eight bf16 values 128 + (code + 8): a bf16 between 128 and 256 has
-// steps of one, so the nibble is its low mantissa bits and one and-or makes two values.
-__device__ __forceinline__ bf16x8 widen(uint32_t w) {
+// steps of one, so the nibble is its low mantissa bits and one and-or makes two values (with the mask in a vector
+// register: the instruction takes one scalar).
+__device__ __forceinline__ bf16x8 widen(uint32_t w, uint32_t mask) {
   u32x4 v;
 #pragma unroll
-  for (int p = 0; p < 4; ++p) v[p] = ((w >> (4 * p)) & 0x000f000fu) | 0x43004300u;
+  for (int p = 0; p < 4; ++p) v[p] = ((w >> (4 * p)) & mask) | 0x43004300u;
+  return __builtin_bit_cast(bf16x8, v);
+}
+__device__ __forceinline__ uint32_t nibble_mask() {
+  uint32_t m = 0x000f000fu;
+  asm volatile("" : "+v"(m));
+  return m;
+}
+// Eight times -136: the widened codes' offset goes out through the accumulator, which starts a group at
+// -136 * sum(x), itself an MFMA.
+__device__ __forceinline__ bf16x8 minus_offset() {
+  const u32x4 v = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};
   return __builtin_bit_cast(bf16x8, v);
 }
 
-// A workgroup computes RB blocks of 16 rows for 16 * MB tokens; its waves take every WAVES-th block of 128
-// columns and meet in LDS.  MFMA 16x16x32: A = weights (lane 16 h + r: row r, columns 8 h .. 8 h + 7 of a
-// 32-column step), B = tokens, D: lane 16 h + t holds rows 4 h .. 4 h + 3 of token t.  The offset of the
-// widened codes goes out in the accumulator: a group's sum starts at -136 * sum(x), itself an MFMA with
-// a constant operand that the RB row blocks share.
-template <int MB, int RB, int GPB, int WAVES>
-__global__ void __launch_bounds__(64 * WAVES)
-w4_linear_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, const uint16_t* __restrict__ s,
-                 const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, int64_t M, int64_t N, int64_t K) {
-  __shared__ f32x4 red[WAVES][RB * MB][64];
+// v + bias[n .. n + 3], rounded to y[m][n .. n + 3]; or a split's part of it.
+__device__ __forceinline__ void store_outputs(f32x4 v, int64_t m, int64_t n, int64_t M, int64_t N, const uint16_t* bias,
+                                              uint16_t* y, float* part, int split, int splits) {
+  if (splits > 1) {
+    *reinterpret_cast<f32x4*>(part + (split * M + m) * N + n) = v;
+    return;
+  }
+  if (bias) {
+    float b[4];
+    bf16x4(*reinterpret_cast<const uint2*>(bias + n), b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += b[i];
+  }
+  *reinterpret_cast<u32x2*>(y + m * N + n) = u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+}
+
+// Up to 16 tokens.  A workgroup computes RB blocks of 16 rows; each of its kSegs waves takes one run of columns,
+// and the runs meet in LDS.  MFMA 16x16x32: A = weights (lane 16 h + r: row r, columns 8 h .. 8 h + 7 of a
+// 32-column step), B = tokens, D: lane 16 h + t holds rows 4 h .. 4 h + 3 of token t.  Bound by the weights' bytes:
+// a wave has the next block's loads in flight while it multiplies.  x and the scales pass through an LDS area
+// of the wave's own: loaded straight into operands, a block of x takes 4 instructions that touch 16 rows
+// each (and with groups of 32 the scales 4 more per row block), which held 5 tokens of 17,408 x 5,120 to 27 us; as
+// XI instructions of 4 whole row pieces and one for the scales they take 15.6 us.
+template <int XI, int RB, int GPB>
+__global__ void __launch_bounds__(64 * kSegs)
+w4_few_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, const uint16_t* __restrict__ s,
+              const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, float* __restrict__ part, int64_t M, int64_t N,
+              int64_t K) {
+  constexpr int XROWS = 4 * XI;                // token rows kept (M <= XROWS; the operand's other lanes repeat them)
+  constexpr int SL = 2 * GPB;                  // 16-byte pieces of a row block's scales
+  static_assert(RB * SL <= 64, "one instruction brings the scales");
+  constexpr int AREA = XROWS * 16 + 64;        // 16-byte units of a wave's area
+  constexpr int UNITS = kSegs * (AREA > RB * 64 ? AREA : RB * 64);
+  __shared__ __attribute__((aligned(16))) u32x4 lds[UNITS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 4, t = lane & 15;
-  const int64_t blocks = (N + kRows - 1) / kRows, b0 = (int64_t)blockIdx.x * RB, m0 = (int64_t)blockIdx.y * 16 * MB;
+  const int split = blockIdx.z, splits = gridDim.z;
+  const int64_t blocks = (N + kRows - 1) / kRows, b0 = (int64_t)blockIdx.x * RB;
   const int kb_all = (int)(K / kCols);
+  const int first = run_begin(kb_all, split * kSegs + wave, kSegs * splits);
+  const int n = run_begin(kb_all, split * kSegs + wave + 1, kSegs * splits) - first;
+  u32x4* xl = lds + wave * AREA;
+  u32x4* sl = xl + XROWS * 16;
 
-  const uint16_t* xp[MB];
+  const uint16_t* xp[XI];
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb) xp[mb] = x + min(m0 + 16 * mb + t, M - 1) * K + 8 * h;   // past M: row M - 1, not stored
+  for (int i = 0; i < XI; ++i) xp[i] = x + min<int64_t>(4 * i + h, M - 1) * K + 8 * t;     // past M: row M - 1, not stored
   const uint8_t* wp[RB];
-  const uint16_t* sp[RB];
 #pragma unroll
-  for (int rb = 0; rb < RB; ++rb) {
-    const int64_t block = min(b0 + rb, blocks - 1) * kb_all;
-    wp[rb] = w + block * kBlockBytes + 16 * lane;
-    sp[rb] = s + block * (GPB * kRows) + 4 * h;
-  }
-  const u32x4 offs = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};   // -136
-  const bf16x8 minus136 = __builtin_bit_cast(bf16x8, offs);
+  for (int rb = 0; rb < RB; ++rb) wp[rb] = w + min(b0 + rb, blocks - 1) * kb_all * kBlockBytes + 16 * lane;
+  const int sc_piece = min(lane, RB * SL - 1);
+  const uint16_t* sp = s + min(b0 + sc_piece / SL, blocks - 1) * kb_all * (GPB * kRows) + sc_piece % SL * 8;
+  const bf16x8 offset = minus_offset();
+  const uint32_t mask = nibble_mask();
 
-  f32x4 tot[RB][MB];
+  f32x4 tot[RB];
 #pragma unroll
-  for (int rb = 0; rb < RB; ++rb)
+  for (int rb = 0; rb < RB; ++rb) tot[rb] = f32x4{0.f, 0.f, 0.f, 0.f};
+  u32x4 wv[2][RB], xv[XI], sv;
+  auto load_w = [&](int d, int i) __attribute__((always_inline)) {
+    const int64_t kb = first + min(i, n - 1);
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb) tot[rb][mb] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  for (int kb = wave; kb < kb_all; kb += WAVES) {
-    u32x4 wv[RB];
-    u32x2 sv[RB][GPB];
-    bf16x8 xv[4][MB];
+    for (int rb = 0; rb < RB; ++rb) wv[d][rb] = *reinterpret_cast<const u32x4*>(wp[rb] + kb * kBlockBytes);
+  };
+  auto load_x = [&](int i) __attribute__((always_inline)) {
+    const int kb = first + min(i, n - 1);
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) wv[rb] = *reinterpret_cast<const u32x4*>(wp[rb] + (int64_t)kb * kBlockBytes);
+    for (int j = 0; j < XI; ++j) xv[j] = *reinterpret_cast<const u32x4*>(xp[j] + kb * kCols);
+    sv = *reinterpret_cast<const u32x4*>(sp + kb * (GPB * kRows));
+  };
+  // a wave's LDS operations are done in their order, so its area needs no barrier
+  auto put_x = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-      for (int g = 0; g < GPB; ++g)
-        sv[rb][g] = *reinterpret_cast<const u32x2*>(sp[rb] + (kb * GPB + g) * kRows);
-#pragma unroll
-    for (int st = 0; st < 4; ++st)
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb) xv[st][mb] = *reinterpret_cast<const bf16x8*>(xp[mb] + kb * kCols + 32 * st);
+    for (int j = 0; j < XI; ++j) xl[(4 * j + h) * 16 + (t ^ (4 * j + h))] = xv[j];
+    sl[lane] = sv;
+  };
+  auto multiply = [&](int d) __attribute__((always_inline)) {
     constexpr int SPG = 4 / GPB;               // MFMA steps per group
 #pragma unroll
     for (int g = 0; g < GPB; ++g) {
-      f32x4 base[MB];
+      bf16x8 xf[SPG];
+      f32x4 base = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) {
-        base[mb] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int st = 0; st < SPG; ++st)
-          base[mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(minus136, xv[g * SPG + st][mb], base[mb], 0, 0, 0);
+      for (int st = 0; st < SPG; ++st) {
+        const int row = t % XROWS;
+        xf[st] = __builtin_bit_cast(bf16x8, xl[row * 16 + ((4 * (g * SPG + st) + h) ^ row)]);
+        base = __builtin_amdgcn_mfma_f32_16x16x32_bf16(offset, xf[st], base, 0, 0, 0);
       }
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
-        f32x4 acc[MB];
+        f32x4 acc = base;
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) acc[mb] = base[mb];
+        for (int st = 0; st < SPG; ++st)
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(wv[d][rb][g * SPG + st], mask), xf[st], acc, 0, 0, 0);
+        float sc[4];
+        bf16x4(reinterpret_cast<const uint2*>(sl)[(rb * GPB + g) * 4 + h], sc);
 #pragma unroll
-        for (int st = 0; st < SPG; ++st) {
-          const bf16x8 a = widen(wv[rb][g * SPG + st]);
+        for (int i = 0; i < 4; ++i) tot[rb][i] = __builtin_fmaf(sc[i], acc[i], tot[rb][i]);
+      }
+    }
+  };
+  if (n > 0) {
+    load_x(0);
+    load_w(0, 0);
+    for (int i = 0; i < n; i += 2) {
 #pragma unroll
-          for (int mb = 0; mb < MB; ++mb)
-            acc[mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, xv[g * SPG + st][mb], acc[mb], 0, 0, 0);
-        }
-        const u32x2 sw = sv[rb][g];
-        const float sc[4] = {__uint_as_float(sw[0] << 16), __uint_as_float(sw[0] & 0xffff0000u),
-                             __uint_as_float(sw[1] << 16), __uint_as_float(sw[1] & 0xffff0000u)};
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tot[rb][mb][i] = __builtin_fmaf(sc[i], acc[mb][i], tot[rb][mb][i]);
+      for (int d = 0; d < 2; ++d) {
+        if (d && i + d >= n) break;
+        __builtin_amdgcn_sched_barrier(0);
+        load_w(d ^ 1, i + d + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        put_x();
+        load_x(i + d + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(d);
       }
     }
   }
 
+  f32x4* red = reinterpret_cast<f32x4*>(lds);
+  __syncthreads();                             // every wave is done with its area
 #pragma unroll
-  for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) red[wave][rb * MB + mb][lane] = tot[rb][mb];
+  for (int rb = 0; rb < RB; ++rb) red[(wave * RB + rb) * 64 + lane] = tot[rb];
   __syncthreads();
-  for (int j = threadIdx.x; j < RB * MB * 64; j += 64 * WAVES) {
-    const int rb = j / 64 / MB, mb = j / 64 % MB, l = j % 64;
-    const int64_t m = m0 + 16 * mb + l % 16, n = (b0 + rb) * kRows + 4 * (l / 16);
-    if (m >= M || n >= N) continue;            // N % 8 == 0: the four rows are whole or absent
-    f32x4 v = red[0][rb * MB + mb][l];
+  for (int j = threadIdx.x; j < RB * 64; j += 64 * kSegs) {
+    const int64_t m = j % 16, row = (b0 + j / 64) * kRows + 4 * (j % 64 / 16);
+    if (m >= M || row >= N) continue;          // N % 8 == 0: the four rows are whole or absent
+    f32x4 v = red[j];
 #pragma unroll
-    for (int wv = 1; wv < WAVES; ++wv) v += red[wv][rb * MB + mb][l];
-    if (bias) {
-      float bv[4];
-      bf16x4(*reinterpret_cast<const uint2*>(bias + n), bv);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += bv[i];
-    }
-    *reinterpret_cast<u32x2*>(y + m * N + n) = u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+    for (int wv = 1; wv < kSegs; ++wv) v += red[wv * RB * 64 + j];
+    store_outputs(v, m, row, M, N, bias, y, part, split, splits);
   }
 }
 
-template <int MB, int RB, int WAVES>
-hipError_t launch_linear(const uint16_t* x, const uint8_t* w, const uint16_t* s, const uint16_t* bias, uint16_t* y,
-                         int64_t M, int64_t N, int64_t K, int group, hipStream_t stream) {
-  const int64_t gx = ((N + kRows - 1) / kRows + RB - 1) / RB, gy = (M + 16 * MB - 1) / (16 * MB);
-  if (gx > 0x7fffffff || gy > 65535) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)gx, (unsigned)gy), block(64 * WAVES);
-  if (group == 128)
-    hipLaunchKernelGGL((w4_linear_kernel<MB, RB, 1, WAVES>), grid, block, 0, stream, x, w, s, bias, y, M, N, K);
-  else if (group == 64)
-    hipLaunchKernelGGL((w4_linear_kernel<MB, RB, 2, WAVES>), grid, block, 0, stream, x, w, s, bias, y, M, N, K);
-  else
-    hipLaunchKernelGGL((w4_linear_kernel<MB, RB, 4, WAVES>), grid, block, 0, stream, x, w, s, bias, y, M, N, K);
+// 17 tokens and more, 16 * MB at a time.  A wave owns a block of 16 rows and walks the split's columns; the workgroup's
+// waves share each 128-column tile of x in LDS (two of them, one barrier a block), so x is read once for
+// all their rows.  Weights and scales go straight to registers, kAhead blocks ahead.  What bounds it is the
+// step from block to block: per wave 32 MFMAs, 16 operand reads and ~120 vector instructions that the
+// barrier keeps in step, about 2,600 cycles for 9 waves where each pipe alone would need 1,150: 64 tokens of
+// 5,120 x 34,816 take 49 us (a wave per row block without sharing x took 197 us).
+constexpr int kAhead = 4;
+__device__ __forceinline__ void lds_barrier() {       // __syncthreads would wait for the loads in flight, too
+  __builtin_amdgcn_s_waitcnt(0xc07f);                 // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <int MB, int GPB, int WMIN, int WMAX>
+__global__ void __launch_bounds__(64 * WMAX)
+w4_many_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, const uint16_t* __restrict__ s,
+               const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, float* __restrict__ part, int64_t M, int64_t N,
+               int64_t K) {
+  constexpr int PIECES = MB * 256;             // 16-byte pieces of a tile of x
+  constexpr int XP = (PIECES + 64 * WMIN - 1) / (64 * WMIN);     // of a thread, at least WMIN waves
+  constexpr int SPG = 4 / GPB;
+  __shared__ __attribute__((aligned(16))) u32x4 tile[2 * PIECES];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
+  const int h = lane >> 4, t = lane & 15;
+  const int split = blockIdx.z, splits = gridDim.z, runs = kSegs * splits;
+  const int64_t blocks = (N + kRows - 1) / kRows, mine = (int64_t)blockIdx.x * waves + wave, m0 = (int64_t)blockIdx.y * 16 * MB;
+  const int kb_all = (int)(K / kCols);
+  const int first = run_begin(kb_all, split * kSegs, runs), n = run_begin(kb_all, split * kSegs + kSegs, runs) - first;
+
+  const uint16_t* xp[XP];
+  int xo[XP];
+#pragma unroll
+  for (int i = 0; i < XP; ++i) {
+    const int p = min(tid + i * 64 * waves, PIECES - 1), row = p / 16, ch = p % 16;   // (past the last: the last again)
+    xp[i] = x + min(m0 + row, M - 1) * K + (int64_t)first * kCols + 8 * ch;
+    xo[i] = row * 16 + (ch ^ (row & 15));
+  }
+  const int64_t block = min(mine, blocks - 1) * kb_all + first;
+  const uint8_t* wp = w + block * kBlockBytes + 16 * lane;
+  const uint16_t* sp = s + block * (GPB * kRows) + 4 * h;
+  const bf16x8 offset = minus_offset();
+  const uint32_t mask = nibble_mask();
+
+  f32x4 tot[MB], sum[MB];
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) tot[mb] = sum[mb] = f32x4{0.f, 0.f, 0.f, 0.f};
+  u32x4 xr[XP], wv[kAhead];
+  uint2 sv[kAhead][GPB];
+  auto load_x = [&](int i) __attribute__((always_inline)) {
+    const int kb = min(i, n - 1);
+#pragma unroll
+    for (int j = 0; j < XP; ++j) xr[j] = *reinterpret_cast<const u32x4*>(xp[j] + kb * kCols);
+  };
+  auto put_x = [&](int b) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < XP; ++j) tile[b * PIECES + xo[j]] = xr[j];
+  };
+  auto load_w = [&](int d, int i) __attribute__((always_inline)) {
+    const int64_t kb = min(i, n - 1);
+    wv[d] = *reinterpret_cast<const u32x4*>(wp + kb * kBlockBytes);
+#pragma unroll
+    for (int g = 0; g < GPB; ++g) sv[d][g] = *reinterpret_cast<const uint2*>(sp + (kb * GPB + g) * kRows);
+  };
+  if (n > 0) {
+    // (in the loop's order, the last weights after the second tile, so that waiting for a tile never waits for
+    // weights that are not needed yet)
+    load_x(0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int d = 0; d < kAhead - 1; ++d) load_w(d, d);
+    __builtin_amdgcn_sched_barrier(0);
+    put_x(0);
+    load_x(1);
+    __builtin_amdgcn_sched_barrier(0);
+    load_w(kAhead - 1, kAhead - 1);
+    __builtin_amdgcn_sched_barrier(0);
+    lds_barrier();
+    int run = 0, run_end = 0, b = 0;
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+#pragma unroll
+      for (int d = 0; d < kAhead; ++d) {
+        const int i = i0 + d;
+        if (d && i >= n) break;
+        put_x(b ^ 1);                          // read last before the barrier just passed
+        load_x(i + 2);
+        __builtin_amdgcn_sched_barrier(0);
+        if (i == run_end) {
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb) {
+            sum[mb] += tot[mb];
+            tot[mb] = f32x4{0.f, 0.f, 0.f, 0.f};
+          }
+          do {                                 // (runs of no blocks add nothing)
+            ++run;
+            run_end = run < kSegs ? run_begin(kb_all, split * kSegs + run, runs) - first : n;
+          } while (i == run_end);
+        }
+#pragma unroll
+        for (int g = 0; g < GPB; ++g) {
+          f32x4 acc[MB];
+          bf16x8 xf[SPG][MB];
+#pragma unroll
+          for (int st = 0; st < SPG; ++st)
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+              xf[st][mb] = __builtin_bit_cast(bf16x8, tile[b * PIECES + (16 * mb + t) * 16 + ((4 * (g * SPG + st) + h) ^ t)]);
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb) {
+            acc[mb] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int st = 0; st < SPG; ++st) acc[mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(offset, xf[st][mb], acc[mb], 0, 0, 0);
+          }
+#pragma unroll
+          for (int st = 0; st < SPG; ++st) {
+            const bf16x8 a = widen(wv[d][g * SPG + st], mask);
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) acc[mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, xf[st][mb], acc[mb], 0, 0, 0);
+          }
+          float sc[4];
+          bf16x4(sv[d][g], sc);
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) tot[mb][e] = __builtin_fmaf(sc[e], acc[mb][e], tot[mb][e]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        load_w(d, i + kAhead);
+        __builtin_amdgcn_sched_barrier(0);
+        b ^= 1;
+        lds_barrier();
+      }
+    }
+  }
+  if (mine >= blocks) return;
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) {
+    const int64_t m = m0 + 16 * mb + t, row = mine * kRows + 4 * h;
+    if (m < M && row < N) store_outputs(sum[mb] + tot[mb], m, row, M, N, bias, y, part, split, splits);
+  }
+}
+
+// The splits' parts, added in order: four outputs a thread.
+__global__ void __launch_bounds__(256)
+w4_combine_kernel(const float* __restrict__ part, const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, int64_t M,
+                  int64_t N, int splits) {
+  const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (j >= M * N / 4) return;
+  f32x4 v = *reinterpret_cast<const f32x4*>(part + 4 * j);
+  for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(part + s * M * N + 4 * j);
+  store_outputs(v, 4 * j / N, 4 * j % N, M, N, bias, y, nullptr, 0, 1);
+}
+
+struct Linear {
+  const uint16_t* x;
+  const uint8_t* w;
+  const uint16_t* s;
+  const uint16_t* bias;
+  uint16_t* y;
+  float* part;
+  int64_t M, N, K;
+  int group, splits;
+  hipStream_t stream;
+};
+
+template <int XI, int RB>
+hipError_t launch_few(const Linear& a) {
+  const int64_t blocks = (a.N + kRows - 1) / kRows, gx = (blocks + RB - 1) / RB;
+  const dim3 grid((unsigned)gx, 1, (unsigned)a.splits), block(64 * kSegs);
+  const auto kernel = a.group == 128 ? w4_few_kernel<XI, RB, 1> : a.group == 64 ? w4_few_kernel<XI, RB, 2> : w4_few_kernel<XI, RB, 4>;
+  hipLaunchKernelGGL(kernel, grid, block, 0, a.stream, a.x, a.w, a.s, a.bias, a.y, a.part, a.M, a.N, a.K);
+  return hipGetLastError();
+}
+
+template <int MB, int WMIN, int WMAX>
+hipError_t launch_many(const Linear& a, int waves) {
+  const int64_t blocks = (a.N + kRows - 1) / kRows;
+  const dim3 grid((unsigned)((blocks + waves - 1) / waves), (unsigned)((a.M + 16 * MB - 1) / (16 * MB)), (unsigned)a.splits);
+  const auto kernel = a.group == 128  ? w4_many_kernel<MB, 1, WMIN, WMAX>
+                      : a.group == 64 ? w4_many_kernel<MB, 2, WMIN, WMAX>
+                                      : w4_many_kernel<MB, 4, WMIN, WMAX>;
+  hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), 0, a.stream, a.x, a.w, a.s, a.bias, a.y, a.part, a.M, a.N, a.K);
   return hipGetLastError();
 }
 
@@ -236,12 +453,41 @@ hipError_t launch_w4_pack(const uint8_t* codes, const uint16_t* scales, int64_t 
   return hipGetLastError();
 }
 
+// Splits of K: one launch is faster unless a weight is long and narrow, where too few workgroups would each walk a
+// long K (5 tokens of 17,408 x 5,120: 19.3 us in one piece, 15.6 us in three with their combination; 5,120 x 5,120
+// and 5,120 x 34,816 are faster in one).  It does not go by M: a token's sums are the same in every batch.
+int w4_splits(int64_t N, int64_t K) {
+  const int64_t blocks = (N + kRows - 1) / kRows;
+  return blocks <= 512 && K / kCols >= 96 ? 3 : 1;
+}
+
 hipError_t launch_w4_linear(const uint16_t* x, const uint8_t* codes_packed, const uint16_t* scales_packed,
                             const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K, int group,
-                            hipStream_t stream) {
-  if (M <= 16) return launch_linear<1, 1, 8>(x, codes_packed, scales_packed, bias, y, M, N, K, group, stream);
-  if (M <= 32) return launch_linear<2, 1, 8>(x, codes_packed, scales_packed, bias, y, M, N, K, group, stream);
-  return launch_linear<4, 1, 8>(x, codes_packed, scales_packed, bias, y, M, N, K, group, stream);
+                            void* workspace, hipStream_t stream) {
+  const Linear a{x, codes_packed, scales_packed, bias, y, static_cast<float*>(workspace), M, N, K, group, w4_splits(N, K), stream};
+  const int64_t blocks = (N + kRows - 1) / kRows;
+  hipError_t e;
+  if (M <= 16) {
+    // more row blocks a workgroup share x, as long as there are workgroups for the 256 CUs
+    const int64_t items = blocks * a.splits;
+    if (M <= 4) e = items >= 512 ? launch_few<1, 2>(a) : launch_few<1, 1>(a);
+    else e = items >= 768 ? launch_few<4, 4>(a) : items >= 512 ? launch_few<4, 2>(a) : launch_few<4, 1>(a);
+  } else {
+    // waves (row blocks) of a workgroup: fewest rounds of the 256 CUs, a round costing a little besides its waves
+    const int64_t tiles = (M + (M <= 32 ? 31 : 63)) / (M <= 32 ? 32 : 64) * a.splits;
+    int waves = 4;
+    int64_t least = 0;
+    for (int v = 4; v <= 12; ++v) {
+      const int64_t cost = ((blocks + v - 1) / v * tiles + 255) / 256 * (v + 3);
+      if (v == 4 || cost < least) waves = v, least = cost;
+    }
+    if (M <= 32) e = waves < 8 ? launch_many<2, 4, 7>(a, waves) : launch_many<2, 8, 12>(a, waves);
+    else e = waves < 8 ? launch_many<4, 4, 7>(a, waves) : launch_many<4, 8, 12>(a, waves);
+  }
+  if (e != hipSuccess || a.splits == 1) return e;
+  hipLaunchKernelGGL(w4_combine_kernel, dim3((unsigned)((M * N / 4 + 255) / 256)), dim3(256), 0, stream, a.part, bias, y, M, N,
+                     a.splits);
+  return hipGetLastError();
 }
 
 }  // namespace w8a8
