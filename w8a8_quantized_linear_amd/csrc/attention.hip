@@ -7,9 +7,12 @@
 //
 // Arithmetic.  Codes are whole numbers below 128 and exact in f16, so both products run on the f16 matrix
 // cores with fp32 sums: a row of q is scaled by a power of two to below 2^8 (what falls under f16's range
-// is below 2^-32 of the row's largest value), the keys' scale multiplies the fp32 score, and the probabilities
-// (below 1, times the values' scale relative to a power of two, times 2^14) are rounded to f16, 11 bits.
-// Maximum, sum and output are fp32.
+// is below 2^-32 of the row's largest value); the keys' scale multiplies the fp32 score, and the values' scale rides in
+// the exponent, p' = 2^(s - max + log2(scale) - e), so it costs nothing per element; p' is rounded to f16, 11 bits, and
+// the sum of p' over a page is divided by the scale again.  A page whose values have scale zero (or subnormal: taken
+// for zero) counts as one of scale 2^(e-1) with codes of zero.  The running maximum moves only when a row's
+// score passes it by more than 2^8 (p' stays below 2^15), which spares most steps the rescaling of the outputs
+// and the exchange between lanes.  Maximum, sum and output are fp32.
 #include <algorithm>
 
 #include "attention_math.h"
@@ -20,37 +23,28 @@ namespace {
 using namespace kva;
 
 constexpr int kWaves = 4;
-constexpr int kTile = 32;                       // tokens of a wave's step: two MFMA tiles of 16
-constexpr int kSegment = 2048;                  // tokens whose page entries are in LDS at once
-constexpr int kEntries = kSegment / 16;         // pages of a segment at the smallest page
+constexpr int kTile = 32;                       // tokens of a wave's step: two runs of 16
 constexpr int kStep = kWaves * kTile;           // pieces of a sequence are whole steps of a workgroup
 static_assert(kPiece % kStep == 0, "pieces are whole steps");
-constexpr int kProbExp = 14;                    // probabilities are rounded below 2^14 (f16 ends at 2^16)
 
-// The largest of the four lanes l, l ^ 16, l ^ 32, l ^ 48.
-__device__ __forceinline__ float max_quarters(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
 }
-__device__ __forceinline__ float sum_quarters(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
-}
-
-struct Entry {
-  int32_t id;        // page, -1: none
-  float k, v;        // its scales
-};
 
 // One workgroup: 16 * NB query rows (tokens x the heads that share a cache head) against one piece of a
-// sequence; its waves take every fourth step of 32 tokens and meet in LDS.
+// sequence; its waves take every fourth step of 32 tokens and meet in LDS.  Bound by the cache's bytes where the
+// sequences are long, by latency where they are short (length -> table -> codes -> scores -> outputs), so a wave has
+// the next step's codes in flight while it computes, keeps the pages and scales of 64 blocks in a register each
+// (lane i: block i) instead of LDS, and waits for no other wave before the end.  MFMA 16x16x32 f16:
+//   S^T = K Q^T: a lane's 16 bytes of a key are two operands as they come from memory;
+//   O^T += V^T P^T: P^T is S^T's layout as it stands; V^T takes byte b of a lane's eight values as output block b,
+//   so one 8-byte piece per token serves all blocks and nothing is transposed through LDS.
 template <int DIM, int NB>
 __global__ void __launch_bounds__(256)
 kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tokens, int group, float scale,
                     int splits, int row_tiles, uint16_t* __restrict__ y, Partial part) {
   constexpr int DC = DIM / 64;                  // 16-byte pieces of a lane's key
   constexpr int DB = DIM / 16;                  // output blocks; bytes of a lane's value piece
-  __shared__ Entry entries[kEntries];
   __shared__ float red_max[kWaves][16], red_sum[kWaves][16];
   __shared__ f32x4 red_out[kWaves][DB][64];
 
@@ -69,6 +63,7 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
   const int first_pos = len - tokens;
   const int last_row = min(row0 + 16 * NB, rows) - 1;
   const int begin = min(split * piece, held), end = min(min(begin + piece, held), first_pos + last_row / group + 1);
+  const int all_seen = min(end, first_pos + row0 / group + 1);         // every row sees the keys before it
 
   // ---- queries: operand B of S^T = K Q^T, lane 16 h + r holds row r, dims 64 c + 16 h .. + 15 ----
   u32x4 qf[NB][DC][2];
@@ -79,28 +74,58 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
     const int row = min(row0 + 16 * n + r, rows - 1);
     const uint16_t* src = q + (seq * tokens + row / group) * ldq + (head * group + row % group) * DIM + 16 * h;
     last_key[n] = first_pos + row / group;
-    u32x4 raw[DC][2];
-    uint32_t top = 0;
 #pragma unroll
     for (int cc = 0; cc < DC; ++cc)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        raw[cc][u] = *reinterpret_cast<const u32x4*>(src + 64 * cc + 8 * u);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) top = max(top, max((raw[cc][u][j] << 16) & 0x7fffffffu, raw[cc][u][j] & 0x7fff0000u));
-      }
-    top = __float_as_uint(max_quarters(__uint_as_float(top)));
-    const int up = query_exp(top);
-    const float by = ldexpf(1.0f, up);
-    qs[n] = ldexpf(scale * 1.44269504088896341f, -up);
-#pragma unroll
-    for (int cc = 0; cc < DC; ++cc)
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          qf[n][cc][u][j] = f16_pair(__uint_as_float(raw[cc][u][j] << 16) * by, __uint_as_float(raw[cc][u][j] & 0xffff0000u) * by);
+      for (int u = 0; u < 2; ++u) qf[n][cc][u] = *reinterpret_cast<const u32x4*>(src + 64 * cc + 8 * u);
   }
+
+  // ---- pages: lane i holds block base + i of the table ----
+  const int32_t* table = c.table + seq * c.width;
+  const int64_t page_bytes = (int64_t)c.heads * c.page * DIM;
+  const int64_t head_bytes = (int64_t)head * c.page * DIM;
+  const int last_block = max(end - 1, 0) >> page_log;
+  int base = begin >> page_log;                 // the blocks in hand: base .. base + 63, then the next 64
+  auto load_ids = [&](int b) { return table[min(b + lane, last_block)]; };
+  int32_t ids = load_ids(base), next_ids = load_ids(base + 64);
+  float k_scale, v_scale, v_log, v_inv;         // of the blocks in hand
+  auto load_scales = [&]() {
+    const bool real = ids >= 0 && ids < c.pages;
+    const int64_t id = (int64_t)(real ? ids : 0) * c.heads + head;
+    k_scale = c.k_scale[id];
+    v_scale = c.v_scale[id];
+    if (!(v_scale >= 0x1p-126f)) v_scale = 0.0f;
+    if (!real) v_scale = -1.0f;                 // not seen
+  };
+
+  struct Codes {
+    u32x4 k[2][DC];
+    uint32_t v[8][DB / 4];
+  };
+  auto load_codes = [&](Codes& to, int t0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      // (a run past the end reads the last block again, at rows that exist)
+      const int t = t0 + 16 * u, block = max(min(t >> page_log, last_block) - base, 0);
+      const int id = block < 64 ? __builtin_amdgcn_readlane(ids, block) : __builtin_amdgcn_readlane(next_ids, block - 64);
+      const int64_t at = (int64_t)(id >= 0 && id < c.pages ? id : 0) * page_bytes + head_bytes + (int64_t)(t & (c.page - 1)) * DIM;
+      const int8_t* kp = c.k_codes + at;
+      const int8_t* vp = c.v_codes + at;
+#pragma unroll
+      for (int cc = 0; cc < DC; ++cc) to.k[u][cc] = *reinterpret_cast<const u32x4*>(kp + (r * DIM + 16 * h) + 64 * cc);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(vp + (4 * h * DIM + DB * r) + i * DIM);
+        if constexpr (DB == 8) {
+          const u32x2 two = *reinterpret_cast<const u32x2*>(p);
+          to.v[4 * u + i][0] = two[0];
+          to.v[4 * u + i][DB / 4 - 1] = two[1];
+        } else {
+          to.v[4 * u + i][0] = *p;
+        }
+      }
+    }
+  };
 
   f32x4 out[NB][DB];                            // O^T: lane 16 h + r, block b: row r, dims DB (4 h + i) + b
   float top[NB], sum[NB];
@@ -111,133 +136,160 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
 #pragma unroll
     for (int b = 0; b < DB; ++b) out[n][b] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  int v_exp = -1000;                            // the values' scales are taken relative to 2^v_exp
+  int v_exp = kLeastExp;                        // the values' scales are taken relative to 2^v_exp
 
-  const int64_t page_bytes = (int64_t)c.heads * c.page * DIM;
-  for (int seg = begin; seg < end; seg += kSegment) {
-    // ---- the segment's pages and scales ----
-    const int seg_end = min(seg + kSegment, end);
-    const int count = ((seg_end - 1) >> page_log) - (seg >> page_log) + 1;
-    __syncthreads();
-    for (int i = threadIdx.x; i < count; i += 256) {
-      const int32_t id = c.table[seq * c.width + (seg >> page_log) + i];
-      const bool real = id >= 0 && id < c.pages;
-      const int64_t base = (int64_t)(real ? id : 0) * c.heads + head;
-      entries[i] = Entry{real ? id : -1, real ? c.k_scale[base] : 0.0f, real ? c.v_scale[base] : 0.0f};
-    }
-    __syncthreads();
-    float v_top = 0.0f;
-    for (int i = lane; i < count; i += 64) v_top = fmaxf(v_top, entries[i].v);
-    v_top = fmaxf(v_top, __shfl_xor(v_top, 1));
-    v_top = fmaxf(v_top, __shfl_xor(v_top, 2));
-    v_top = fmaxf(v_top, __shfl_xor(v_top, 4));
-    v_top = fmaxf(v_top, __shfl_xor(v_top, 8));
-    v_top = max_quarters(v_top);
-    const int seg_exp = scale_exp(v_top);
-    if (seg_exp > v_exp) {
+  auto step = [&](const Codes& x, int t0) __attribute__((always_inline)) {
+    // ---- scores S^T: lane 16 h + r, run u: row r, tokens 4 h + i ----
+    f32x4 s[NB][2];
 #pragma unroll
-      for (int n = 0; n < NB; ++n)
+    for (int u = 0; u < 2; ++u) {
 #pragma unroll
-        for (int b = 0; b < DB; ++b) out[n][b] *= ldexpf(1.0f, max(v_exp - seg_exp, -200));
-      v_exp = seg_exp;
-    }
-    const float v_by = ldexpf(1.0f, kProbExp - v_exp);
-
-    for (int t0 = seg + wave * kTile; t0 < seg_end; t0 += kStep) {
-      Entry e[2];
+      for (int n = 0; n < NB; ++n) s[n][u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int u = 0; u < 2; ++u) e[u] = entries[min(((t0 + 16 * u) >> page_log) - (seg >> page_log), count - 1)];
-      u32x4 kraw[2][DC];
-      uint32_t vraw[8][DB / 4];
+      for (int cc = 0; cc < DC; ++cc)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int64_t base = max(e[u].id, 0) * page_bytes + ((int64_t)head * c.page + ((t0 + 16 * u) & (c.page - 1))) * DIM;
+        for (int half = 0; half < 2; ++half) {
+          u32x4 a;
 #pragma unroll
-        for (int cc = 0; cc < DC; ++cc)
-          kraw[u][cc] = *reinterpret_cast<const u32x4*>(c.k_codes + base + r * DIM + 64 * cc + 16 * h);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int w = 0; w < DB / 4; ++w)
-            vraw[4 * u + i][w] = reinterpret_cast<const uint32_t*>(c.v_codes + base + (4 * h + i) * DIM + DB * r)[w] ^ 0x80808080u;
-      }
-      // ---- scores S^T: lane 16 h + r, tile u: row r, tokens 4 h + i ----
-      f32x4 s[NB][2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-#pragma unroll
-        for (int n = 0; n < NB; ++n) s[n][u] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int cc = 0; cc < DC; ++cc)
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            u32x4 a;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              uint32_t two[2];
-              f16_word(kraw[u][cc][2 * half + j], two);
-              a[2 * j] = two[0], a[2 * j + 1] = two[1];
-            }
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-              s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
-                                                              __builtin_bit_cast(f16x8, qf[n][cc][half]), s[n][u], 0, 0, 0);
+          for (int j = 0; j < 2; ++j) {
+            uint32_t two[2];
+            f16_word(x.k[u][cc][2 * half + j], two);
+            a[2 * j] = two[0], a[2 * j + 1] = two[1];
           }
-      }
-      // ---- running softmax; P^T as the second product's operand: lane 16 h + r: row r, tokens 4 h + i of both tiles ----
-      u32x4 p[NB];
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        float m = -INFINITY;
+          for (int n = 0; n < NB; ++n)
+            s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                            __builtin_bit_cast(f16x8, qf[n][cc][half]), s[n][u], 0, 0, 0);
+        }
+    }
+    float rk[2], rv[2], rlog[2], rinv[2];       // the runs' scales, the same for the whole wave
+    int tile_exp = kLeastExp;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u) {
+      const int block = min((t0 + 16 * u) >> page_log, last_block) - base;
+      rk[u] = lane_value(k_scale, block);
+      rv[u] = t0 + 16 * u < end ? lane_value(v_scale, block) : -1.0f;
+      rlog[u] = lane_value(v_log, block);
+      rinv[u] = lane_value(v_inv, block);
+      if (rv[u] > 0.0f) tile_exp = max(tile_exp, scale_exp(rv[u]));
+    }
+    const bool whole = t0 + kTile <= all_seen && rv[0] >= 0.0f && rv[1] >= 0.0f;
+    // ---- running softmax; P^T as the second product's operand: lane 16 h + r: row r, tokens 4 h + i of both runs ----
+    u32x4 p[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      float factor[2], m = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        factor[u] = rk[u] * qs[n];
+        if (!whole) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int key = t0 + 16 * u + 4 * h + i;
-            const bool seen = key < end && key <= last_key[n] && e[u].id >= 0;
-            s[n][u][i] = seen ? s[n][u][i] * (e[u].k * qs[n]) : -INFINITY;
-            m = fmaxf(m, s[n][u][i]);
+            const bool seen = key < end && key <= last_key[n] && rv[u] >= 0.0f;
+            s[n][u][i] = seen ? s[n][u][i] * factor[u] : -INFINITY;
           }
-        m = fmaxf(max_quarters(m), top[n]);
-        const float ref = m == -INFINITY ? 0.0f : m;
-        const float shrink = __builtin_amdgcn_exp2f(top[n] - ref);
-        top[n] = m;
+          factor[u] = 1.0f;
+        }
+        m = fmaxf(m, fmaxf(fmaxf(s[n][u][0], s[n][u][1]), fmaxf(s[n][u][2], s[n][u][3])) * factor[u]);
+      }
+      if (__any(m > top[n] + kLazy) || tile_exp > v_exp) {
+        const float next = fmaxf(max_quarters(m), top[n]), ref = next == -INFINITY ? 0.0f : next;
+        const float by = __builtin_amdgcn_exp2f(top[n] - ref);
+        const float scaled = ldexpf(by, v_exp - max(tile_exp, v_exp));
+        sum[n] *= by;
+#pragma unroll
+        for (int b = 0; b < DB; ++b) out[n][b] *= scaled;
+        top[n] = next;
+      }
+      const float ref = top[n] == -INFINITY ? 0.0f : top[n];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int e = max(tile_exp, v_exp);
+        const bool some = rv[u] > 0.0f;         // zeros count as a scale of 2^(e-1) with codes of zero
+        const float off = (some ? rlog[u] + (float)(kProbExp - e) : (float)(kProbExp - 1)) - ref;
         float add = 0.0f;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float by = e[u].v * v_by;
-#pragma unroll
-          for (int i = 0; i < 4; i += 2) {
-            const float a = __builtin_amdgcn_exp2f(s[n][u][i] - ref), b = __builtin_amdgcn_exp2f(s[n][u][i + 1] - ref);
-            add += a + b;
-            p[n][2 * u + i / 2] = f16_pair(a * by, b * by);
-          }
+        for (int i = 0; i < 4; i += 2) {
+          const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][u][i], factor[u], off));
+          const float b = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][u][i + 1], factor[u], off));
+          add += a + b;
+          p[n][2 * u + i / 2] = some ? f16_pair(a, b) : 0u;
         }
-        sum[n] = __builtin_fmaf(sum[n], shrink, add);
-#pragma unroll
-        for (int b = 0; b < DB; ++b) out[n][b] *= shrink;
+        sum[n] = __builtin_fmaf(add, some ? ldexpf(rinv[u], e - kProbExp) : ldexpf(1.0f, 1 - kProbExp), sum[n]);
       }
-      // ---- O^T += V^T P^T: block b's operand is byte b of the lane's eight values ----
+    }
+    v_exp = max(tile_exp, v_exp);
+    // ---- O^T += V^T P^T: block b's operand is byte b of the lane's eight values ----
+    uint32_t v[8][DB / 4];
 #pragma unroll
-      for (int b = 0; b < DB; ++b) {
-        u32x4 a;
-        const uint32_t pick = 0x0c000c00u | (4 + b % 4) << 16 | (b % 4);
+    for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) a[j] = f16_codes(__builtin_amdgcn_perm(vraw[2 * j + 1][b / 4], vraw[2 * j][b / 4], pick));
+      for (int w = 0; w < DB / 4; ++w) v[j][w] = x.v[j][w] ^ 0x80808080u;
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
-          out[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, p[n]),
-                                                            out[n][b], 0, 0, 0);
+    for (int b = 0; b < DB; ++b) {
+      u32x4 a;
+      const uint32_t pick = 0x0c000c00u | (4 + b % 4) << 16 | (b % 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a[j] = f16_codes(__builtin_amdgcn_perm(v[2 * j + 1][b / 4], v[2 * j][b / 4], pick));
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+        out[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, p[n]),
+                                                          out[n][b], 0, 0, 0);
+    }
+  };
+
+  // (the wave's first step may lie past the end: its codes are loaded all the same, from the last block)
+  Codes codes[2];
+  int t0 = begin + wave * kTile;
+  load_codes(codes[0], t0);
+  load_scales();
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int cc = 0; cc < DC; ++cc)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) most = max(most, max((qf[n][cc][u][j] << 16) & 0x7fffffffu, qf[n][cc][u][j] & 0x7fff0000u));
+    const int up = query_exp(__float_as_uint(max_quarters(__uint_as_float(most))));
+    const float by = ldexpf(scale < 0.0f ? -1.0f : 1.0f, up);      // scores are scaled by what is not negative
+    qs[n] = ldexpf(fabsf(scale) * 1.44269504088896341f, -up);
+#pragma unroll
+    for (int cc = 0; cc < DC; ++cc)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          qf[n][cc][u][j] = f16_pair(__uint_as_float(qf[n][cc][u][j] << 16) * by, __uint_as_float(qf[n][cc][u][j] & 0xffff0000u) * by);
+  }
+  v_log = __log2f(v_scale);
+  v_inv = 1.0f / v_scale;
+  while (t0 < end) {
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      load_codes(codes[d ^ 1], t0 + kStep);
+      step(codes[d], t0);
+      t0 += kStep;
+      if (t0 >= end) break;
+      if ((t0 >> page_log) - base >= 64) {      // the next 64 blocks
+        base += 64;
+        ids = next_ids;
+        next_ids = load_ids(base + 64);
+        load_scales();
+        v_log = __log2f(v_scale);
+        v_inv = 1.0f / v_scale;
       }
     }
   }
 
   // ---- the waves' parts meet ----
-  const float back = v_exp < -500 ? 0.0f : ldexpf(1.0f, v_exp - kProbExp);
+  const float back = ldexpf(1.0f, v_exp - kProbExp);
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
     const float total = sum_quarters(sum[n]);
-    __syncthreads();
+    if (n) __syncthreads();
     if (h == 0) {
       red_max[wave][r] = top[n];
       red_sum[wave][r] = total;
@@ -273,10 +325,8 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
         *reinterpret_cast<u32x2*>(dst + b) = u32x2{bf16x2_rne(o[b] * inv, o[b + 1] * inv), bf16x2_rne(o[b + 2] * inv, o[b + 3] * inv)};
     } else {
       const int64_t index = ((seq * c.heads + head) * rows + row) * splits + split;
-      if (m != -INFINITY) {
 #pragma unroll
-        for (int b = 0; b < DB; b += 4) *reinterpret_cast<f32x4*>(part.out + index * DIM + d0 + b) = f32x4{o[b], o[b + 1], o[b + 2], o[b + 3]};
-      }
+      for (int b = 0; b < DB; b += 4) *reinterpret_cast<f32x4*>(part.out + index * DIM + d0 + b) = f32x4{o[b], o[b + 1], o[b + 2], o[b + 3]};
       if (h == 0 && wave == 0) {
         part.stat[2 * index] = m;
         part.stat[2 * index + 1] = l;
@@ -285,40 +335,47 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
   }
 }
 
-// The pieces of a row meet: one workgroup per row, four dims a thread, the pieces dealt to the DIM / 4 lanes'
-// groups.  Latency bound (two dependent loads and a sum in LDS): for 128 pieces of 32 rows 3 us, where one wave
-// per row that walked the pieces took 70 us.
-template <int DIM>
+// The pieces of a row meet, four dims a thread.  Many pieces of few rows: a workgroup a row (WIDE), the pieces dealt to
+// its threads and summed in LDS; latency bound, two dependent loads and the sum.  Few pieces of many rows: a thread
+// adds all pieces of its dims, 256 / (DIM / 4) rows a workgroup; bound by the partial results' bytes.
+template <int DIM, bool WIDE>
 __global__ void __launch_bounds__(256)
-kv_combine_kernel(int rows, int heads, int group, int splits, uint16_t* __restrict__ y, Partial part) {
+kv_combine_kernel(int64_t all, int rows, int heads, int group, int splits, uint16_t* __restrict__ y, Partial part) {
   constexpr int COLS = DIM / 4, PARTS = 256 / COLS;
   __shared__ f32x4 red_out[PARTS][COLS];
   __shared__ float red_sum[PARTS];
-  const int64_t index = blockIdx.x;
   const int col = threadIdx.x % COLS, mine = threadIdx.x / COLS;
+  const int64_t index = WIDE ? blockIdx.x : (int64_t)blockIdx.x * PARTS + mine;
+  if (index >= all) return;
   const float* stat = part.stat + 2 * index * splits;
+  const float* out = part.out + index * splits * DIM + 4 * col;
   float m = -INFINITY;
-  for (int s = threadIdx.x & 63; s < splits; s += 64) m = fmaxf(m, stat[2 * s]);
+  if constexpr (WIDE) {
+    for (int s = threadIdx.x & 63; s < splits; s += 64) m = fmaxf(m, stat[2 * s]);
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+  } else {
+    for (int s = 0; s < splits; ++s) m = fmaxf(m, stat[2 * s]);
+  }
   const float ref = m == -INFINITY ? 0.0f : m;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
   float l = 0.0f;
-  for (int s = mine; s < splits; s += PARTS) {
-    const float ms = stat[2 * s];
-    if (ms == -INFINITY) continue;             // a piece without a key has written no outputs
-    const float by = __builtin_amdgcn_exp2f(ms - ref);
+#pragma unroll 4
+  for (int s = WIDE ? mine : 0; s < splits; s += WIDE ? PARTS : 1) {    // (a piece without a key: outputs and sum of zero)
+    const float by = __builtin_amdgcn_exp2f(stat[2 * s] - ref);
     l = __builtin_fmaf(by, stat[2 * s + 1], l);
-    o += *reinterpret_cast<const f32x4*>(part.out + (index * splits + s) * DIM + 4 * col) * by;
+    o += *reinterpret_cast<const f32x4*>(out + (int64_t)s * DIM) * by;
   }
-  red_out[mine][col] = o;
-  if (col == 0) red_sum[mine] = l;
-  __syncthreads();
-  if (mine) return;
+  if constexpr (WIDE) {
+    red_out[mine][col] = o;
+    if (col == 0) red_sum[mine] = l;
+    __syncthreads();
+    if (mine) return;
 #pragma unroll
-  for (int g = 1; g < PARTS; ++g) {
-    o += red_out[g][col];
-    l += red_sum[g];
+    for (int g = 1; g < PARTS; ++g) {
+      o += red_out[g][col];
+      l += red_sum[g];
+    }
   }
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
   const int64_t row = index % rows, seq = index / rows / heads, head = index / rows % heads;
@@ -351,8 +408,11 @@ hipError_t launch_all(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t 
   else if (blocks_of(rows) == 2) e = launch<DIM, 2>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
   else e = launch<DIM, 4>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
   if (e != hipSuccess || splits == 1) return e;
-  hipLaunchKernelGGL((kv_combine_kernel<DIM>), dim3((unsigned)all), dim3(256), 0, stream, (int)rows, c.heads, group, (int)splits,
-                     y, part);
+  // a workgroup a row while those fit the GPU's 256 CUs a few times over
+  const bool wide = all <= 2048;
+  const int64_t blocks = wide ? all : (all + 1024 / DIM - 1) / (1024 / DIM);
+  const auto kernel = wide ? kv_combine_kernel<DIM, true> : kv_combine_kernel<DIM, false>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, stream, all, (int)rows, c.heads, group, (int)splits, y, part);
   return hipGetLastError();
 }
 
@@ -373,9 +433,12 @@ int64_t kv_attention_splits(int64_t seqs, int64_t tokens, int q_heads, int heads
     }
     return best;
   }
-  // workgroups enough for four on each of the 256 CUs, but no piece of a full table below one step
-  const int64_t tile = 16 * blocks_of(rows), one = seqs * heads * ((rows + tile - 1) / tile);
-  return std::max<int64_t>(1, std::min<int64_t>((1024 + one - 1) / one, most));
+  // a workgroup for each of the 256 CUs (32 sequences up to 2,270 tokens: 25.3 us, with twice as many 27.2 us, with
+  // four times 29.7 us; one of 131,072: 52.9, 55.5 and 59.0 us), but one piece alone up to 512 tokens of a full table (a
+  // step of 128 takes less than the combination's 3 us) and no piece below 256
+  const int64_t tile = 16 * blocks_of(rows), one = seqs * heads * ((rows + tile - 1) / tile), most_tokens = width * page;
+  if (most_tokens <= 512) return 1;
+  return std::max<int64_t>(1, std::min<int64_t>((256 + one - 1) / one, most_tokens / 256));
 }
 
 hipError_t launch_kv_attention(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs, int64_t tokens,

@@ -15,6 +15,9 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
+constexpr float kLazy = 8.0f;                   // log2 of how far scores may pass the running maximum
+constexpr int kProbExp = 7;                     // p' < 2^(kLazy + kProbExp); f16 ends at 2^16
+constexpr int kLeastExp = -112;                 // scales are taken relative to 2^e with at least this e
 constexpr int kPiece = 128;                     // pieces of a sequence are whole multiples of this
 
 // Tokens of each of the `splits` pieces of a sequence.
@@ -43,8 +46,31 @@ __device__ __forceinline__ void f16_word(uint32_t word, uint32_t* two) {
 // The power of two that brings a row of queries whose largest magnitude has these bits into [2^7, 2^8).
 __device__ __forceinline__ int query_exp(uint32_t top_bits) { return min(134 - (int)(top_bits >> 23), 126); }
 
-// The least e (at least -112) with s < 2^e, for a scale s >= 0.
-__device__ __forceinline__ int scale_exp(float s) { return max((int)(__float_as_uint(s) >> 23) - 126, -112); }
+// The least e (at least kLeastExp) with s < 2^e, for a scale s >= 0.
+__device__ __forceinline__ int scale_exp(float s) { return max((int)(__float_as_uint(s) >> 23) - 126, kLeastExp); }
+
+// The larger (sum) of lanes l and l ^ 32; of lanes l, l ^ 16, l ^ 32 and l ^ 48.  The swaps exchange the odd rows
+// of 16 (the upper half) of one copy with the even rows (the lower half) of the other.
+__device__ __forceinline__ float max_halves(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+__device__ __forceinline__ float sum_halves(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+__device__ __forceinline__ float max_quarters(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto s = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return max_halves(fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1])));
+}
+__device__ __forceinline__ float sum_quarters(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto s = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return sum_halves(__uint_as_float(s[0]) + __uint_as_float(s[1]));
+}
 
 // Partial results of a row's pieces, for each row and piece: unnormalised outputs [dim], and maximum and sum.
 struct Partial {

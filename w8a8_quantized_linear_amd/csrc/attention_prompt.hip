@@ -10,10 +10,6 @@
 //   block in register i, which is the second operand of O^T += V^T P^T as it stands, if the tokens of a
 //   16-token step are taken in the order 4 h + j, 8 + 4 h + j (j < 4) for each half h: the order in which
 //   the values are written to LDS.
-// The values' scale goes into the exponent, p' = 2^(s - max + log2(scale) - e), so it costs nothing per element;
-// the sum of p' over a page is divided by the scale again.  A page whose values have scale zero (or subnormal: taken
-// for zero) counts as one of scale 2^(e-1) with codes of zero.  The running maximum moves only when a row's score passes it by more than
-// 2^8 (the probabilities stay below 2^15), which spares most tiles the rescaling of the outputs.
 #include "attention_math.h"
 
 namespace w8a8 {
@@ -24,8 +20,6 @@ constexpr int kTile = 64;                       // tokens
 constexpr int kSubs = kTile / 16;               // 16-token runs: no page boundary falls inside one
 constexpr int kWaves = kPromptRows / 32;
 constexpr int kThreads = 64 * kWaves;
-constexpr float kLazy = 8.0f;                   // log2 of how far scores may pass the running maximum
-constexpr int kProbExp = 7;                     // p' < 2^(kLazy + kProbExp), f16 ends at 2^16
 
 struct Run {
   float k;           // the keys' scale
@@ -33,9 +27,6 @@ struct Run {
   float v_log;       // log2 of it
   float v_inv;       // 1 / it
 };
-
-// The larger of lanes l and l ^ 32.
-__device__ __forceinline__ float max_halves(float v) { return fmaxf(v, __shfl_xor(v, 32)); }
 
 template <int DIM>
 __global__ void __launch_bounds__(kThreads)
@@ -172,7 +163,7 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
 #pragma unroll
     for (int i = 0; i < 16; ++i) out[b][i] = 0.0f;
   float top = -INFINITY, sum = 0.0f;
-  int v_exp = -112;
+  int v_exp = kLeastExp;
 
   if (begin < end) {
     load_ids(begin);
@@ -203,13 +194,13 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
       Run run[kSubs];
       float factor[kSubs];
       bool whole = t0 + kTile <= all_seen;
-      int tile_exp = -112;
+      int tile_exp = kLeastExp;
 #pragma unroll
       for (int u = 0; u < kSubs; ++u) {
         run[u] = runs[buf][u];
         factor[u] = run[u].k * qs;
         whole = whole && run[u].v >= 0.0f;
-        tile_exp = max(tile_exp, run[u].v > 0.0f ? scale_exp(run[u].v) : -112);
+        tile_exp = max(tile_exp, run[u].v > 0.0f ? scale_exp(run[u].v) : kLeastExp);
       }
       if (!__builtin_amdgcn_readfirstlane(whole)) {             // some row does not see some token
 #pragma unroll
@@ -231,10 +222,9 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
         for (int i = 1; i < 8; ++i) mu = fmaxf(mu, s[u / 2][8 * (u % 2) + i]);
         m = fmaxf(m, mu * factor[u]);
       }
-      m = max_halves(m);
       tile_exp = __builtin_amdgcn_readfirstlane(tile_exp);
       if (__any(m > top + kLazy) || tile_exp > v_exp) {
-        const float next = fmaxf(m, top), ref = next == -INFINITY ? 0.0f : next;
+        const float next = fmaxf(max_halves(m), top), ref = next == -INFINITY ? 0.0f : next;
         const int exp = max(tile_exp, v_exp);
         const float by = __builtin_amdgcn_exp2f(top - ref);
         sum *= by;
@@ -276,7 +266,7 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
   }
 
   // ---- outputs: register i of block b is dim 32 b + 8 (i / 4) + 4 h + i % 4 ----
-  sum += __shfl_xor(sum, 32);
+  sum = sum_halves(sum);
   if (row0 + r >= rows) return;
   const float back = ldexpf(1.0f, v_exp - kProbExp);
   const float by = splits == 1 ? (sum > 0.0f ? back / sum : 0.0f) : back;
@@ -290,7 +280,7 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
       const f32x4 o = {out[b][i] * by, out[b][i + 1] * by, out[b][i + 2] * by, out[b][i + 3] * by};
       if (splits == 1)
         *reinterpret_cast<u32x2*>(dst + d) = u32x2{bf16x2_rne(o[0], o[1]), bf16x2_rne(o[2], o[3])};
-      else if (top != -INFINITY)
+      else
         *reinterpret_cast<f32x4*>(part.out + index * DIM + d) = o;
     }
   if (splits > 1 && h == 0) {
