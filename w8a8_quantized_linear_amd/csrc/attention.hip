@@ -229,9 +229,8 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
 #pragma unroll
     for (int b = 0; b < DB; ++b) {
       u32x4 a;
-      const uint32_t pick = 0x0c000c00u | (4 + b % 4) << 16 | (b % 4);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) a[j] = f16_codes(__builtin_amdgcn_perm(v[2 * j + 1][b / 4], v[2 * j][b / 4], pick));
+      for (int j = 0; j < 4; ++j) a[j] = f16_bytes(v[2 * j + 1][b / 4], v[2 * j][b / 4], b % 4);
 #pragma unroll
       for (int n = 0; n < NB; ++n)
         out[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, p[n]),

@@ -25,10 +25,10 @@ __host__ __device__ __forceinline__ int piece_of(int held, int splits) {
   return ((held + splits - 1) / splits + kPiece - 1) / kPiece * kPiece;
 }
 
-// Two bytes holding code + 128 in the low bytes of 16-bit halves -> two f16 codes: with 0x64 above it a byte u
-// is the f16 1024 + u, and 1152 less is the code, exactly.
-__device__ __forceinline__ uint32_t f16_codes(uint32_t halves) {
-  const f16x2 v = __builtin_bit_cast(f16x2, halves | 0x64006400u) - f16x2{(_Float16)1152.0f, (_Float16)1152.0f};
+// Two f16 values 1024 + u -> u - 128, exactly: with 0x64 above it a byte u is the f16 1024 + u, and a code with its
+// top bit flipped is u = code + 128.
+__device__ __forceinline__ uint32_t f16_codes(uint32_t biased) {
+  const f16x2 v = __builtin_bit_cast(f16x2, biased) - f16x2{(_Float16)1152.0f, (_Float16)1152.0f};
   return __builtin_bit_cast(uint32_t, v);
 }
 
@@ -39,8 +39,13 @@ __device__ __forceinline__ uint32_t f16_pair(float a, float b) {
 // Four codes in memory order -> f16, two per word.
 __device__ __forceinline__ void f16_word(uint32_t word, uint32_t* two) {
   word ^= 0x80808080u;
-  two[0] = f16_codes(__builtin_amdgcn_perm(0, word, 0x0c010c00u));
-  two[1] = f16_codes(__builtin_amdgcn_perm(0, word, 0x0c030c02u));
+  two[0] = f16_codes(__builtin_amdgcn_perm(0x64646464u, word, 0x04010400u));
+  two[1] = f16_codes(__builtin_amdgcn_perm(0x64646464u, word, 0x04030402u));
+}
+
+// Byte b of two words with their codes' top bits flipped -> f16.
+__device__ __forceinline__ uint32_t f16_bytes(uint32_t hi, uint32_t lo, int b) {
+  return f16_codes(__builtin_amdgcn_perm(hi, lo, 0x0c000c00u | (4 + b) << 16 | b) | 0x64006400u);
 }
 
 // The power of two that brings a row of queries whose largest magnitude has these bits into [2^7, 2^8).

@@ -35,7 +35,7 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
   constexpr int KS = DIM / 16;                  // MFMA steps of a key
   constexpr int DB = DIM / 32;                  // output blocks
   constexpr int KCH = DIM / 8;                  // 16-byte chunks of an f16 key row
-  constexpr int KP = kTile * DIM / 16 / 256;    // 16-byte pieces of codes per thread of the keys' half
+  constexpr int KP = kTile * DIM / 16 / 256;    // 16-byte pieces of codes per lane of the keys' waves
   __shared__ __attribute__((aligned(16))) u32x4 k_lds[2][kTile * KCH];
   __shared__ __attribute__((aligned(16))) u32x4 v_lds[2][DIM * (kTile / 8)];
   __shared__ Run runs[2][kSubs];
@@ -84,46 +84,53 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
         qf[s][j] = f16_pair(__uint_as_float(qf[s][j] << 16) * by, __uint_as_float(qf[s][j] & 0xffff0000u) * by);
   }
 
-  // ---- staging: waves 0 .. 3 the values, 4 .. 7 the keys ----
+  // ---- staging: waves 0 .. 3 bring the values of a run of 16 tokens each, 4 .. 7 the keys of KP runs ----
   const bool keys = wave >= 4;
-  const int st = tid & 255;
-  const int v_quad = st % (DIM / 4), v_half = st / (DIM / 4) % 2, v_sub = st / (DIM / 2);      // v_sub >= kSubs: none
+  const int stage = wave & 3;
+  const int v_quad = lane % (DIM / 4), v_half = lane / (DIM / 4);       // (dim 64: lanes 32 .. 63 have none)
   const int64_t head_base = (int64_t)head * c.page * DIM;
   const int64_t page_bytes = (int64_t)c.heads * c.page * DIM;
   const int32_t* table = c.table + seq * c.width;
-  int32_t ids[2];                               // pages of the next tile's runs that this thread stages
+  constexpr int KL = DIM / 16;                  // lanes of a key: 16 codes each
+  const int k_row = lane / KL, k_piece = lane % KL;
+  // dim 128: a wave's instruction brings 8 keys, so waves 4, 5 share runs 0 and 2, waves 6, 7 runs 1 and 3; dim 64: a
+  // run each
+  const int k_token = DIM == 128 ? 8 * (stage & 1) + k_row : k_row;
+  auto run_of = [&](int i) { return !keys ? stage : DIM == 128 ? stage / 2 + 2 * i : stage; };
+  const int lane_bytes = keys ? k_token * DIM + 16 * k_piece : (4 * v_half) * DIM + 4 * v_quad;
+  int ids[KP];                                  // pages of the next tile's runs that this wave stages
   u32x4 raw[2];                                 // its codes
-  float run_scale[2];
-  // the run of 16 tokens behind piece i of this thread
-  auto sub_of = [&](int i) { return keys ? (i * 256 + st) / (DIM / 16) / 16 : min(v_sub, kSubs - 1); };
-  auto load_ids = [&](int t0) {
+  float run_scale[KP];
+  auto load_ids = [&](int t0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < KP; ++i) ids[i] = table[min((t0 + 16 * sub_of(i)) >> page_log, (int)c.width - 1)];
+    for (int i = 0; i < KP; ++i) ids[i] = table[min((t0 + 16 * run_of(i)) >> page_log, (int)c.width - 1)];
   };
-  auto load_codes = [&](int t0) {
+  auto load_codes = [&](int t0) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < KP; ++i) {
-      const int t = t0 + 16 * sub_of(i);
-      const bool real = ids[i] >= 0 && ids[i] < c.pages && t < end;
-      const int64_t id = real ? ids[i] : 0;
+      const int t = t0 + 16 * run_of(i), named = __builtin_amdgcn_readfirstlane(ids[i]);
+      const bool real = named >= 0 && named < c.pages && t < end;
+      const int64_t id = real ? named : 0;
       const int64_t base = id * page_bytes + head_base + (int64_t)(t & (c.page - 1)) * DIM;
       if (keys) {
-        const int p = i * 256 + st;
-        raw[i] = *reinterpret_cast<const u32x4*>(c.k_codes + base + (p / (DIM / 16) % 16) * DIM + p % (DIM / 16) * 16);
+        raw[i] = *reinterpret_cast<const u32x4*>(c.k_codes + base + lane_bytes);
         run_scale[i] = real ? c.k_scale[id * c.heads + head] : 0.0f;
       } else if (i == 0) {
+        const int8_t* from = c.v_codes + base;
+        if (v_half < 2) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          raw[j / 4][j % 4] = *reinterpret_cast<const uint32_t*>(c.v_codes + base + (4 * v_half + j % 4 + 8 * (j / 4)) * DIM + 4 * v_quad);
+          for (int j = 0; j < 8; ++j)
+            raw[j / 4][j % 4] = *reinterpret_cast<const uint32_t*>(from + lane_bytes + (j % 4 + 8 * (j / 4)) * DIM);
+        }
         run_scale[0] = real ? c.v_scale[id * c.heads + head] : -1.0f;
       }
     }
   };
-  auto store = [&](int buf) {
+  auto store = [&](int buf) __attribute__((always_inline)) {
     if (keys) {
 #pragma unroll
       for (int i = 0; i < KP; ++i) {
-        const int p = i * 256 + st, t = p / (DIM / 16), ch = 2 * (p % (DIM / 16));
+        const int t = 16 * run_of(i) + k_token, ch = 2 * k_piece;
         u32x4 lo, hi;
         uint32_t two[2];
 #pragma unroll
@@ -134,25 +141,25 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
         }
         k_lds[buf][t * KCH + (ch ^ (t & (KCH - 1)))] = lo;
         k_lds[buf][t * KCH + ((ch + 1) ^ (t & (KCH - 1)))] = hi;
-        if (p % (DIM / 16) == 0 && t % 16 == 0) runs[buf][t / 16].k = run_scale[i];
+        if (t % 16 == 0 && k_piece == 0) runs[buf][t / 16].k = run_scale[i];
       }
-    } else if (v_sub < kSubs) {
-      const int ch = 2 * v_sub + v_half;
+    } else if (v_half < 2) {
+      const int ch = 2 * stage + v_half;
       const bool zeros = !(run_scale[0] >= 0x1p-126f);
 #pragma unroll
+      for (int j = 0; j < 8; ++j) raw[j / 4][j % 4] ^= 0x80808080u;
+#pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const uint32_t pick = 0x0c000c00u | (4 + b) << 16 | b;
         u32x4 a;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          a[j] = f16_codes(__builtin_amdgcn_perm(raw[j / 2][2 * (j % 2) + 1] ^ 0x80808080u, raw[j / 2][2 * (j % 2)] ^ 0x80808080u, pick));
+        for (int j = 0; j < 4; ++j) a[j] = f16_bytes(raw[j / 2][2 * (j % 2) + 1], raw[j / 2][2 * (j % 2)], b);
         const int d = 4 * v_quad + b;
         v_lds[buf][d * (kTile / 8) + (ch ^ ((d ^ (d >> 2)) & 7))] = zeros ? u32x4{0, 0, 0, 0} : a;
       }
-      if (v_quad == 0 && v_half == 0) {
-        runs[buf][v_sub].v = zeros && run_scale[0] != -1.0f ? 0.0f : run_scale[0];
-        runs[buf][v_sub].v_log = __log2f(run_scale[0]);
-        runs[buf][v_sub].v_inv = 1.0f / run_scale[0];
+      if (lane == 0) {
+        runs[buf][stage].v = zeros && run_scale[0] != -1.0f ? 0.0f : run_scale[0];
+        runs[buf][stage].v_log = __log2f(run_scale[0]);
+        runs[buf][stage].v_inv = 1.0f / run_scale[0];
       }
     }
   };
@@ -165,18 +172,27 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
   float top = -INFINITY, sum = 0.0f;
   int v_exp = kLeastExp;
 
+  // The keys' waves convert the next tile before they multiply, the values' waves after it (their codes are loaded
+  // an iteration later), so that the two waves of a SIMD are out of step: one's products run under the other's softmax
+  // and conversions.  In step, a tile of 256 rows took the sum of both, ~6,000 cycles at dim 128.
   if (begin < end) {
     load_ids(begin);
     load_codes(begin);
     load_ids(begin + kTile);
     store(0);
+    if (keys) {
+      load_codes(begin + kTile);
+      load_ids(begin + 2 * kTile);
+    }
     __syncthreads();
   }
   for (int t0 = begin, buf = 0; t0 < end; t0 += kTile, buf ^= 1) {
     const bool more = t0 + kTile < end;
     if (more) {
-      load_codes(t0 + kTile);
-      load_ids(t0 + 2 * kTile);
+      if (keys) store(buf ^ 1);
+      const int next = keys ? t0 + 2 * kTile : t0 + kTile;
+      load_codes(next);
+      load_ids(next + kTile);
     }
     if (t0 < wave_end) {
       f32x16 s[2];
@@ -261,7 +277,7 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
           out[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, p[u]), out[b], 0, 0, 0);
         }
     }
-    if (more) store(buf ^ 1);
+    if (more && !keys) store(buf ^ 1);
     __syncthreads();
   }
 
