@@ -195,9 +195,8 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
       }
       if (__any(m > top[n] + kLazy) || tile_exp > v_exp) {
         const float next = fmaxf(max_quarters(m), top[n]), ref = next == -INFINITY ? 0.0f : next;
-        const float by = __builtin_amdgcn_exp2f(top[n] - ref);
-        const float scaled = ldexpf(by, v_exp - max(tile_exp, v_exp));
-        sum[n] *= by;
+        const float scaled = ldexpf(__builtin_amdgcn_exp2f(top[n] - ref), v_exp - max(tile_exp, v_exp));
+        sum[n] *= scaled;
 #pragma unroll
         for (int b = 0; b < DB; ++b) out[n][b] *= scaled;
         top[n] = next;
@@ -216,21 +215,16 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
           add += a + b;
           p[n][2 * u + i / 2] = some ? f16_pair(a, b) : 0u;
         }
-        sum[n] = __builtin_fmaf(add, some ? ldexpf(rinv[u], e - kProbExp) : ldexpf(1.0f, 1 - kProbExp), sum[n]);
+        sum[n] = __builtin_fmaf(add, some ? rinv[u] : ldexpf(1.0f, 1 - e), sum[n]);
       }
     }
     v_exp = max(tile_exp, v_exp);
     // ---- O^T += V^T P^T: block b's operand is byte b of the lane's eight values ----
-    uint32_t v[8][DB / 4];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int w = 0; w < DB / 4; ++w) v[j][w] = x.v[j][w] ^ 0x80808080u;
 #pragma unroll
     for (int b = 0; b < DB; ++b) {
       u32x4 a;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) a[j] = f16_bytes(v[2 * j + 1][b / 4], v[2 * j][b / 4], b % 4);
+      for (int j = 0; j < 4; ++j) a[j] = f16_bytes(x.v[2 * j + 1][b / 4], x.v[2 * j][b / 4], b % 4);
 #pragma unroll
       for (int n = 0; n < NB; ++n)
         out[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, p[n]),
@@ -287,7 +281,7 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
   const float back = ldexpf(1.0f, v_exp - kProbExp);
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
-    const float total = sum_quarters(sum[n]);
+    const float total = sum_quarters(sum[n]) * back;
     if (n) __syncthreads();
     if (h == 0) {
       red_max[wave][r] = top[n];
@@ -421,9 +415,9 @@ int64_t kv_attention_splits(int64_t seqs, int64_t tokens, int q_heads, int heads
   const int64_t rows = tokens * (q_heads / heads);
   const int64_t most = (width * page + kPiece - 1) / kPiece;
   if (prompt_rows(rows)) {
-    // one workgroup fits a CU: the cut that leaves the fewest rounds of 256, a piece more costing a twentieth
+    // 256 rows fit a CU: the cut that leaves the fewest rounds of 256, a piece more costing a twentieth
     // (its partial results pass through memory)
-    const int64_t one = seqs * heads * ((rows + kPromptRows - 1) / kPromptRows);
+    const int64_t tile = prompt_rows_of(width * page), one = (seqs * heads * ((rows + tile - 1) / tile) * tile + 255) / 256;
     int64_t best = 1;
     double least = 0.0;
     for (int64_t s = 1; s <= std::min<int64_t>(8, most); ++s) {

@@ -17,7 +17,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr float kLazy = 8.0f;                   // log2 of how far scores may pass the running maximum
 constexpr int kProbExp = 7;                     // p' < 2^(kLazy + kProbExp); f16 ends at 2^16
-constexpr int kLeastExp = -112;                 // scales are taken relative to 2^e with at least this e
+constexpr int kLeastExp = -80;                  // scales are taken relative to 2^e with at least this e
 constexpr int kPiece = 128;                     // pieces of a sequence are whole multiples of this
 
 // Tokens of each of the `splits` pieces of a sequence.
@@ -43,9 +43,9 @@ __device__ __forceinline__ void f16_word(uint32_t word, uint32_t* two) {
   two[1] = f16_codes(__builtin_amdgcn_perm(0x64646464u, word, 0x04030402u));
 }
 
-// Byte b of two words with their codes' top bits flipped -> f16.
+// Byte b of two words -> f16.
 __device__ __forceinline__ uint32_t f16_bytes(uint32_t hi, uint32_t lo, int b) {
-  return f16_codes(__builtin_amdgcn_perm(hi, lo, 0x0c000c00u | (4 + b) << 16 | b) | 0x64006400u);
+  return f16_codes(__builtin_amdgcn_perm(hi, lo, 0x0c000c00u | (4 + b) << 16 | b) ^ 0x64806480u);
 }
 
 // The power of two that brings a row of queries whose largest magnitude has these bits into [2^7, 2^8).
@@ -83,8 +83,10 @@ struct Partial {
   float* stat;
 };
 
-// Prompt form (attention_prompt.hip): 256 query rows a workgroup.
-constexpr int kPromptRows = 256;
+// Prompt form (attention_prompt.hip): query rows of a workgroup, by the longest sequence that the table can hold.  2 x 84
+// tokens (12/4 heads of 128): 10.5 us with 128 rows, 14.5 us with 256; 636 tokens (16/2 of 64) 18.0 and 20.0 us; 4 x 1,502
+// (40/8 of 128) 148 and 146 us; 500 behind 12,016 (32/8) 141 and 130 us.
+inline int prompt_rows_of(int64_t length) { return length <= 1024 ? 128 : 256; }
 template <int DIM>
 hipError_t launch_prompt(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs, int64_t tokens, int group,
                          float scale, int64_t splits, uint16_t* y, Partial part, hipStream_t stream);

@@ -1,15 +1,15 @@
 // Attention over the paged 8-bit cache for many query rows: prompts and pieces of prompts.
 //
-// The mathematics is that of attention.hip.  Here the products bound the time, not the cache's bytes, so a
-// workgroup turns each 64 tokens of codes into f16 once, in LDS, for 256 query rows (8 waves of 32): keys
-// [token][dim], values transposed [dim][token].  Per wave and tile the matrix core needs 1,024 cycles
-// (dim 128), the softmax of 64 x 32 scores about 900 vector cycles, the conversions 200, and the operands'
-// reads from LDS a quarter of the CU's 1,024: two waves on each SIMD overlap one's products with the other's
-// softmax.
-//   S^T = K Q^T  (MFMA 32x32x16 f16): lane 32 h + r holds row r, tokens 8 (i / 4) + 4 h + i % 4 of a 32-token
-//   block in register i, which is the second operand of O^T += V^T P^T as it stands, if the tokens of a
-//   16-token step are taken in the order 4 h + j, 8 + 4 h + j (j < 4) for each half h: the order in which
-//   the values are written to LDS.
+// The mathematics is that of attention.hip.  Here the arithmetic bounds the time, not the cache's bytes, so a
+// workgroup turns each tile of 64 tokens of codes into f16 once, in LDS, for all its query rows (32 a wave): keys
+// [token][dim], values transposed [dim][token].  MFMA 32x32x16 f16:
+//   S^T = K Q^T: lane 32 h + r holds row r, tokens 8 (i / 4) + 4 h + i % 4 of a 32-token block in register i, which is the
+//   second operand of O^T += V^T P^T as it stands, if the tokens of a 16-token step are taken in the order
+//   4 h + j, 8 + 4 h + j (j < 4) for each half h: the order in which the values are written to LDS.
+// Per wave and tile (dim 128) the matrix core needs 1,024 cycles, the vector unit about 900 and the exponentials 530.
+// The units overlap only in part (two waves of a SIMD, one with products and one with multiply-adds, together take
+// 0.71 of the sum of their times; products and exponentials overlap fully, measured), so ~1,500 is what a tile
+// could take; it takes 2,800: two waves a SIMD leave waits for LDS, for the products and at the barrier.
 #include "attention_math.h"
 
 namespace w8a8 {
@@ -18,24 +18,27 @@ namespace {
 
 constexpr int kTile = 64;                       // tokens
 constexpr int kSubs = kTile / 16;               // 16-token runs: no page boundary falls inside one
-constexpr int kWaves = kPromptRows / 32;
-constexpr int kThreads = 64 * kWaves;
 
 struct Run {
   float k;           // the keys' scale
-  float v;           // the values' scale, 0 where they are all zeros, -1 where the table names no page
-  float v_log;       // log2 of it
+  float v_log;       // log2 of the values' scale
   float v_inv;       // 1 / it
+  int v_exp;         // scale_exp of it; kZeros: the values are all zeros, kNone: the table names no page
 };
+constexpr int kZeros = -500, kNone = -1000;
 
-template <int DIM>
-__global__ void __launch_bounds__(kThreads)
+// WAVES = 8: 256 rows, waves 0 .. 3 bring the values of a run of 16 tokens each and waves 4 .. 7 the keys.  WAVES = 4: 128
+// rows, two workgroups a CU, each wave brings the keys and values of a run: twice the conversions for every row,
+// but less to wait for where there are few tiles.
+template <int DIM, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, 2)
 kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tokens, int group, float scale, int splits,
                  int row_tiles, int total, uint16_t* __restrict__ y, Partial part) {
   constexpr int KS = DIM / 16;                  // MFMA steps of a key
   constexpr int DB = DIM / 32;                  // output blocks
   constexpr int KCH = DIM / 8;                  // 16-byte chunks of an f16 key row
-  constexpr int KP = kTile * DIM / 16 / 256;    // 16-byte pieces of codes per lane of the keys' waves
+  constexpr int KP = kTile * DIM / 16 / 256;    // 16-byte pieces of codes per lane that brings keys
+  constexpr int ROWS = 32 * WAVES;
   __shared__ __attribute__((aligned(16))) u32x4 k_lds[2][kTile * KCH];
   __shared__ __attribute__((aligned(16))) u32x4 v_lds[2][DIM * (kTile / 8)];
   __shared__ Run runs[2][kSubs];
@@ -51,10 +54,10 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
   at /= row_tiles;
   const int head = at % c.heads, page_log = __builtin_ctz(c.page);
   const int64_t seq = at / c.heads;
-  const int rows = tokens * group, row0 = tile * kPromptRows + 32 * wave;
+  const int rows = tokens * group, row0 = tile * ROWS + 32 * wave;
   const int len = max(c.lens[seq], 0), held = min(len, (int)c.width << page_log), piece = piece_of(held, splits);
   const int first_pos = len - tokens;
-  const int tile_last = min((tile + 1) * kPromptRows, rows) - 1;
+  const int tile_last = min((tile + 1) * ROWS, rows) - 1;
   const int begin = min(split * piece, held), end = min(min(begin + piece, held), first_pos + tile_last / group + 1);
   const int row = min(row0 + r, rows - 1), last_key = first_pos + row / group;
   // this wave's keys: none if it has no rows; every row sees those before `all_seen`
@@ -84,23 +87,25 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
         qf[s][j] = f16_pair(__uint_as_float(qf[s][j] << 16) * by, __uint_as_float(qf[s][j] & 0xffff0000u) * by);
   }
 
-  // ---- staging: waves 0 .. 3 bring the values of a run of 16 tokens each, 4 .. 7 the keys of KP runs ----
-  const bool keys = wave >= 4;
+  // ---- staging ----
+  const bool keys = WAVES == 4 || wave >= 4, values = wave < 4;         // what this wave brings
   const int stage = wave & 3;
-  const int v_quad = lane % (DIM / 4), v_half = lane / (DIM / 4);       // (dim 64: lanes 32 .. 63 have none)
+  const int v_quad = lane % (DIM / 4), v_half = lane / (DIM / 4);       // (dim 64: lanes 32 .. 63 have no values)
   const int64_t head_base = (int64_t)head * c.page * DIM;
   const int64_t page_bytes = (int64_t)c.heads * c.page * DIM;
   const int32_t* table = c.table + seq * c.width;
-  constexpr int KL = DIM / 16;                  // lanes of a key: 16 codes each
+  // An instruction brings 64 / KL keys, KL lanes of 16 codes each.  The run and the first token in it of piece i:
+  // a wave's own run where it brings values too or a piece is a run, else (8 waves, dim 128: 8 keys) waves 4, 5 share
+  // runs 0 and 2, waves 6, 7 runs 1 and 3.
+  constexpr int KL = DIM / 16;
+  constexpr bool SHARED = WAVES == 8 && DIM == 128;
   const int k_row = lane / KL, k_piece = lane % KL;
-  // dim 128: a wave's instruction brings 8 keys, so waves 4, 5 share runs 0 and 2, waves 6, 7 runs 1 and 3; dim 64: a
-  // run each
-  const int k_token = DIM == 128 ? 8 * (stage & 1) + k_row : k_row;
-  auto run_of = [&](int i) { return !keys ? stage : DIM == 128 ? stage / 2 + 2 * i : stage; };
-  const int lane_bytes = keys ? k_token * DIM + 16 * k_piece : (4 * v_half) * DIM + 4 * v_quad;
-  int ids[KP];                                  // pages of the next tile's runs that this wave stages
-  u32x4 raw[2];                                 // its codes
-  float run_scale[KP];
+  auto run_of = [&](int i) { return SHARED && keys ? stage / 2 + 2 * i : stage; };
+  auto token_of = [&](int i) { return (SHARED ? 8 * (stage & 1) : (64 / KL) * i) + k_row; };
+  const int v_lane = (4 * v_half) * DIM + 4 * v_quad;
+  int ids[KP];                                  // pages of the runs of the tile to be loaded next
+  u32x4 raw_k[KP], raw_v[2];                    // codes to be converted next
+  float run_k[KP], run_v;
   auto load_ids = [&](int t0) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < KP; ++i) ids[i] = table[min((t0 + 16 * run_of(i)) >> page_log, (int)c.width - 1)];
@@ -113,16 +118,16 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
       const int64_t id = real ? named : 0;
       const int64_t base = id * page_bytes + head_base + (int64_t)(t & (c.page - 1)) * DIM;
       if (keys) {
-        raw[i] = *reinterpret_cast<const u32x4*>(c.k_codes + base + lane_bytes);
-        run_scale[i] = real ? c.k_scale[id * c.heads + head] : 0.0f;
-      } else if (i == 0) {
-        const int8_t* from = c.v_codes + base;
+        raw_k[i] = *reinterpret_cast<const u32x4*>(c.k_codes + base + token_of(i) * DIM + 16 * k_piece);
+        run_k[i] = real ? c.k_scale[id * c.heads + head] : 0.0f;
+      }
+      if (values && i == 0) {
         if (v_half < 2) {
+          const int8_t* from = c.v_codes + base + v_lane;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            raw[j / 4][j % 4] = *reinterpret_cast<const uint32_t*>(from + lane_bytes + (j % 4 + 8 * (j / 4)) * DIM);
+          for (int j = 0; j < 8; ++j) raw_v[j / 4][j % 4] = *reinterpret_cast<const uint32_t*>(from + (j % 4 + 8 * (j / 4)) * DIM);
         }
-        run_scale[0] = real ? c.v_scale[id * c.heads + head] : -1.0f;
+        run_v = real ? c.v_scale[id * c.heads + head] : -1.0f;
       }
     }
   };
@@ -130,36 +135,37 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
     if (keys) {
 #pragma unroll
       for (int i = 0; i < KP; ++i) {
-        const int t = 16 * run_of(i) + k_token, ch = 2 * k_piece;
+        const int t = 16 * run_of(i) + token_of(i), ch = 2 * k_piece;
         u32x4 lo, hi;
         uint32_t two[2];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          f16_word(raw[i][j], two);
+          f16_word(raw_k[i][j], two);
           if (j < 2) lo[2 * j] = two[0], lo[2 * j + 1] = two[1];
           else hi[2 * j - 4] = two[0], hi[2 * j - 3] = two[1];
         }
         k_lds[buf][t * KCH + (ch ^ (t & (KCH - 1)))] = lo;
         k_lds[buf][t * KCH + ((ch + 1) ^ (t & (KCH - 1)))] = hi;
-        if (t % 16 == 0 && k_piece == 0) runs[buf][t / 16].k = run_scale[i];
+        if (t % 16 == 0 && k_piece == 0) runs[buf][t / 16].k = run_k[i];
       }
-    } else if (v_half < 2) {
+    }
+    if (values) {
       const int ch = 2 * stage + v_half;
-      const bool zeros = !(run_scale[0] >= 0x1p-126f);
+      const bool zeros = !(run_v >= 0x1p-126f);
+      if (v_half < 2) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) raw[j / 4][j % 4] ^= 0x80808080u;
+        for (int b = 0; b < 4; ++b) {
+          u32x4 a;
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        u32x4 a;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) a[j] = f16_bytes(raw[j / 2][2 * (j % 2) + 1], raw[j / 2][2 * (j % 2)], b);
-        const int d = 4 * v_quad + b;
-        v_lds[buf][d * (kTile / 8) + (ch ^ ((d ^ (d >> 2)) & 7))] = zeros ? u32x4{0, 0, 0, 0} : a;
+          for (int j = 0; j < 4; ++j) a[j] = f16_bytes(raw_v[j / 2][2 * (j % 2) + 1], raw_v[j / 2][2 * (j % 2)], b);
+          const int d = 4 * v_quad + b;
+          v_lds[buf][d * (kTile / 8) + (ch ^ ((d ^ (d >> 2)) & 7))] = zeros ? u32x4{0, 0, 0, 0} : a;
+        }
       }
       if (lane == 0) {
-        runs[buf][stage].v = zeros && run_scale[0] != -1.0f ? 0.0f : run_scale[0];
-        runs[buf][stage].v_log = __log2f(run_scale[0]);
-        runs[buf][stage].v_inv = 1.0f / run_scale[0];
+        runs[buf][stage].v_log = __log2f(run_v);
+        runs[buf][stage].v_inv = 1.0f / run_v;
+        runs[buf][stage].v_exp = zeros ? run_v == -1.0f ? kNone : kZeros : scale_exp(run_v);
       }
     }
   };
@@ -172,16 +178,17 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
   float top = -INFINITY, sum = 0.0f;
   int v_exp = kLeastExp;
 
-  // The keys' waves convert the next tile before they multiply, the values' waves after it (their codes are loaded
+  // Of 8 waves the keys' convert the next tile before they multiply, the values' after it (their codes are loaded
   // an iteration later), so that the two waves of a SIMD are out of step: one's products run under the other's softmax
-  // and conversions.  In step, a tile of 256 rows took the sum of both, ~6,000 cycles at dim 128.
+  // and conversions (four prompts of 1,502 tokens: 149 us, in step 160 us).
+  const bool ahead = WAVES == 8 && keys;
   if (begin < end) {
     load_ids(begin);
     load_codes(begin);
     load_ids(begin + kTile);
     store(0);
-    if (keys) {
-      load_codes(begin + kTile);
+    if (ahead) {
+      load_codes(begin + kTile);                // (past the end: rows of a page that exists, not seen)
       load_ids(begin + 2 * kTile);
     }
     __syncthreads();
@@ -189,19 +196,21 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
   for (int t0 = begin, buf = 0; t0 < end; t0 += kTile, buf ^= 1) {
     const bool more = t0 + kTile < end;
     if (more) {
-      if (keys) store(buf ^ 1);
-      const int next = keys ? t0 + 2 * kTile : t0 + kTile;
+      if (ahead) store(buf ^ 1);
+      const int next = ahead ? t0 + 2 * kTile : t0 + kTile;
       load_codes(next);
       load_ids(next + kTile);
     }
     if (t0 < wave_end) {
       f32x16 s[2];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
+      for (int k = 0; k < KS; ++k) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
           const int t = 32 * b + r;
           const u32x4 a = k_lds[buf][t * KCH + ((2 * k + h) ^ (t & (KCH - 1)))];
           s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, qf[k]), s[b], 0, 0, 0);
@@ -209,22 +218,22 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
       }
       Run run[kSubs];
       float factor[kSubs];
-      bool whole = t0 + kTile <= all_seen;
-      int tile_exp = kLeastExp;
+      int least = 0, tile_exp = kLeastExp;
 #pragma unroll
       for (int u = 0; u < kSubs; ++u) {
         run[u] = runs[buf][u];
         factor[u] = run[u].k * qs;
-        whole = whole && run[u].v >= 0.0f;
-        tile_exp = max(tile_exp, run[u].v > 0.0f ? scale_exp(run[u].v) : kLeastExp);
+        const int e = __builtin_amdgcn_readfirstlane(run[u].v_exp);
+        least = min(least, e);
+        tile_exp = max(tile_exp, e);
       }
-      if (!__builtin_amdgcn_readfirstlane(whole)) {             // some row does not see some token
+      if (t0 + kTile > all_seen || least == kNone) {             // some row does not see some token
 #pragma unroll
         for (int u = 0; u < kSubs; ++u) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int key = t0 + 16 * u + 8 * (i / 4) + 4 * h + i % 4;
-            const bool seen = key < end && key <= last_key && run[u].v >= 0.0f;
+            const bool seen = key < end && key <= last_key && run[u].v_exp != kNone;
             s[u / 2][8 * (u % 2) + i] = seen ? s[u / 2][8 * (u % 2) + i] * factor[u] : -INFINITY;
           }
           factor[u] = 1.0f;
@@ -238,13 +247,11 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
         for (int i = 1; i < 8; ++i) mu = fmaxf(mu, s[u / 2][8 * (u % 2) + i]);
         m = fmaxf(m, mu * factor[u]);
       }
-      tile_exp = __builtin_amdgcn_readfirstlane(tile_exp);
       if (__any(m > top + kLazy) || tile_exp > v_exp) {
         const float next = fmaxf(max_halves(m), top), ref = next == -INFINITY ? 0.0f : next;
         const int exp = max(tile_exp, v_exp);
-        const float by = __builtin_amdgcn_exp2f(top - ref);
-        sum *= by;
-        const float scaled = ldexpf(by, v_exp - exp);
+        const float scaled = ldexpf(__builtin_amdgcn_exp2f(top - ref), v_exp - exp);
+        sum *= scaled;
 #pragma unroll
         for (int b = 0; b < DB; ++b)
 #pragma unroll
@@ -252,12 +259,15 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
         top = next;
         v_exp = exp;
       }
-      const float ref = top == -INFINITY ? 0.0f : top;
+      const float ref = top == -INFINITY ? 0.0f : top, rest = (float)(kProbExp - v_exp) - ref;
       u32x4 p[kSubs];
 #pragma unroll
       for (int u = 0; u < kSubs; ++u) {
-        const bool scaled = run[u].v > 0.0f;
-        const float off = (scaled ? run[u].v_log + (float)(kProbExp - v_exp) : (float)(kProbExp - 1)) - ref;
+        float off = run[u].v_log + rest, inv = run[u].v_inv;
+        if (least <= kZeros && run[u].v_exp <= kZeros) {        // as a scale of 2^(v_exp - 1)
+          off = (float)(kProbExp - 1) - ref;
+          inv = ldexpf(1.0f, 1 - v_exp);
+        }
         float add = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
@@ -266,18 +276,18 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
           add += a + b;
           p[u][i / 2] = f16_pair(a, b);
         }
-        sum = __builtin_fmaf(add, scaled ? ldexpf(run[u].v_inv, v_exp - kProbExp) : ldexpf(1.0f, 1 - kProbExp), sum);
+        sum = __builtin_fmaf(add, inv, sum);
       }
 #pragma unroll
-      for (int b = 0; b < DB; ++b)
+      for (int u = 0; u < kSubs; ++u)
 #pragma unroll
-        for (int u = 0; u < kSubs; ++u) {
+        for (int b = 0; b < DB; ++b) {
           const int d = 32 * b + r;
           const u32x4 a = v_lds[buf][d * (kTile / 8) + ((2 * u + h) ^ ((d ^ (d >> 2)) & 7))];
           out[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, p[u]), out[b], 0, 0, 0);
         }
     }
-    if (more && !keys) store(buf ^ 1);
+    if (more && !ahead) store(buf ^ 1);
     __syncthreads();
   }
 
@@ -285,7 +295,7 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
   sum = sum_halves(sum);
   if (row0 + r >= rows) return;
   const float back = ldexpf(1.0f, v_exp - kProbExp);
-  const float by = splits == 1 ? (sum > 0.0f ? back / sum : 0.0f) : back;
+  const float by = splits == 1 ? (sum > 0.0f ? 1.0f / sum : 0.0f) : back;
   const int64_t index = ((seq * c.heads + head) * rows + row) * splits + split;
   uint16_t* dst = y + ((seq * tokens + row / group) * c.heads * group + head * group + row % group) * DIM;
 #pragma unroll
@@ -301,7 +311,7 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
     }
   if (splits > 1 && h == 0) {
     part.stat[2 * index] = top;
-    part.stat[2 * index + 1] = sum;
+    part.stat[2 * index + 1] = sum * back;
   }
 }
 
@@ -310,10 +320,12 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
 template <int DIM>
 hipError_t launch_prompt(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs, int64_t tokens, int group,
                          float scale, int64_t splits, uint16_t* y, Partial part, hipStream_t stream) {
-  const int64_t tiles = (tokens * group + kPromptRows - 1) / kPromptRows, total = seqs * c.heads * tiles * splits;
+  const int rows = prompt_rows_of(c.width * c.page);
+  const int64_t tiles = (tokens * group + rows - 1) / rows, total = seqs * c.heads * tiles * splits;
   if (total > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((kv_prompt_kernel<DIM>), dim3((unsigned)total), dim3(kThreads), 0, stream, c, q, ldq, (int)tokens, group,
-                     scale, (int)splits, (int)tiles, (int)total, y, part);
+  const auto kernel = rows == 256 ? kv_prompt_kernel<DIM, 8> : kv_prompt_kernel<DIM, 4>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)total), dim3(2 * rows), 0, stream, c, q, ldq, (int)tokens, group, scale, (int)splits,
+                     (int)tiles, (int)total, y, part);
   return hipGetLastError();
 }
 
