@@ -37,16 +37,17 @@ __device__ __forceinline__ int64_t held_of(const KvCache& c, int64_t seq) { retu
 template <int DIM>
 __global__ void __launch_bounds__(256)
 kv_append_kernel(KvCache c, const uint16_t* __restrict__ k, int64_t ldk, const uint16_t* __restrict__ v, int64_t ldv,
-                 int64_t tokens, int64_t touched) {
+                 int64_t tokens, unsigned touched) {
   constexpr int kPieces = 128 * DIM / 8 / 256;   // of the largest page
   __shared__ float wave_max[4];
-  int64_t at = blockIdx.x;
+  const int page_log = __builtin_ctz(c.page);
+  unsigned at = blockIdx.x;
   const bool values = at & 1;
   at >>= 1;
-  const int head = (int)(at % c.heads);
+  const int head = at % c.heads;
   at /= c.heads;
   const int64_t seq = at / touched, held = held_of(c, seq), first = len_of(c, seq) - tokens;
-  const int64_t block = max<int64_t>(first, 0) / c.page + at % touched, start = block * c.page;
+  const int64_t block = (max(first, (int64_t)0) >> page_log) + at % touched, start = block << page_log;
   if (start >= held) return;
   const int64_t id = page_of(c, seq, block);
   if (id < 0) return;
@@ -55,8 +56,8 @@ kv_append_kernel(KvCache c, const uint16_t* __restrict__ k, int64_t ldk, const u
   const int64_t base = id * c.heads + head;
   int8_t* dst = (values ? c.v_codes : c.k_codes) + base * c.page * DIM;
   float* scale = (values ? c.v_scale : c.k_scale) + base;
-  const int rows = (int)min<int64_t>(c.page, held - start);         // rows of the block in use
-  const int old_rows = (int)min<int64_t>(max<int64_t>(first - start, 0), rows);   // from before
+  const int rows = (int)min((int64_t)c.page, held - start);         // rows of the block in use
+  const int old_rows = (int)min(max(first - start, (int64_t)0), (int64_t)rows);   // from before
 
   u32x4 raw[kPieces];
   float amax = 0.0f;
@@ -111,30 +112,47 @@ kv_append_kernel(KvCache c, const uint16_t* __restrict__ k, int64_t ldk, const u
   if (threadIdx.x == 0) *scale = s;                  // every thread has read s_old (barrier above)
 }
 
-// k, v [seqs][length][heads][dim] bf16: one thread per 8 values of both.
+// k, v [seqs][length][heads][dim] bf16.  A workgroup takes 2048 / DIM tokens of a sequence and up to kReadHeads heads, a
+// thread 8 values of each: a head's codes of those tokens are one piece of a page, and no index needs a division
+// per thread (one thread per 8 values of the flat output took 9.7 us for 61 sequences of 299 tokens, 8 heads of 64).
+constexpr int kReadHeads = 4;
 template <int DIM>
 __global__ void __launch_bounds__(256)
-kv_read_kernel(KvCache c, int64_t length, int64_t pieces, uint16_t* __restrict__ k, uint16_t* __restrict__ v) {
-  const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (j >= pieces) return;
-  const int d = (int)(j % (DIM / 8)) * 8;
-  const int64_t row = j / (DIM / 8), head = row % c.heads, pos = row / c.heads % length, seq = row / c.heads / length;
-  const int64_t id = pos < held_of(c, seq) ? page_of(c, seq, pos / c.page) : -1;
-  u32x4 out[2] = {u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
-  if (id >= 0) {
-    const int64_t base = id * c.heads + head, code = (base * c.page + pos % c.page) * DIM + d;
-    const u32x2_t w[2] = {*reinterpret_cast<const u32x2_t*>(c.k_codes + code), *reinterpret_cast<const u32x2_t*>(c.v_codes + code)};
-    const float s[2] = {c.k_scale[base], c.v_scale[base]};
+kv_read_kernel(KvCache c, int64_t length, int chunks, uint16_t* __restrict__ k, uint16_t* __restrict__ v) {
+  constexpr int LANES = DIM / 8;
+  const int d = threadIdx.x % LANES * 8, page_log = __builtin_ctz(c.page);
+  const int64_t seq = blockIdx.x / chunks, pos = (int64_t)(blockIdx.x % chunks) * (256 / LANES) + threadIdx.x / LANES;
+  const int head0 = blockIdx.y * kReadHeads;
+  if (pos >= length) return;
+  const int64_t id = pos < held_of(c, seq) ? page_of(c, seq, pos >> page_log) : -1;
+  const int64_t base = max(id, (int64_t)0) * c.heads, row = (int64_t)(pos & (c.page - 1)) * DIM + d;
+  u32x2_t w[kReadHeads][2];
+  float s[kReadHeads][2];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t b = w[t][i / 2] >> (16 * (i % 2));
-        out[t][i] = bf16x2_rne((float)(int8_t)b * s[t], (float)(int8_t)(b >> 8) * s[t]);
-      }
+  for (int i = 0; i < kReadHeads; ++i) {        // (past the last head: the last again, not stored)
+    const int64_t at = base + min(head0 + i, c.heads - 1), code = at * c.page * DIM + row;
+    w[i][0] = *reinterpret_cast<const u32x2_t*>(c.k_codes + code);
+    w[i][1] = *reinterpret_cast<const u32x2_t*>(c.v_codes + code);
+    s[i][0] = c.k_scale[at];
+    s[i][1] = c.v_scale[at];
   }
-  *reinterpret_cast<u32x4*>(k + j * 8) = out[0];
-  *reinterpret_cast<u32x4*>(v + j * 8) = out[1];
+#pragma unroll
+  for (int i = 0; i < kReadHeads; ++i) {
+    if (head0 + i >= c.heads) break;
+    const int64_t to = ((seq * length + pos) * c.heads + head0 + i) * DIM + d;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      u32x4 out = {0, 0, 0, 0};
+      if (id >= 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t b = w[i][t][j / 2] >> (16 * (j % 2));
+          out[j] = bf16x2_rne((float)(int8_t)b * s[i][t], (float)(int8_t)(b >> 8) * s[i][t]);
+        }
+      }
+      *reinterpret_cast<u32x4*>((t ? v : k) + to) = out;
+    }
+  }
 }
 
 }  // namespace
@@ -145,20 +163,20 @@ hipError_t launch_kv_append(const KvCache& c, const uint16_t* k, int64_t ldk, co
   const int64_t blocks = seqs * touched * c.heads * 2;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
   if (c.dim == 64)
-    hipLaunchKernelGGL((kv_append_kernel<64>), dim3((unsigned)blocks), dim3(256), 0, stream, c, k, ldk, v, ldv, tokens, touched);
+    hipLaunchKernelGGL((kv_append_kernel<64>), dim3((unsigned)blocks), dim3(256), 0, stream, c, k, ldk, v, ldv, tokens, (unsigned)touched);
   else
-    hipLaunchKernelGGL((kv_append_kernel<128>), dim3((unsigned)blocks), dim3(256), 0, stream, c, k, ldk, v, ldv, tokens, touched);
+    hipLaunchKernelGGL((kv_append_kernel<128>), dim3((unsigned)blocks), dim3(256), 0, stream, c, k, ldk, v, ldv, tokens, (unsigned)touched);
   return hipGetLastError();
 }
 
 hipError_t launch_kv_read(const KvCache& c, int64_t seqs, int64_t length, uint16_t* k, uint16_t* v,
                           hipStream_t stream) {
-  const int64_t pieces = seqs * length * c.heads * (c.dim / 8), blocks = (pieces + 255) / 256;
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  if (c.dim == 64)
-    hipLaunchKernelGGL((kv_read_kernel<64>), dim3((unsigned)blocks), dim3(256), 0, stream, c, length, pieces, k, v);
-  else
-    hipLaunchKernelGGL((kv_read_kernel<128>), dim3((unsigned)blocks), dim3(256), 0, stream, c, length, pieces, k, v);
+  const int tokens = 2048 / c.dim;              // of a workgroup
+  const int64_t chunks = (length + tokens - 1) / tokens;
+  if (chunks * seqs > 0x7fffffff) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)(chunks * seqs), (unsigned)((c.heads + kReadHeads - 1) / kReadHeads));
+  const auto kernel = c.dim == 64 ? kv_read_kernel<64> : kv_read_kernel<128>;
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, c, length, (int)chunks, k, v);
   return hipGetLastError();
 }
 

@@ -157,7 +157,7 @@ w4_few_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, con
 
   const uint16_t* xp[XI];
 #pragma unroll
-  for (int i = 0; i < XI; ++i) xp[i] = x + min<int64_t>(4 * i + h, M - 1) * K + 8 * t;     // past M: row M - 1, not stored
+  for (int i = 0; i < XI; ++i) xp[i] = x + min((int64_t)(4 * i + h), M - 1) * K + 8 * t;     // past M: row M - 1, not stored
   const uint8_t* wp[RB];
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb) wp[rb] = w + min(b0 + rb, blocks - 1) * kb_all * kBlockBytes + 16 * lane;
