@@ -84,6 +84,16 @@ def test_a_token_alone_and_in_a_batch(lib, N, K, group):
         assert torch.equal(part.view(torch.int16), y[rows].view(torch.int16)), rows
 
 
+# 17 tokens and more: 2, 3 and 4 row blocks an item, items that a workgroup takes one after another, runs without a
+# block (K < 1024), K in splits; and the tile of x shared by 4 .. 7 and by 8 .. 12 waves
+@pytest.mark.parametrize("M,N,K,group", ((64, 4096, 640, 64), (64, 5120, 1152, 128), (24, 34816, 256, 32), (256, 4096, 1152, 128), (250, 4088, 384, 32), (20, 5128, 12416, 64), (129, 2056, 12288, 32), (256, 5120, 640, 64), (500, 4096, 384, 32), (490, 4104, 1280, 128)))
+def test_many_tokens(lib, M, N, K, group):
+    y, (x, cp, sp, b) = run(lib, M, N, K, group, True, 900 + M)
+    few = [lib.w8a8_w4_linear(x[m:m + 16].cuda(), cp, sp, N, group, b.cuda()) for m in (0, 16, (M - 1) // 16 * 16)]
+    for m, f in zip((0, 16, (M - 1) // 16 * 16), few):
+        assert torch.equal(y[m:m + 16], f), f"rows {m} .. of {M} differ from the same rows alone"
+
+
 def test_whole_numbers_are_exact(lib):
     """x = +-1 and scales of one: sums of whole numbers below 2^24, so the only rounding is the output's."""
     K, N = 1280, 48

@@ -245,25 +245,196 @@ w4_few_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, con
   }
 }
 
-// 17 tokens and more, 16 * MB at a time.  A wave owns a block of 16 rows and walks the split's columns; the workgroup's
-// waves share each 128-column tile of x in LDS (two of them, one barrier a block), so x is read once for
-// all their rows.  Weights and scales go straight to registers, kAhead blocks ahead.  What bounds it is the
-// step from block to block: per wave 32 MFMAs, 16 operand reads and ~120 vector instructions that the
-// barrier keeps in step, about 2,600 cycles for 9 waves where each pipe alone would need 1,150: 64 tokens of
-// 5,120 x 34,816 take 49 us (a wave per row block without sharing x took 197 us).
-constexpr int kAhead = 4;
 __device__ __forceinline__ void lds_barrier() {       // __syncthreads would wait for the loads in flight, too
   __builtin_amdgcn_s_waitcnt(0xc07f);                 // lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
 
-template <int MB, int GPB, int WMIN, int WMAX>
+// From 17 tokens on, 32 at a time, while the workgroups go a few times round the 256 CUs.  As above, a wave takes a
+// run of columns through an LDS area of its own; a widened weight serves two blocks of tokens, and the
+// offset's MFMA RB blocks of rows.  A workgroup walks over items (RB blocks of rows, 32 tokens, a split) and
+// loads the next item's first step while it still multiplies and adds up the present one.  What bounds it is the
+// issue of MFMAs and of the ~230 vector instructions a step, and x, which every RB blocks of rows read again from
+// L2: 2 us a step of RB = 4.  64 tokens of 5,120 x 5,120 take 11.7 us and 64 of 4,096 x 4,096 9.2 us, where a
+// tile of x shared by waves of different rows (the form below) takes 27.3 and 22.2 us with its few waves; x and
+// scales two steps ahead, or workgroups that end with their item, were no faster.
+template <int RB, int GPB>
+__global__ void __launch_bounds__(64 * kSegs)
+w4_mid_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, const uint16_t* __restrict__ s,
+               const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, float* __restrict__ part, int64_t M, int64_t N,
+               int64_t K, unsigned m_blocks, unsigned row_items, int splits) {
+  constexpr int MB = 2, TOKENS = 16 * MB, XI = 4 * MB, SPG = 4 / GPB;
+  constexpr int SL = 2 * GPB;                  // 16-byte pieces of a row block's scales
+  static_assert(RB * SL <= 64, "one instruction brings the scales");
+  constexpr int AREA = TOKENS * 16 + 64;       // 16-byte units of a wave's area
+  __shared__ __attribute__((aligned(16))) u32x4 lds[kSegs * (AREA + RB * MB * 64)];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = lane >> 4, t = lane & 15;
+  const int64_t blocks = (N + kRows - 1) / kRows;
+  const int kb_all = (int)(K / kCols);
+  u32x4* xl = lds + wave * AREA;
+  u32x4* sl = xl + TOKENS * 16;
+  f32x4* red = reinterpret_cast<f32x4*>(lds + kSegs * AREA);
+  const unsigned xcd = blockIdx.x % 8;
+
+  // the XCD's item j: an XCD's workgroups take all tokens of a split of RB row blocks together, so its L2 brings
+  // the weights once
+  struct Item {
+    int64_t m0, b0;
+    int split, first, n;
+  };
+  auto item_at = [&](unsigned j) __attribute__((always_inline)) {
+    Item a;
+    const unsigned r = j / m_blocks, c = r / splits;
+    a.m0 = (int64_t)(j - r * m_blocks) * TOKENS;
+    a.split = r - c * splits;
+    a.b0 = (int64_t)(c * 8 + xcd) * RB;
+    a.first = run_begin(kb_all, a.split * kSegs + wave, kSegs * splits);
+    a.n = run_begin(kb_all, a.split * kSegs + wave + 1, kSegs * splits) - a.first;
+    return a;
+  };
+  const unsigned rows_here = (row_items + 7 - xcd) / 8, mine = rows_here * splits * m_blocks, step = gridDim.x / 8;
+  unsigned j = blockIdx.x / 8;
+  if (j >= mine) return;
+  Item cur = item_at(j), nxt = cur;            // the one that is multiplied, and the one that is loaded: its
+  unsigned jn = j;                             // number and its step
+  int ln = 0;
+  uint32_t xo[XI], so;                         // bytes; past M and past N: the last row again, not stored
+  auto lanes = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < XI; ++i) xo[i] = 2 * ((uint32_t)min((int64_t)(4 * i + h), M - 1 - nxt.m0) * (uint32_t)K + 8 * t);
+    const int piece = min(lane, RB * SL - 1);
+    so = 2 * ((uint32_t)min((int64_t)(piece / SL), blocks - 1 - nxt.b0) * (uint32_t)(kb_all * GPB * kRows) + piece % SL * 8);
+  };
+  lanes();
+  const bf16x8 offset = minus_offset();
+  const uint32_t mask = nibble_mask();
+  f32x4 tot[RB][MB];
+  u32x4 wv[2][RB], xv[XI], sv;
+  auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) tot[rb][mb] = f32x4{0.f, 0.f, 0.f, 0.f};
+  };
+  clear();
+  auto load_w = [&](int d) __attribute__((always_inline)) {
+    const int64_t kb = min(nxt.first + ln, kb_all - 1);
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+      wv[d][rb] = *reinterpret_cast<const u32x4*>(w + (min(nxt.b0 + rb, blocks - 1) * kb_all + kb) * kBlockBytes + 16 * lane);
+  };
+  auto load_x = [&]() __attribute__((always_inline)) {
+    const int64_t kb = min(nxt.first + ln, kb_all - 1);
+    const char* xb = reinterpret_cast<const char*>(x + nxt.m0 * K + kb * kCols);
+#pragma unroll
+    for (int i = 0; i < XI; ++i) xv[i] = *reinterpret_cast<const u32x4*>(xb + xo[i]);
+    sv = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(s + (nxt.b0 * kb_all + kb) * (GPB * kRows)) + so);
+  };
+  auto advance = [&]() __attribute__((always_inline)) {
+    if (++ln < nxt.n) return;
+    ln = 0;
+    jn += step;
+    if (jn < mine) nxt = item_at(jn), lanes();
+  };
+  // a wave's LDS operations are done in their order, so its area needs no barrier
+  auto put_x = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < XI; ++i) xl[(4 * i + h) * 16 + (t ^ ((4 * i + h) & 15))] = xv[i];
+    sl[lane] = sv;
+  };
+  auto multiply = [&](int d) __attribute__((always_inline)) {
+#pragma unroll
+    for (int g = 0; g < GPB; ++g) {
+      __builtin_amdgcn_sched_barrier(0);
+      bf16x8 xf[SPG][MB];
+      f32x4 base[MB];
+#pragma unroll
+      for (int st = 0; st < SPG; ++st)
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          xf[st][mb] = __builtin_bit_cast(bf16x8, xl[(16 * mb + t) * 16 + ((4 * (g * SPG + st) + h) ^ t)]);
+          base[mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(offset, xf[st][mb], st ? base[mb] : f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+        }
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) {
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 acc[MB];
+#pragma unroll
+        for (int st = 0; st < SPG; ++st) {
+          const bf16x8 a = widen(wv[d][rb][g * SPG + st], mask);
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb)
+            acc[mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, xf[st][mb], st ? acc[mb] : base[mb], 0, 0, 0);
+        }
+        float sc[4];
+        bf16x4(reinterpret_cast<const uint2*>(sl)[(rb * GPB + g) * 4 + h], sc);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) tot[rb][mb][e] = __builtin_fmaf(sc[e], acc[mb][e], tot[rb][mb][e]);
+      }
+    }
+  };
+  auto finish = [&]() __attribute__((always_inline)) {
+    lds_barrier();                             // the last item's sums have been read
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+        red[((wave * RB + rb) * MB + mb) * 64 + lane] = cur.n ? tot[rb][mb] : f32x4{0.f, 0.f, 0.f, 0.f};
+    clear();
+    lds_barrier();
+    for (int q = threadIdx.x; q < RB * MB * 64; q += 64 * kSegs) {
+      const int64_t m = cur.m0 + 16 * (q / 64 % MB) + q % 16, row = (cur.b0 + q / (64 * MB)) * kRows + 4 * (q % 64 / 16);
+      if (m >= M || row >= N) continue;        // N % 8 == 0: the four rows are whole or absent
+      f32x4 v = red[q];
+#pragma unroll
+      for (int r = 1; r < kSegs; ++r) v += red[r * RB * MB * 64 + q];
+      store_outputs(v, m, row, M, N, bias, y, part, cur.split, splits);
+    }
+  };
+  load_x();
+  load_w(0);
+  advance();
+  int i = 0;
+  for (;;) {
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      __builtin_amdgcn_sched_barrier(0);
+      load_w(d ^ 1);
+      __builtin_amdgcn_sched_barrier(0);
+      put_x();
+      load_x();
+      advance();
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(d);
+      __builtin_amdgcn_sched_barrier(0);
+      if (++i >= cur.n) {
+        finish();
+        j += step;
+        if (j >= mine) return;
+        cur = item_at(j);
+        i = 0;
+      }
+    }
+  }
+}
+
+// Many tokens and rows, 64 tokens at a time.  A wave owns a block of 16 rows and walks the split's columns; the workgroup's
+// waves share each 128-column tile of x in LDS (two of them, one barrier a block), so x is read once for
+// all their rows.  Weights and scales go straight to registers, kAhead blocks ahead.  What bounds it is the
+// step from block to block: per wave 32 MFMAs, 16 operand reads and ~120 vector instructions that the
+// barrier keeps in step, about 2,600 cycles for 9 waves where each pipe alone would need 1,150: 64 tokens of
+// 5,120 x 34,816 take 49 us (a wave per row block without sharing x took 197 us).
+constexpr int kAhead = 4;
+template <int GPB, int WMIN, int WMAX>
 __global__ void __launch_bounds__(64 * WMAX)
 w4_many_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, const uint16_t* __restrict__ s,
                const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, float* __restrict__ part, int64_t M, int64_t N,
                int64_t K) {
-  constexpr int PIECES = MB * 256;             // 16-byte pieces of a tile of x
+  constexpr int MB = 4, PIECES = MB * 256;     // 16-byte pieces of a tile of x
   constexpr int XP = (PIECES + 64 * WMIN - 1) / (64 * WMIN);     // of a thread, at least WMIN waves
   constexpr int SPG = 4 / GPB;
   __shared__ __attribute__((aligned(16))) u32x4 tile[2 * PIECES];
@@ -418,13 +589,24 @@ hipError_t launch_few(const Linear& a) {
   return hipGetLastError();
 }
 
-template <int MB, int WMIN, int WMAX>
+template <int RB>
+hipError_t launch_mid(const Linear& a) {
+  const int64_t blocks = (a.N + kRows - 1) / kRows, row_items = (blocks + RB - 1) / RB, m_blocks = (a.M + 31) / 32;
+  const int64_t items = (row_items + 7) / 8 * 8 * m_blocks * a.splits;           // (XCDs take the same number)
+  if (items > 0x7fffffff) return hipErrorInvalidValue;
+  const auto kernel = a.group == 128 ? w4_mid_kernel<RB, 1> : a.group == 64 ? w4_mid_kernel<RB, 2> : w4_mid_kernel<RB, 4>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(items, 256)), dim3(64 * kSegs), 0, a.stream, a.x, a.w, a.s, a.bias,
+                     a.y, a.part, a.M, a.N, a.K, (unsigned)m_blocks, (unsigned)row_items, a.splits);
+  return hipGetLastError();
+}
+
+template <int WMIN, int WMAX>
 hipError_t launch_many(const Linear& a, int waves) {
   const int64_t blocks = (a.N + kRows - 1) / kRows;
-  const dim3 grid((unsigned)((blocks + waves - 1) / waves), (unsigned)((a.M + 16 * MB - 1) / (16 * MB)), (unsigned)a.splits);
-  const auto kernel = a.group == 128  ? w4_many_kernel<MB, 1, WMIN, WMAX>
-                      : a.group == 64 ? w4_many_kernel<MB, 2, WMIN, WMAX>
-                                      : w4_many_kernel<MB, 4, WMIN, WMAX>;
+  const dim3 grid((unsigned)((blocks + waves - 1) / waves), (unsigned)((a.M + 63) / 64), (unsigned)a.splits);
+  const auto kernel = a.group == 128  ? w4_many_kernel<1, WMIN, WMAX>
+                      : a.group == 64 ? w4_many_kernel<2, WMIN, WMAX>
+                                      : w4_many_kernel<4, WMIN, WMAX>;
   hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), 0, a.stream, a.x, a.w, a.s, a.bias, a.y, a.part, a.M, a.N, a.K);
   return hipGetLastError();
 }
@@ -473,16 +655,21 @@ hipError_t launch_w4_linear(const uint16_t* x, const uint8_t* codes_packed, cons
     if (M <= 4) e = items >= 512 ? launch_few<1, 2>(a) : launch_few<1, 1>(a);
     else e = items >= 768 ? launch_few<4, 4>(a) : items >= 512 ? launch_few<4, 2>(a) : launch_few<4, 1>(a);
   } else {
-    // waves (row blocks) of a workgroup: fewest rounds of the 256 CUs, a round costing a little besides its waves
-    const int64_t tiles = (M + (M <= 32 ? 31 : 63)) / (M <= 32 ? 32 : 64) * a.splits;
-    int waves = 4;
+    // 32 tokens and RB row blocks an item, or 64 tokens and a row block for each of v waves: a round of the 256
+    // CUs was measured to take about RB + 2 parts of one and 2 (v + 3) of the other (of 128 columns a run: 1.2 us
+    // a part), and up to 32 tokens half of the second's work would be thrown away
+    int rb = 2, waves = 0;
     int64_t least = 0;
-    for (int v = 4; v <= 12; ++v) {
-      const int64_t cost = ((blocks + v - 1) / v * tiles + 255) / 256 * (v + 3);
-      if (v == 4 || cost < least) waves = v, least = cost;
+    for (int v = 2; v <= 4; ++v) {
+      const int64_t cost = (((blocks + v - 1) / v) * ((M + 31) / 32) * a.splits + 255) / 256 * (v + 2);
+      if (v == 2 || cost < least) rb = v, least = cost;
     }
-    if (M <= 32) e = waves < 8 ? launch_many<2, 4, 7>(a, waves) : launch_many<2, 8, 12>(a, waves);
-    else e = waves < 8 ? launch_many<4, 4, 7>(a, waves) : launch_many<4, 8, 12>(a, waves);
+    for (int v = 4; v <= 12 && M > 32; ++v) {
+      const int64_t cost = ((blocks + v - 1) / v * ((M + 63) / 64) * a.splits + 255) / 256 * 2 * (v + 3);
+      if (cost < least) waves = v, least = cost;
+    }
+    if (waves) e = waves < 8 ? launch_many<4, 7>(a, waves) : launch_many<8, 12>(a, waves);
+    else e = rb == 2 ? launch_mid<2>(a) : rb == 3 ? launch_mid<3>(a) : launch_mid<4>(a);
   }
   if (e != hipSuccess || a.splits == 1) return e;
   hipLaunchKernelGGL(w4_combine_kernel, dim3((unsigned)((M * N / 4 + 255) / 256)), dim3(256), 0, stream, a.part, bias, y, M, N,
