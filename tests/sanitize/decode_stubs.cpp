@@ -1,6 +1,6 @@
 // Host-only stand-ins for the few-token launchers, for the sanitizer build of csrc/decode_api.cpp: no path
 // reaches a launch without a gfx950 device; if one did, it would report an error.
-#include "internal.h"
+#include "decode.h"
 
 namespace w8a8 {
 

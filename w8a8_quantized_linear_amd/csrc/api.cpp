@@ -6,6 +6,7 @@
 #include <atomic>
 #include <cstring>
 
+#include "entry.h"
 #include "internal.h"
 
 namespace {

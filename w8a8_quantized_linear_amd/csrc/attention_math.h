@@ -2,8 +2,8 @@
 // sequence into pieces, and where the pieces leave their partial results.
 #pragma once
 
+#include "decode.h"
 #include "epilogue_math.h"
-#include "internal.h"
 
 namespace w8a8 {
 namespace kva {

@@ -5,7 +5,8 @@
 
 #include <cmath>
 
-#include "internal.h"
+#include "decode.h"
+#include "entry.h"
 
 namespace {
 

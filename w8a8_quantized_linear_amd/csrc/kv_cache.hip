@@ -11,8 +11,8 @@
 // single fp32 operations, so the codes are the same on every run and machine.
 //
 // Bound: memory traffic (2 bytes read and 1 written per new value) and, for single tokens, latency.
+#include "decode.h"
 #include "epilogue_math.h"
-#include "internal.h"
 #include "quant_math.h"
 
 namespace w8a8 {

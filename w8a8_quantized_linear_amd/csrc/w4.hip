@@ -4,8 +4,8 @@
 // c in [-8, 7], one bf16 scale for each row and group of 32, 64 or 128 columns, bf16 activations and
 // fp32 sums.  For a few tokens the weight codes are the traffic (half a byte for every 2M operations),
 // so the kernel is built around one pass over them.
+#include "decode.h"
 #include "epilogue_math.h"
-#include "internal.h"
 
 namespace w8a8 {
 namespace {
