@@ -255,10 +255,12 @@ __device__ __forceinline__ void lds_barrier() {       // __syncthreads would wai
 // run of columns through an LDS area of its own; a widened weight serves two blocks of tokens, and the
 // offset's MFMA RB blocks of rows.  A workgroup walks over items (RB blocks of rows, 32 tokens, a split) and
 // loads the next item's first step while it still multiplies and adds up the present one.  What bounds it is the
-// issue of MFMAs and of the ~230 vector instructions a step, and x, which every RB blocks of rows read again from
-// L2: 2 us a step of RB = 4.  64 tokens of 5,120 x 5,120 take 11.7 us and 64 of 4,096 x 4,096 9.2 us, where a
-// tile of x shared by waves of different rows (the form below) takes 27.3 and 22.2 us with its few waves; x and
-// scales two steps ahead, or workgroups that end with their item, were no faster.
+// issue of a step's MFMAs (40 for RB = 4, 640 cycles) and vector instructions (210, 840 cycles) by two waves a SIMD,
+// which overlap little: 4,400 cycles a step, and 4,000 with every load a cache hit.  64 tokens of 5,120 x 5,120 take
+// 11.4 us and 64 of 4,096 x 4,096 8.8 us, where a tile of x shared by waves of different rows (the form below) takes
+// 27.3 and 22.2 us with its few waves.  The scales are read with the operands: read where they are used they
+// cost 34.9 us instead of 31.0 (64 tokens of 17,408 x 5,120, groups of 32).  x and scales two steps ahead, four blocks
+// of tokens a wave, or workgroups that end with their item were no faster.
 template <int RB, int GPB>
 __global__ void __launch_bounds__(64 * kSegs)
 w4_mid_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, const uint16_t* __restrict__ s,
@@ -350,6 +352,9 @@ w4_mid_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, con
       __builtin_amdgcn_sched_barrier(0);
       bf16x8 xf[SPG][MB];
       f32x4 base[MB];
+      uint2 sw[RB];
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) sw[rb] = reinterpret_cast<const uint2*>(sl)[(rb * GPB + g) * 4 + h];
 #pragma unroll
       for (int st = 0; st < SPG; ++st)
 #pragma unroll
@@ -359,7 +364,6 @@ w4_mid_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, con
         }
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
-        __builtin_amdgcn_sched_barrier(0);
         f32x4 acc[MB];
 #pragma unroll
         for (int st = 0; st < SPG; ++st) {
@@ -369,7 +373,7 @@ w4_mid_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, con
             acc[mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, xf[st][mb], st ? acc[mb] : base[mb], 0, 0, 0);
         }
         float sc[4];
-        bf16x4(reinterpret_cast<const uint2*>(sl)[(rb * GPB + g) * 4 + h], sc);
+        bf16x4(sw[rb], sc);
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
