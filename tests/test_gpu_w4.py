@@ -84,6 +84,15 @@ def test_a_token_alone_and_in_a_batch(lib, N, K, group):
         assert torch.equal(part.view(torch.int16), y[rows].view(torch.int16)), rows
 
 
+# 1 to 4 row blocks a workgroup: few rows, rows in one round of the CUs, in several, in splits
+@pytest.mark.parametrize("M,N,K,group", ((5, 4096, 640, 64), (16, 5120, 1152, 128), (9, 12288, 384, 32), (16, 12280, 1152, 64), (7, 16384, 256, 128), (16, 34816, 128, 32), (13, 5120, 12416, 64), (16, 16400, 640, 128)))
+def test_up_to_sixteen_tokens(lib, M, N, K, group):
+    y, (x, cp, sp, b) = run(lib, M, N, K, group, True, 700 + M)
+    for m in (0, M - 1):
+        one = lib.w8a8_w4_linear(x[m:m + 1].cuda(), cp, sp, N, group, b.cuda())
+        assert torch.equal(y[m:m + 1], one), f"row {m} of {M} differs from the row alone"
+
+
 # 17 tokens and more: 2, 3 and 4 row blocks an item, items that a workgroup takes one after another, runs without a
 # block (K < 1024), K in splits; and the tile of x shared by 4 .. 7 and by 8 .. 12 waves
 @pytest.mark.parametrize("M,N,K,group", ((64, 4096, 640, 64), (64, 5120, 1152, 128), (24, 34816, 256, 32), (256, 4096, 1152, 128), (250, 4088, 384, 32), (20, 5128, 12416, 64), (129, 2056, 12288, 32), (256, 5120, 640, 64), (500, 4096, 384, 32), (490, 4104, 1280, 128)))

@@ -193,6 +193,9 @@ w4_few_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, con
     for (int g = 0; g < GPB; ++g) {
       bf16x8 xf[SPG];
       f32x4 base = {0.f, 0.f, 0.f, 0.f};
+      uint2 sw[RB];
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) sw[rb] = reinterpret_cast<const uint2*>(sl)[(rb * GPB + g) * 4 + h];
 #pragma unroll
       for (int st = 0; st < SPG; ++st) {
         const int row = t % XROWS;
@@ -206,7 +209,7 @@ w4_few_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, con
         for (int st = 0; st < SPG; ++st)
           acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(wv[d][rb][g * SPG + st], mask), xf[st], acc, 0, 0, 0);
         float sc[4];
-        bf16x4(reinterpret_cast<const uint2*>(sl)[(rb * GPB + g) * 4 + h], sc);
+        bf16x4(sw[rb], sc);
 #pragma unroll
         for (int i = 0; i < 4; ++i) tot[rb][i] = __builtin_fmaf(sc[i], acc[i], tot[rb][i]);
       }
@@ -654,10 +657,22 @@ hipError_t launch_w4_linear(const uint16_t* x, const uint8_t* codes_packed, cons
   const int64_t blocks = (N + kRows - 1) / kRows;
   hipError_t e;
   if (M <= 16) {
-    // more row blocks a workgroup share x, as long as there are workgroups for the 256 CUs
-    const int64_t items = blocks * a.splits;
-    if (M <= 4) e = items >= 512 ? launch_few<1, 2>(a) : launch_few<1, 1>(a);
-    else e = items >= 768 ? launch_few<4, 4>(a) : items >= 512 ? launch_few<4, 2>(a) : launch_few<4, 1>(a);
+    if (M <= 4) {
+      // row blocks of a workgroup share x, as long as there are workgroups for the 256 CUs
+      e = blocks * a.splits >= 512 ? launch_few<1, 2>(a) : launch_few<1, 1>(a);
+    } else {
+      // x weighs more: a round of 256 workgroups was measured to take about 3, 4, 6 and 8 parts with 1 to 4 row blocks
+      // (16 tokens of 5,120 x 34,816: 35, 26, 22 and 27 us in 9, 5, 3 and 3 rounds; of 8,192 x 8,192 11.5, 10.3, 10.8
+      // and 13.4 us in 2, 1, 1 and 1)
+      constexpr int kParts[5] = {0, 3, 4, 6, 8};
+      int rb = 1;
+      int64_t least = 0;
+      for (int v = 1; v <= 4; ++v) {
+        const int64_t cost = ((blocks + v - 1) / v * a.splits + 255) / 256 * kParts[v];
+        if (v == 1 || cost <= least) rb = v, least = cost;
+      }
+      e = rb == 1 ? launch_few<4, 1>(a) : rb == 2 ? launch_few<4, 2>(a) : rb == 3 ? launch_few<4, 3>(a) : launch_few<4, 4>(a);
+    }
   } else {
     // 32 tokens and RB row blocks an item, or 64 tokens and a row block for each of v waves: a round of the 256
     // CUs was measured to take about RB + 2 parts of one and 2 (v + 3) of the other (of 128 columns a run: 1.2 us
