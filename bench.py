@@ -116,6 +116,11 @@ def parse():
     ap.add_argument("--drift", action="store_true",
                     help="instead of timing: relative L2 drift of every workload's W8A8 output from "
                          "the fp64 unquantized projection, without and with the block rotation")
+    ap.add_argument("--decode", action="store_true",
+                    help="instead of the workload line: a decoder layer (5,120 wide, 40 query and 8 cache heads "
+                         "of 128, 17,408 in the MLP) on 1, 8 and 32 sequences: a prompt of 1,502 tokens each "
+                         "through the 8-bit projections, then steps of one token through the 4-bit ones, "
+                         "the paged 8-bit cache and its attention, captured into a HIP graph")
     ap.add_argument("--pmc-summary", nargs=2, metavar=("FETCH_DIR", "WRITE_DIR"),
                     help="summarize rocprofv3 FETCH_SIZE / WRITE_SIZE runs of this script into "
                          "profiles/traffic_<workload>.json and exit")
@@ -328,6 +333,61 @@ def stream_peak(torch, W, lib, names, launches=50):
         torch.cuda.empty_cache()
 
 
+def decode(torch, lib, prompt=1502, steps=64, page=64, layers=3):
+    """Time of a prompt and of a captured single-token step of one decoder layer, beside the bytes that a step
+    cannot do without (4-bit weights and scales, the cache's codes).  Several layers take turns, so that
+    their weights do not stay in the last-level cache."""
+    from w8a8_quantized_linear_amd.decode import random_layer
+    hidden, q_heads, heads, dim, ffn, group = 5120, 40, 8, 128, 17408, 64
+    stack = [random_layer(hidden, q_heads, heads, dim, ffn, group, seed=i) for i in range(layers)]
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    weight_bytes = sum(p.N * (k // 2 + 2 * k // group) for p, k in
+                       ((stack[0].qkv, hidden), (stack[0].o, q_heads * dim), (stack[0].gateup, hidden), (stack[0].down, ffn)))
+
+    def timed(run, n):
+        torch.cuda.synchronize()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for _ in range(n):
+            run()
+        e1.record()
+        torch.cuda.synchronize()
+        return e0.elapsed_time(e1) / (n * layers)
+
+    for seqs in (1, 8, 32):
+        width = -(-(prompt + steps) // page)
+        caches = [lib.kv_cache(seqs * width, heads, page, dim) for _ in stack]
+        table = torch.randperm(seqs * width, generator=gen, device="cuda").view(seqs, width).to(torch.int32)
+        lens = torch.full((seqs,), prompt, dtype=torch.int32, device="cuda")
+        x = torch.randn(seqs, prompt, hidden, generator=gen, device="cuda").to(torch.bfloat16)
+        one = x[:, -1:].contiguous()
+
+        def run(x):
+            for layer, cache in zip(stack, caches):
+                x = layer(x, cache, table, lens)
+            return x
+        prompt_ms = min([timed(lambda: run(x), 1) for _ in range(4)][1:])
+        run(one)
+        torch.cuda.synchronize()
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=side):
+            lens.add_(1)
+            y = run(one)
+        step = []
+        for _ in range(4):
+            lens.fill_(prompt)
+            step.append(timed(graph.replay, steps))
+        step_us = min(step[1:]) * 1e3
+        if not torch.isfinite(y.float()).all():
+            raise RuntimeError("a step's output is not finite")
+        cache_bytes = 2 * seqs * heads * dim * (prompt + steps // 2)
+        print(json.dumps({"decode": "one decoder layer", "sequences": seqs, "prompt_tokens": prompt,
+                          "prompt_ms": prompt_ms, "step_us": step_us, "weight_bytes": weight_bytes,
+                          "cache_bytes": cache_bytes, "step_gbs": (weight_bytes + cache_bytes) / step_us / 1e3,
+                          "config": {"hidden": hidden, "q_heads": q_heads, "heads": heads, "dim": dim, "ffn": ffn,
+                                     "group": group, "page": page, "layers_in_turn": layers}}), flush=True)
+
+
 def lds_patterns(torch, blocks=512, iters=4096, launches=5):
     """Per-launch time of the LDS read-pattern probe (bench-only probe library) for each
     chunk placement, after an untimed launch of each; median of three timed runs."""
@@ -447,6 +507,9 @@ def main():
         return
     if args.lds_patterns:
         lds_patterns(torch)
+        return
+    if args.decode:
+        decode(torch, lib)
         return
     if args.drift:
         import numpy as np
