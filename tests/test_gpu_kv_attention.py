@@ -89,6 +89,44 @@ def test_prompt(lib):
     run(lib, [333, 300], 300, 6, 2, 128, 64, seed=4)
 
 
+# both sizes of the prompt form's workgroups (tables to 1,024 tokens and past them), pieces of a sequence, rows that
+# do not fill a block, groups that straddle one, lengths around a page and a tile, sequences shorter than the call
+@pytest.mark.parametrize("lens,tokens,q_heads,heads,dim,page", (
+    ([700, 699], 65, 2, 2, 128, 32), ([513, 1, 64], 130, 8, 1, 64, 128), ([1300, 40, 0], 200, 4, 2, 64, 16),
+    ([1025], 1025, 2, 1, 128, 128), ([3000, 2999], 70, 3, 1, 128, 64), ([2049], 33, 40, 8, 64, 16), ([127, 129, 128], 129, 5, 1, 64, 32)))
+def test_prompt_shapes(lib, lens, tokens, q_heads, heads, dim, page):
+    run(lib, lens, tokens, q_heads, heads, dim, page, seed=len(lens) + tokens)
+
+
+@pytest.mark.parametrize("dim,page,length", ((64, 16, 600), (128, 64, 1500), (128, 128, 4000)))
+def test_prompt_with_holes_and_pages_of_zeros(lib, dim, page, length):
+    """Holes, pages of zero scales or of scales far apart, and whatever stands where nothing is held."""
+    lens, tokens = [length, length - 37, 90], 100
+    table, pages = tables(lens, page, 3, 8)
+    cache = filled(lib, pages, 2, page, dim, 9)
+    g = torch.Generator(device="cuda").manual_seed(10)
+    cache.v_scale.mul_(2.0 ** torch.randint(-30, 10, cache.v_scale.shape, generator=g, device="cuda"))
+    cache.v_scale[table[0, 1::4].long()] = 0
+    cache.k_scale[table[1, ::3].long()] = 0
+    table[0, 2], table[0, -1], table[1, 0] = -1, pages, 2147483647
+    q = rows_of(3, tokens, 6, dim, 11)
+    y = attend(lib, q, cache, table, lens)
+    check(y, q, cache, table, lens, dim ** -0.5, "prompt with holes")
+    used = torch.zeros(pages, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        ids = table[b, :-(-n // page)].long()
+        used[ids[(ids >= 0) & (ids < pages)]] = True
+    for s in (cache.k_scale, cache.v_scale):
+        s[~used.cuda()] = float("nan")
+    for b, n in enumerate(lens):
+        p = int(table[b, n // page]) if n % page else -1
+        if 0 <= p < pages:
+            cache.k_codes[p, :, n % page:] = 127
+            cache.v_codes[p, :, n % page:] = -127
+    again = attend(lib, q, cache, table, lens)
+    assert torch.equal(again.view(torch.int16), y.view(torch.int16))
+
+
 def test_peaked_scores(lib):
     """Scores of several hundred: one key takes nearly everything, the running maximum moves late."""
     lens, dim, page = [700, 90], 64, 32
@@ -115,6 +153,25 @@ def test_scales_far_apart(lib):
     cache.v_scale[table[2, :4].long()] = 0                   # a sequence whose values are all zeros
     q = rows_of(3, 2, 4, dim, 3)
     check(attend(lib, q, cache, table, lens), q, cache, table, lens, dim ** -0.5, "scales")
+
+
+@pytest.mark.parametrize("tokens", (1, 100))
+@pytest.mark.parametrize("apart", (2.0 ** 20, 2.0 ** 40, 2.0 ** 60))
+def test_large_values_that_are_not_attended(lib, tokens, apart):
+    """A page of values 2^20 and more times the others', first or in the middle, whose keys score far below theirs."""
+    lens, dim, page = [300, 200], 64, 32
+    table, pages = tables(lens, page, 0, 1)
+    cache = filled(lib, pages, 1, page, dim, 2)
+    q = rows_of(1, 1, 2, dim, 3).expand(2, tokens, 2, dim).contiguous()
+    q[:, :, 1] = q[:, :, 0]
+    toward = q[0, 0, 0].sign()
+    cache.k_codes[:] = (toward * 60).to(torch.int8)
+    cache.k_codes[..., ::3] = cache.v_codes[..., ::3] // 2     # (some spread of the scores)
+    cache.k_scale.fill_(0.5)
+    for p in (int(table[0, 0]), int(table[1, 2])):
+        cache.k_codes[p] = (-100 * toward).to(torch.int8)
+        cache.v_scale[p] *= apart
+    check(attend(lib, q, cache, table, lens), q, cache, table, lens, dim ** -0.5, "not attended")
 
 
 @pytest.mark.parametrize("by", (2.0 ** -60, 2.0 ** -20, 2.0 ** 40))

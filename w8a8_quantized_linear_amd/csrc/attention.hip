@@ -8,11 +8,13 @@
 // Arithmetic.  Codes are whole numbers below 128 and exact in f16, so both products run on the f16 matrix
 // cores with fp32 sums: a row of q is scaled by a power of two to below 2^8 (what falls under f16's range
 // is below 2^-32 of the row's largest value); the keys' scale multiplies the fp32 score, and the values' scale rides in
-// the exponent, p' = 2^(s - max + log2(scale) - e), so it costs nothing per element; p' is rounded to f16, 11 bits, and
-// the sum of p' over a page is divided by the scale again.  A page whose values have scale zero (or subnormal: taken
-// for zero) counts as one of scale 2^(e-1) with codes of zero.  The running maximum moves only when a row's
-// score passes it by more than 2^8 (p' stays below 2^15), which spares most steps the rescaling of the outputs
-// and the exchange between lanes.  Maximum, sum and output are fp32.
+// the exponent, p' = 2^(s + log2(scale) - max), so it costs nothing per element; p' is rounded to f16, 11 bits, and
+// the sum of p' over a page is divided by the scale again.  The maximum is a row's own, over s + log2(scale) of what it
+// sees: a key counts by what it adds to the output, however far the scales of pages lie apart, and what f16
+// loses is below 2^-31 of the row's largest p * scale.  A page whose values have a scale below 2^-90 counts as one
+// of that scale with codes of zero.  The running maximum moves only when it is passed by more than 2^8 (p' stays below
+// 2^15), which spares most steps the rescaling of the outputs and the exchange between lanes.  Maximum, sum and
+// output are fp32.
 #include <algorithm>
 
 #include "attention_math.h"
@@ -94,8 +96,12 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
     const int64_t id = (int64_t)(real ? ids : 0) * c.heads + head;
     k_scale = c.k_scale[id];
     v_scale = c.v_scale[id];
-    if (!(v_scale >= 0x1p-126f)) v_scale = 0.0f;
+    if (!(v_scale >= 0x1p-90f)) v_scale = 0.0f; // kLeastLog
     if (!real) v_scale = -1.0f;                 // not seen
+  };
+  auto take_logs = [&]() {                      // (apart from the loads, so as not to wait for them)
+    v_log = v_scale > 0.0f ? __log2f(v_scale) : kLeastLog;
+    v_inv = v_scale > 0.0f ? 1.0f / v_scale : 0x1p90f;
   };
 
   struct Codes {
@@ -136,7 +142,6 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
 #pragma unroll
     for (int b = 0; b < DB; ++b) out[n][b] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  int v_exp = kLeastExp;                        // the values' scales are taken relative to 2^v_exp
 
   auto step = [&](const Codes& x, int t0) __attribute__((always_inline)) {
     // ---- scores S^T: lane 16 h + r, run u: row r, tokens 4 h + i ----
@@ -163,7 +168,6 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
         }
     }
     float rk[2], rv[2], rlog[2], rinv[2];       // the runs' scales, the same for the whole wave
-    int tile_exp = kLeastExp;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int block = min((t0 + 16 * u) >> page_log, last_block) - base;
@@ -171,7 +175,6 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
       rv[u] = t0 + 16 * u < end ? lane_value(v_scale, block) : -1.0f;
       rlog[u] = lane_value(v_log, block);
       rinv[u] = lane_value(v_inv, block);
-      if (rv[u] > 0.0f) tile_exp = max(tile_exp, scale_exp(rv[u]));
     }
     const bool whole = t0 + kTile <= all_seen && rv[0] >= 0.0f && rv[1] >= 0.0f;
     // ---- running softmax; P^T as the second product's operand: lane 16 h + r: row r, tokens 4 h + i of both runs ----
@@ -191,11 +194,11 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
           }
           factor[u] = 1.0f;
         }
-        m = fmaxf(m, fmaxf(fmaxf(s[n][u][0], s[n][u][1]), fmaxf(s[n][u][2], s[n][u][3])) * factor[u]);
+        m = fmaxf(m, __builtin_fmaf(fmaxf(fmaxf(s[n][u][0], s[n][u][1]), fmaxf(s[n][u][2], s[n][u][3])), factor[u], rlog[u]));
       }
-      if (__any(m > top[n] + kLazy) || tile_exp > v_exp) {
+      if (__any(m > top[n] + kLazy)) {
         const float next = fmaxf(max_quarters(m), top[n]), ref = next == -INFINITY ? 0.0f : next;
-        const float scaled = ldexpf(__builtin_amdgcn_exp2f(top[n] - ref), v_exp - max(tile_exp, v_exp));
+        const float scaled = __builtin_amdgcn_exp2f(top[n] - ref);
         sum[n] *= scaled;
 #pragma unroll
         for (int b = 0; b < DB; ++b) out[n][b] *= scaled;
@@ -204,9 +207,8 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
       const float ref = top[n] == -INFINITY ? 0.0f : top[n];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int e = max(tile_exp, v_exp);
-        const bool some = rv[u] > 0.0f;         // zeros count as a scale of 2^(e-1) with codes of zero
-        const float off = (some ? rlog[u] + (float)(kProbExp - e) : (float)(kProbExp - 1)) - ref;
+        const bool some = rv[u] > 0.0f;         // (zeros: codes of zero, whatever they are)
+        const float off = rlog[u] + (kProbExp - ref);
         float add = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
@@ -215,10 +217,9 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
           add += a + b;
           p[n][2 * u + i / 2] = some ? f16_pair(a, b) : 0u;
         }
-        sum[n] = __builtin_fmaf(add, some ? rinv[u] : ldexpf(1.0f, 1 - e), sum[n]);
+        sum[n] = __builtin_fmaf(add, rinv[u], sum[n]);
       }
     }
-    v_exp = max(tile_exp, v_exp);
     // ---- O^T += V^T P^T: block b's operand is byte b of the lane's eight values ----
 #pragma unroll
     for (int b = 0; b < DB; ++b) {
@@ -257,8 +258,7 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
         for (int j = 0; j < 4; ++j)
           qf[n][cc][u][j] = f16_pair(__uint_as_float(qf[n][cc][u][j] << 16) * by, __uint_as_float(qf[n][cc][u][j] & 0xffff0000u) * by);
   }
-  v_log = __log2f(v_scale);
-  v_inv = 1.0f / v_scale;
+  take_logs();
   while (t0 < end) {
 #pragma unroll
     for (int d = 0; d < 2; ++d) {
@@ -271,17 +271,15 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
         ids = next_ids;
         next_ids = load_ids(base + 64);
         load_scales();
-        v_log = __log2f(v_scale);
-        v_inv = 1.0f / v_scale;
+        take_logs();
       }
     }
   }
 
   // ---- the waves' parts meet ----
-  const float back = ldexpf(1.0f, v_exp - kProbExp);
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
-    const float total = sum_quarters(sum[n]) * back;
+    const float total = sum_quarters(sum[n]);
     if (n) __syncthreads();
     if (h == 0) {
       red_max[wave][r] = top[n];
@@ -292,7 +290,7 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) m = fmaxf(m, red_max[w][r]);
     const float ref = m == -INFINITY ? 0.0f : m;
-    const float by = __builtin_amdgcn_exp2f(top[n] - ref) * back;
+    const float by = __builtin_amdgcn_exp2f(top[n] - ref);
 #pragma unroll
     for (int b = 0; b < DB; ++b) red_out[wave][b][lane] = out[n][b] * by;
     __syncthreads();

@@ -15,9 +15,10 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-constexpr float kLazy = 8.0f;                   // log2 of how far scores may pass the running maximum
-constexpr int kProbExp = 7;                     // p' < 2^(kLazy + kProbExp); f16 ends at 2^16
-constexpr int kLeastExp = -80;                  // scales are taken relative to 2^e with at least this e
+constexpr float kLazy = 8.0f;                   // log2 of how far p * scale may pass the running maximum
+constexpr float kProbExp = 7.0f;                // p' < 2^(kLazy + kProbExp); f16 ends at 2^16
+constexpr float kLeastLog = -90.0f;             // values' scales below 2^this count as zero (the sum of p' / scale
+                                                // over 2^30 tokens has to stay in fp32's range)
 constexpr int kPiece = 128;                     // pieces of a sequence are whole multiples of this
 
 // Tokens of each of the `splits` pieces of a sequence.
@@ -50,9 +51,6 @@ __device__ __forceinline__ uint32_t f16_bytes(uint32_t hi, uint32_t lo, int b) {
 
 // The power of two that brings a row of queries whose largest magnitude has these bits into [2^7, 2^8).
 __device__ __forceinline__ int query_exp(uint32_t top_bits) { return min(134 - (int)(top_bits >> 23), 126); }
-
-// The least e (at least kLeastExp) with s < 2^e, for a scale s >= 0.
-__device__ __forceinline__ int scale_exp(float s) { return max((int)(__float_as_uint(s) >> 23) - 126, kLeastExp); }
 
 // The larger (sum) of lanes l and l ^ 32; of lanes l, l ^ 16, l ^ 32 and l ^ 48.  The swaps exchange the odd rows
 // of 16 (the upper half) of one copy with the even rows (the lower half) of the other.

@@ -21,11 +21,10 @@ constexpr int kSubs = kTile / 16;               // 16-token runs: no page bounda
 
 struct Run {
   float k;           // the keys' scale
-  float v_log;       // log2 of the values' scale
+  float v_log;       // log2 of the values' scale (zeros: kLeastLog)
   float v_inv;       // 1 / it
-  int v_exp;         // scale_exp of it; kZeros: the values are all zeros, kNone: the table names no page
+  int real;          // 0: the table names no page
 };
-constexpr int kZeros = -500, kNone = -1000;
 
 // WAVES = 8: 256 rows, waves 0 .. 3 bring the values of a run of 16 tokens each and waves 4 .. 7 the keys.  WAVES = 4: 128
 // rows, two workgroups a CU, each wave brings the keys and values of a run: twice the conversions for every row,
@@ -151,7 +150,7 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
     }
     if (values) {
       const int ch = 2 * stage + v_half;
-      const bool zeros = !(run_v >= 0x1p-126f);
+      const bool zeros = !(run_v >= 0x1p-90f);  // kLeastLog
       if (v_half < 2) {
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -163,9 +162,9 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
         }
       }
       if (lane == 0) {
-        runs[buf][stage].v_log = __log2f(run_v);
-        runs[buf][stage].v_inv = 1.0f / run_v;
-        runs[buf][stage].v_exp = zeros ? run_v == -1.0f ? kNone : kZeros : scale_exp(run_v);
+        runs[buf][stage].v_log = zeros ? kLeastLog : __log2f(run_v);
+        runs[buf][stage].v_inv = zeros ? 0x1p90f : 1.0f / run_v;
+        runs[buf][stage].real = run_v != -1.0f;
       }
     }
   };
@@ -176,7 +175,6 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
 #pragma unroll
     for (int i = 0; i < 16; ++i) out[b][i] = 0.0f;
   float top = -INFINITY, sum = 0.0f;
-  int v_exp = kLeastExp;
 
   // Of 8 waves the keys' convert the next tile before they multiply, the values' after it (their codes are loaded
   // an iteration later), so that the two waves of a SIMD are out of step: one's products run under the other's softmax
@@ -218,22 +216,20 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
       }
       Run run[kSubs];
       float factor[kSubs];
-      int least = 0, tile_exp = kLeastExp;
+      int real = 1;
 #pragma unroll
       for (int u = 0; u < kSubs; ++u) {
         run[u] = runs[buf][u];
         factor[u] = run[u].k * qs;
-        const int e = __builtin_amdgcn_readfirstlane(run[u].v_exp);
-        least = min(least, e);
-        tile_exp = max(tile_exp, e);
+        real &= __builtin_amdgcn_readfirstlane(run[u].real);
       }
-      if (t0 + kTile > all_seen || least == kNone) {             // some row does not see some token
+      if (t0 + kTile > all_seen || !real) {             // some row does not see some token
 #pragma unroll
         for (int u = 0; u < kSubs; ++u) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int key = t0 + 16 * u + 8 * (i / 4) + 4 * h + i % 4;
-            const bool seen = key < end && key <= last_key && run[u].v_exp != kNone;
+            const bool seen = key < end && key <= last_key && run[u].real;
             s[u / 2][8 * (u % 2) + i] = seen ? s[u / 2][8 * (u % 2) + i] * factor[u] : -INFINITY;
           }
           factor[u] = 1.0f;
@@ -245,29 +241,23 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
         float mu = s[u / 2][8 * (u % 2)];
 #pragma unroll
         for (int i = 1; i < 8; ++i) mu = fmaxf(mu, s[u / 2][8 * (u % 2) + i]);
-        m = fmaxf(m, mu * factor[u]);
+        m = fmaxf(m, __builtin_fmaf(mu, factor[u], run[u].v_log));
       }
-      if (__any(m > top + kLazy) || tile_exp > v_exp) {
+      if (__any(m > top + kLazy)) {
         const float next = fmaxf(max_halves(m), top), ref = next == -INFINITY ? 0.0f : next;
-        const int exp = max(tile_exp, v_exp);
-        const float scaled = ldexpf(__builtin_amdgcn_exp2f(top - ref), v_exp - exp);
+        const float scaled = __builtin_amdgcn_exp2f(top - ref);
         sum *= scaled;
 #pragma unroll
         for (int b = 0; b < DB; ++b)
 #pragma unroll
           for (int i = 0; i < 16; ++i) out[b][i] *= scaled;
         top = next;
-        v_exp = exp;
       }
-      const float ref = top == -INFINITY ? 0.0f : top, rest = (float)(kProbExp - v_exp) - ref;
+      const float ref = top == -INFINITY ? 0.0f : top, rest = kProbExp - ref;
       u32x4 p[kSubs];
 #pragma unroll
       for (int u = 0; u < kSubs; ++u) {
-        float off = run[u].v_log + rest, inv = run[u].v_inv;
-        if (least <= kZeros && run[u].v_exp <= kZeros) {        // as a scale of 2^(v_exp - 1)
-          off = (float)(kProbExp - 1) - ref;
-          inv = ldexpf(1.0f, 1 - v_exp);
-        }
+        const float off = run[u].v_log + rest;
         float add = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
@@ -276,7 +266,7 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
           add += a + b;
           p[u][i / 2] = f16_pair(a, b);
         }
-        sum = __builtin_fmaf(add, inv, sum);
+        sum = __builtin_fmaf(add, run[u].v_inv, sum);
       }
 #pragma unroll
       for (int u = 0; u < kSubs; ++u)
@@ -294,8 +284,7 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
   // ---- outputs: register i of block b is dim 32 b + 8 (i / 4) + 4 h + i % 4 ----
   sum = sum_halves(sum);
   if (row0 + r >= rows) return;
-  const float back = ldexpf(1.0f, v_exp - kProbExp);
-  const float by = splits == 1 ? (sum > 0.0f ? 1.0f / sum : 0.0f) : back;
+  const float by = splits == 1 ? (sum > 0.0f ? 1.0f / sum : 0.0f) : 1.0f;
   const int64_t index = ((seq * c.heads + head) * rows + row) * splits + split;
   uint16_t* dst = y + ((seq * tokens + row / group) * c.heads * group + head * group + row % group) * DIM;
 #pragma unroll
@@ -311,7 +300,7 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
     }
   if (splits > 1 && h == 0) {
     part.stat[2 * index] = top;
-    part.stat[2 * index + 1] = sum * back;
+    part.stat[2 * index + 1] = sum;
   }
 }
 
