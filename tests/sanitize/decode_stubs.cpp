@@ -22,7 +22,7 @@ hipError_t launch_kv_append(const KvCache&, const uint16_t*, int64_t, const uint
 hipError_t launch_kv_read(const KvCache&, int64_t, int64_t, uint16_t*, uint16_t*, hipStream_t) {
   return hipErrorInvalidValue;
 }
-int64_t kv_attention_splits(int64_t, int64_t, int, int, int, int64_t) { return 2; }
+int64_t kv_attention_splits(int64_t, int64_t, int, int, int, int, int64_t) { return 2; }
 hipError_t launch_kv_attention(const KvCache&, const uint16_t*, int64_t, int64_t, int64_t, int, float, uint16_t*,
                                void*, hipStream_t) {
   return hipErrorInvalidValue;

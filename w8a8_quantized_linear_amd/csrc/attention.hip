@@ -394,7 +394,7 @@ hipError_t launch_all(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t 
                       int64_t splits, uint16_t* y, Partial part, hipStream_t stream) {
   const int64_t rows = tokens * group, all = seqs * c.heads * rows;
   hipError_t e;
-  if (prompt_rows(rows)) e = launch_prompt<DIM>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
+  if (prompt_rows(rows)) e = launch_prompt<DIM>(c, q, ldq, seqs, tokens, group, scale, prompt_cut(seqs, rows, tokens, c.heads, DIM, c.width * c.page), y, part, stream);
   else if (blocks_of(rows) == 1) e = launch<DIM, 1>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
   else if (blocks_of(rows) == 2) e = launch<DIM, 2>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
   else e = launch<DIM, 4>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
@@ -409,21 +409,9 @@ hipError_t launch_all(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t 
 
 }  // namespace
 
-int64_t kv_attention_splits(int64_t seqs, int64_t tokens, int q_heads, int heads, int page, int64_t width) {
+int64_t kv_attention_splits(int64_t seqs, int64_t tokens, int q_heads, int heads, int dim, int page, int64_t width) {
   const int64_t rows = tokens * (q_heads / heads);
-  const int64_t most = (width * page + kPiece - 1) / kPiece;
-  if (prompt_rows(rows)) {
-    // 256 rows fit a CU: the cut that leaves the fewest rounds of 256, a piece more costing a twentieth
-    // (its partial results pass through memory)
-    const int64_t tile = prompt_rows_of(width * page), one = (seqs * heads * ((rows + tile - 1) / tile) * tile + 255) / 256;
-    int64_t best = 1;
-    double least = 0.0;
-    for (int64_t s = 1; s <= std::min<int64_t>(8, most); ++s) {
-      const double cost = (double)((one * s + 255) / 256) / (double)s * (1.0 + 0.05 * (double)(s - 1));
-      if (s == 1 || cost < least) best = s, least = cost;
-    }
-    return best;
-  }
+  if (prompt_rows(rows)) return prompt_cut(seqs, rows, tokens, heads, dim, width * page).splits;
   // a workgroup for each of the 256 CUs (32 sequences up to 2,270 tokens: 25.3 us, with twice as many 27.2 us, with
   // four times 29.7 us; one of 131,072: 52.9, 55.5 and 59.0 us), but one piece alone up to 512 tokens of a full table (a
   // step of 128 takes less than the combination's 3 us) and no piece below 256
@@ -434,7 +422,7 @@ int64_t kv_attention_splits(int64_t seqs, int64_t tokens, int q_heads, int heads
 
 hipError_t launch_kv_attention(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs, int64_t tokens,
                                int q_heads, float scale, uint16_t* y, void* workspace, hipStream_t stream) {
-  const int64_t splits = kv_attention_splits(seqs, tokens, q_heads, c.heads, c.page, c.width);
+  const int64_t splits = kv_attention_splits(seqs, tokens, q_heads, c.heads, c.dim, c.page, c.width);
   Partial part{nullptr, nullptr};
   if (splits > 1) {
     part.out = static_cast<float*>(workspace);

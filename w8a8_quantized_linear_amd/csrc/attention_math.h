@@ -81,13 +81,15 @@ struct Partial {
   float* stat;
 };
 
-// Prompt form (attention_prompt.hip): query rows of a workgroup, by the longest sequence that the table can hold.  2 x 84
-// tokens (12/4 heads of 128): 10.5 us with 128 rows, 14.5 us with 256; 636 tokens (16/2 of 64) 18.0 and 20.0 us; 4 x 1,502
-// (40/8 of 128) 148 and 146 us; 500 behind 12,016 (32/8) 141 and 130 us.
-inline int prompt_rows_of(int64_t length) { return length <= 1024 ? 128 : 256; }
+// Prompt form (attention_prompt.hip): query rows of a workgroup (128 or 256) and pieces of a sequence.
+struct PromptCut {
+  int rows;
+  int64_t splits;
+};
+PromptCut prompt_cut(int64_t seqs, int64_t rows, int64_t tokens, int heads, int dim, int64_t length);
 template <int DIM>
 hipError_t launch_prompt(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs, int64_t tokens, int group,
-                         float scale, int64_t splits, uint16_t* y, Partial part, hipStream_t stream);
+                         float scale, PromptCut cut, uint16_t* y, Partial part, hipStream_t stream);
 
 }  // namespace kva
 }  // namespace w8a8

@@ -10,6 +10,8 @@
 // The units overlap only in part (two waves of a SIMD, one with products and one with multiply-adds, together take
 // 0.71 of the sum of their times; products and exponentials overlap fully, measured), so ~1,500 is what a tile
 // could take; it takes 2,800: two waves a SIMD leave waits for LDS, for the products and at the barrier.
+#include <algorithm>
+
 #include "attention_math.h"
 
 namespace w8a8 {
@@ -306,21 +308,51 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
 
 }  // namespace
 
+// What a cut takes, in microseconds as measured (dim 128; 64 in proportion): a workgroup takes 4 and, for a tile
+// of 64 tokens, 1.8 with 128 rows alone on its CU, 3.1 with two of them there, 2.5 with 256 rows; the pieces'
+// results take 5 and their bytes twice at 4 TB/s.  The longest a table can hold stands for every sequence, and
+// a row of a prompt sees half of the prompt.  (400 tokens of 633, 40/8 heads: one piece 25 us, two 31; 64 of 2,000, 32/8: 63
+// us in one, 22 in eight pieces of 128 rows, 26 of 256; 500 of 12,016, 32/8: 135 us in four of 128, 121 of 256; 100 of
+// 20,000, 16/4: 84 us in eight, 52 in sixteen.)
+PromptCut prompt_cut(int64_t seqs, int64_t rows, int64_t tokens, int heads, int dim, int64_t length) {
+  const double by_dim = dim / 128.0;
+  const double seen = 1.0 - 0.5 * (double)std::min(tokens, length) / (double)length;
+  PromptCut best{0, 0};
+  double least = 0.0;
+  for (int tile = 128; tile <= 256; tile *= 2) {
+    const int64_t one = seqs * heads * ((rows + tile - 1) / tile);
+    for (int64_t s = 1; s <= 32; ++s) {
+      const int64_t piece = piece_of((int)length, (int)s);
+      if (s > 1 && (s - 1) * piece >= length) continue;       // no more pieces than with fewer
+      const int64_t n = one * s;
+      const double tiles = (double)((piece + kTile - 1) / kTile);
+      // (two on a CU, until the one of fewer tiles ends)
+      const double per = tile == 256 ? 0.8 + 1.7 * by_dim : 0.9 + 0.9 * by_dim + (n > 256 ? seen * (0.1 + 1.2 * by_dim) : 0.0);
+      const double slots = tile == 256 ? 256.0 : 512.0;
+      const double whole = 4.0 + tiles * per, all = (double)n * (4.0 + tiles * seen * per) / slots;
+      const double join = s > 1 ? 5.0 + 2.0 * (double)(seqs * heads * rows * s) * dim * 4.0 / 4e6 : 0.0;
+      const double cost = std::max(whole, all) + join;
+      if (!best.rows || cost < least) best = {tile, s}, least = cost;
+    }
+  }
+  return best;
+}
+
 template <int DIM>
 hipError_t launch_prompt(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs, int64_t tokens, int group,
-                         float scale, int64_t splits, uint16_t* y, Partial part, hipStream_t stream) {
-  const int rows = prompt_rows_of(c.width * c.page);
-  const int64_t tiles = (tokens * group + rows - 1) / rows, total = seqs * c.heads * tiles * splits;
+                         float scale, PromptCut cut, uint16_t* y, Partial part, hipStream_t stream) {
+  const int rows = cut.rows;
+  const int64_t tiles = (tokens * group + rows - 1) / rows, total = seqs * c.heads * tiles * cut.splits;
   if (total > 0x7fffffff) return hipErrorInvalidValue;
   const auto kernel = rows == 256 ? kv_prompt_kernel<DIM, 8> : kv_prompt_kernel<DIM, 4>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)total), dim3(2 * rows), 0, stream, c, q, ldq, (int)tokens, group, scale, (int)splits,
+  hipLaunchKernelGGL(kernel, dim3((unsigned)total), dim3(2 * rows), 0, stream, c, q, ldq, (int)tokens, group, scale, (int)cut.splits,
                      (int)tiles, (int)total, y, part);
   return hipGetLastError();
 }
 
-template hipError_t launch_prompt<64>(const KvCache&, const uint16_t*, int64_t, int64_t, int64_t, int, float, int64_t,
+template hipError_t launch_prompt<64>(const KvCache&, const uint16_t*, int64_t, int64_t, int64_t, int, float, PromptCut,
                                       uint16_t*, Partial, hipStream_t);
-template hipError_t launch_prompt<128>(const KvCache&, const uint16_t*, int64_t, int64_t, int64_t, int, float, int64_t,
+template hipError_t launch_prompt<128>(const KvCache&, const uint16_t*, int64_t, int64_t, int64_t, int, float, PromptCut,
                                        uint16_t*, Partial, hipStream_t);
 
 }  // namespace kva

@@ -38,7 +38,7 @@ hipError_t launch_kv_read(const KvCache& c, int64_t seqs, int64_t length, uint16
 
 // Attention over the cache (attention.hip).  kv_attention_splits: the number of
 // pieces that each sequence's tokens are cut into (1: no workspace is used).
-int64_t kv_attention_splits(int64_t seqs, int64_t tokens, int q_heads, int heads, int page, int64_t width);
+int64_t kv_attention_splits(int64_t seqs, int64_t tokens, int q_heads, int heads, int dim, int page, int64_t width);
 hipError_t launch_kv_attention(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs, int64_t tokens,
                                int q_heads, float scale, uint16_t* y, void* workspace, hipStream_t stream);
 

@@ -137,7 +137,7 @@ size_t w8a8_kv_attention_workspace_bytes(int64_t seqs, int64_t tokens, int64_t q
   if (seqs == 0 || tokens < 1 || tokens > W8A8_KV_MAX_TOKENS || q_heads < heads || q_heads > W8A8_KV_MAX_HEADS ||
       q_heads % heads != 0)
     return 0;
-  const int64_t splits = w8a8::kv_attention_splits(seqs, tokens, (int)q_heads, (int)heads, (int)page, width);
+  const int64_t splits = w8a8::kv_attention_splits(seqs, tokens, (int)q_heads, (int)heads, (int)dim, (int)page, width);
   return splits == 1 ? 0 : align256((size_t)(seqs * tokens * q_heads * splits) * (size_t)(dim + 2) * sizeof(float));
 }
 
