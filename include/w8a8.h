@@ -312,8 +312,8 @@ w8a8_status w8a8_w4_pack(const uint8_t* codes, const uint16_t* scales, int64_t N
 
 /* y[m][n] = bf16( sum over groups of scale * sum(x * code) + bias[n] ), fp32 sums,
  * one rounding.  x bf16 [M, K], bias bf16 [N] or NULL, y bf16 [M, N].  N % 8 == 0,
- * 0 <= M <= W8A8_W4_MAX_M.  Made for M up to 64, where one pass over the weight
- * serves every token; larger M is computed 64 tokens at a time.  A token's
+ * 0 <= M <= W8A8_W4_MAX_M.  Made for M up to 64; larger M is computed in blocks of
+ * 32 or 64 tokens, each of which passes over the weight again.  A token's
  * result does not depend on the others in the call, nor on their number.  The
  * workspace holds fp32 partial sums where K is long and N small, so that K is cut;
  * w8a8_w4_workspace_bytes is 0, and workspace may be NULL, where it is not. */
@@ -351,6 +351,9 @@ w8a8_status w8a8_w4_linear(const uint16_t* x, const uint8_t* codes_packed, const
  * receives some: scale = max(old scale if the page holds earlier tokens of the
  * sequence, amax / 127 of the new values), held codes become
  * round-half-even(code * (old / new scale)), new ones round-half-even(x / scale).
+ * A scale of a page that holds nothing from before is not read: a cache needs no
+ * initialisation.  Values are taken as finite: a NaN or an infinity spoils the
+ * codes of its page and head (of no other).
  * Filling a page in one call rounds each value once; token by token, a page's
  * earlier codes are rounded again whenever a larger value arrives (each time by
  * at most half a step of the new scale). */
@@ -369,7 +372,10 @@ w8a8_status w8a8_kv_read(const int8_t* k_codes, const float* k_scale, const int8
 /* Attention of the last `tokens` tokens of every sequence over what it holds:
  * query i is at position p = lens - tokens + i and sees keys 0 .. p,
  *   y = sum_j exp(scale * q.k_j - max) v_j / sum_j exp(scale * q.k_j - max);
- * a query that sees no key (p < 0, an empty sequence) gives zeros.  q: rows
+ * a query that sees no key (p < 0, an empty sequence) gives zeros.  Scales are not
+ * negative, as append makes them; values of a page whose scale is below 2^-90 count
+ * as zeros.  What lies in pages or rows that a sequence does not hold is not
+ * used, NaN included.  q: rows
  * [seqs * tokens] of [q_heads, dim] bf16, ldq elements apart (>= q_heads * dim, a
  * multiple of 8); q_heads % heads == 0, query head a reads cache head
  * a / (q_heads / heads).  y bf16 [seqs, tokens, q_heads, dim], dense.  scale is

@@ -1,4 +1,6 @@
-"""Python binding of the MI355X W8A8 quantized projection library (``libw8a8.so``).
+"""Python binding of the MI355X W8A8 quantized projection library (``libw8a8.so``),
+with its operators for few tokens: 4-bit-weight projections, a paged 8-bit cache
+of keys and values, and attention over it.
 
 The functions below carry the names of the C entry points declared in
 ``include/w8a8.h`` and only marshal arguments: they check dtypes/devices,

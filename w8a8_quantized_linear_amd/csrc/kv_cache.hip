@@ -10,7 +10,9 @@
 // and the new ones are RNE(x / s), the library's per-token rule with the scale of a block.  All steps are
 // single fp32 operations, so the codes are the same on every run and machine.
 //
-// Bound: memory traffic (2 bytes read and 1 written per new value) and, for single tokens, latency.
+// Bound: memory traffic (append 2 bytes read and 1 written per value, read 1 and 2) and, for single tokens,
+// latency.  8 sequences of 1,502 tokens (8 heads of 128): append 17.8 us (4.1 TB/s), read 16.2 us (4.6 TB/s; a copy of
+// 2 GiB reaches 4.9); one token for each of 61 sequences of up to 299 tokens 4.2 us, their read 8.9 us.
 #include "decode.h"
 #include "epilogue_math.h"
 #include "quant_math.h"
