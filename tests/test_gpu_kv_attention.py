@@ -98,6 +98,69 @@ def test_prompt_shapes(lib, lens, tokens, q_heads, heads, dim, page):
     run(lib, lens, tokens, q_heads, heads, dim, page, seed=len(lens) + tokens)
 
 
+def long_table(table, seqs, rows, heads, page, seed=77):
+    """The table with columns past every sequence, named at random, until there is work for the prompt form."""
+    width = -(-2 * (256 * 16 * 1536 * 2 + 1) // (rows * seqs * heads * page))
+    more = torch.randint(-5, 10 ** 6, (table.shape[0], max(width - table.shape[1], 0)), generator=torch.Generator().manual_seed(seed), dtype=torch.int32)
+    return torch.cat((table, more), 1)
+
+
+# the same shapes in the prompt form, whose pieces are then mostly empty, and shapes that are large enough by themselves
+@pytest.mark.parametrize("lens,tokens,q_heads,heads,dim,page", (
+    ([700, 699], 65, 2, 2, 128, 32), ([513, 1, 64], 130, 8, 1, 64, 128), ([1300, 40, 0], 200, 4, 2, 64, 16),
+    ([1025], 1025, 2, 1, 128, 128), ([3000, 2999], 70, 3, 1, 128, 64), ([2049], 33, 40, 8, 64, 16), ([127, 129, 128], 129, 5, 1, 64, 32),
+    ([1300, 900], 900, 8, 2, 64, 32), ([1200], 1150, 10, 2, 128, 64), ([1030, 1, 1029], 700, 6, 2, 128, 16)))
+def test_prompt_form(lib, lens, tokens, q_heads, heads, dim, page):
+    say(f"prompt form lens={lens} tokens={tokens} heads={q_heads}/{heads} dim={dim} page={page}")
+    table, pages = tables(lens, page, 2, 5)
+    table = long_table(table, len(lens), tokens * q_heads // heads, heads, page)
+    cache = filled(lib, pages, heads, page, dim, 6)
+    q = rows_of(len(lens), tokens, q_heads, dim, 7, by=2.0)
+    y = attend(lib, q, cache, table, lens)
+    check(y, q, cache, table, lens, dim ** -0.5, "prompt form")
+
+
+@pytest.mark.parametrize("dim,page,length", ((64, 16, 600), (128, 64, 1500)))
+def test_prompt_form_with_holes_and_pages_of_zeros(lib, dim, page, length):
+    lens, tokens = [length, length - 37, 90], 100
+    table, pages = tables(lens, page, 3, 8)
+    cache = filled(lib, pages, 2, page, dim, 9)
+    g = torch.Generator(device="cuda").manual_seed(10)
+    cache.v_scale.mul_(2.0 ** torch.randint(-30, 10, cache.v_scale.shape, generator=g, device="cuda"))
+    cache.v_scale[table[0, 1::4].long()] = 0
+    cache.k_scale[table[1, ::3].long()] = 0
+    table[0, 2], table[1, 0] = -1, 2147483647
+    used = torch.zeros(pages, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        ids = table[b, :-(-n // page)].long()
+        used[ids[(ids >= 0) & (ids < pages)]] = True
+    table = long_table(table, 3, 300, 2, page)
+    q = rows_of(3, tokens, 6, dim, 11)
+    y = attend(lib, q, cache, table, lens)
+    check(y, q, cache, table, lens, dim ** -0.5, "prompt form with holes")
+    for s in (cache.k_scale, cache.v_scale):
+        s[~used.cuda()] = float("nan")
+    assert torch.equal(attend(lib, q, cache, table, lens).view(torch.int16), y.view(torch.int16))
+
+
+@pytest.mark.parametrize("apart", (2.0 ** 20, 2.0 ** 60))
+def test_prompt_form_and_large_values_that_are_not_attended(lib, apart):
+    lens, dim, page, tokens = [300, 200], 64, 32, 100
+    table, pages = tables(lens, page, 0, 1)
+    cache = filled(lib, pages, 1, page, dim, 2)
+    q = rows_of(1, 1, 2, dim, 3).expand(2, tokens, 2, dim).contiguous()
+    q[:, :, 1] = q[:, :, 0]
+    toward = q[0, 0, 0].sign()
+    cache.k_codes[:] = (toward * 60).to(torch.int8)
+    cache.k_codes[..., ::3] = cache.v_codes[..., ::3] // 2
+    cache.k_scale.fill_(0.5)
+    for p in (int(table[0, 0]), int(table[1, 2])):
+        cache.k_codes[p] = (-100 * toward).to(torch.int8)
+        cache.v_scale[p] *= apart
+    table = long_table(table, 2, 2 * tokens, 1, page)
+    check(attend(lib, q, cache, table, lens), q, cache, table, lens, dim ** -0.5, "not attended")
+
+
 @pytest.mark.parametrize("dim,page,length", ((64, 16, 600), (128, 64, 1500), (128, 128, 4000)))
 def test_prompt_with_holes_and_pages_of_zeros(lib, dim, page, length):
     """Holes, pages of zero scales or of scales far apart, and whatever stands where nothing is held."""

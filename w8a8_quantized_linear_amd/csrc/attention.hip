@@ -87,8 +87,10 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
   const int64_t page_bytes = (int64_t)c.heads * c.page * DIM;
   const int64_t head_bytes = (int64_t)head * c.page * DIM;
   const int last_block = max(end - 1, 0) >> page_log;
-  int base = begin >> page_log;                 // the blocks in hand: base .. base + 63, then the next 64
-  auto load_ids = [&](int b) { return table[min(b + lane, last_block)]; };
+  // the blocks in hand: base .. base + 63, then the next 64 (of a short table all, so that loading them does not
+  // wait for the length)
+  int base = c.width <= 64 ? 0 : begin >> page_log;
+  auto load_ids = [&](int b) { return table[min(b + lane, (int)c.width - 1)]; };
   int32_t ids = load_ids(base), next_ids = load_ids(base + 64);
   float k_scale, v_scale, v_log, v_inv;         // of the blocks in hand
   auto load_scales = [&]() {
@@ -374,9 +376,18 @@ kv_combine_kernel(int64_t all, int rows, int heads, int group, int splits, uint1
   *reinterpret_cast<u32x2*>(dst) = u32x2{bf16x2_rne(o[0] * inv, o[1] * inv), bf16x2_rne(o[2] * inv, o[3] * inv)};
 }
 
-// Blocks of 16 rows of a workgroup; rows past 64 take the prompt form.
-int blocks_of(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
-bool prompt_rows(int64_t rows) { return rows > 64; }
+// Blocks of 16 rows of a workgroup: two read the codes once for both, one leaves more workgroups and shorter steps.
+// Two where a CU has more than 256 tokens of a cache head to read (64 rows: 8 x 8,000 tokens of 8 heads 32 against 40 us,
+// 30,000 of 4 heads 22.7 and 24.7 us; but 500 of 8 heads 12.7 and 9.2 us, 8 x 1,500 of 4 heads 14.8 and 12.4 us; four blocks
+// were never faster than two).
+int blocks_of(int64_t rows, int64_t head_tokens) { return rows > 16 && head_tokens > 256 * 256 ? 2 : 1; }
+// The prompt form, from 65 rows on and where every CU has more than 16 rows against 1,536 tokens that they see (at 128
+// dims): below, its few long workgroups take longer (500 tokens of 8/8 heads 17.7 against 9.4 us here, 40 of 500 of 32/8
+// 14.0 and 9.3, 64 of 2,000 22.3 and 18.4, 1,502 of 2/2 22.4 and 19.4, 636 of 16/2 of 64 18.7 and 10.5; but 20 tokens of
+// 4 x 4,000 26.6 against 35 us, 400 of 633 of 40/8 25.6 and 26.1).
+bool prompt_form(int64_t rows, int64_t tokens, int64_t head_tokens, int64_t length, int dim) {
+  return rows > 64 && (double)rows * (double)head_tokens * seen_of(tokens, length) * dim > 256.0 * 16 * 1536 * 128;
+}
 
 template <int DIM, int NB>
 hipError_t launch(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs, int64_t tokens, int group, float scale,
@@ -392,12 +403,11 @@ hipError_t launch(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs
 template <int DIM>
 hipError_t launch_all(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs, int64_t tokens, int group, float scale,
                       int64_t splits, uint16_t* y, Partial part, hipStream_t stream) {
-  const int64_t rows = tokens * group, all = seqs * c.heads * rows;
+  const int64_t rows = tokens * group, all = seqs * c.heads * rows, head_tokens = seqs * c.heads * c.width * c.page;
   hipError_t e;
-  if (prompt_rows(rows)) e = launch_prompt<DIM>(c, q, ldq, seqs, tokens, group, scale, prompt_cut(seqs, rows, tokens, c.heads, DIM, c.width * c.page), y, part, stream);
-  else if (blocks_of(rows) == 1) e = launch<DIM, 1>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
-  else if (blocks_of(rows) == 2) e = launch<DIM, 2>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
-  else e = launch<DIM, 4>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
+  if (prompt_form(rows, tokens, head_tokens, c.width * c.page, DIM)) e = launch_prompt<DIM>(c, q, ldq, seqs, tokens, group, scale, prompt_cut(seqs, rows, tokens, c.heads, DIM, c.width * c.page), y, part, stream);
+  else if (blocks_of(rows, head_tokens) == 1) e = launch<DIM, 1>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
+  else e = launch<DIM, 2>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
   if (e != hipSuccess || splits == 1) return e;
   // a workgroup a row while those fit the GPU's 256 CUs a few times over
   const bool wide = all <= 2048;
@@ -410,12 +420,12 @@ hipError_t launch_all(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t 
 }  // namespace
 
 int64_t kv_attention_splits(int64_t seqs, int64_t tokens, int q_heads, int heads, int dim, int page, int64_t width) {
-  const int64_t rows = tokens * (q_heads / heads);
-  if (prompt_rows(rows)) return prompt_cut(seqs, rows, tokens, heads, dim, width * page).splits;
+  const int64_t rows = tokens * (q_heads / heads), most_tokens = width * page, head_tokens = seqs * heads * most_tokens;
+  if (prompt_form(rows, tokens, head_tokens, most_tokens, dim)) return prompt_cut(seqs, rows, tokens, heads, dim, most_tokens).splits;
   // a workgroup for each of the 256 CUs (32 sequences up to 2,270 tokens: 25.3 us, with twice as many 27.2 us, with
   // four times 29.7 us; one of 131,072: 52.9, 55.5 and 59.0 us), but one piece alone up to 512 tokens of a full table (a
   // step of 128 takes less than the combination's 3 us) and no piece below 256
-  const int64_t tile = 16 * blocks_of(rows), one = seqs * heads * ((rows + tile - 1) / tile), most_tokens = width * page;
+  const int64_t tile = 16 * blocks_of(rows, head_tokens), one = seqs * heads * ((rows + tile - 1) / tile);
   if (most_tokens <= 512) return 1;
   return std::max<int64_t>(1, std::min<int64_t>((256 + one - 1) / one, most_tokens / 256));
 }

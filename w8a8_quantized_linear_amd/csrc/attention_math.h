@@ -81,6 +81,11 @@ struct Partial {
   float* stat;
 };
 
+// The part of `length` tokens that the last `tokens` of them see on average.
+inline double seen_of(int64_t tokens, int64_t length) {
+  return tokens < length ? 1.0 - 0.5 * (double)tokens / (double)length : 0.5;
+}
+
 // Prompt form (attention_prompt.hip): query rows of a workgroup (128 or 256) and pieces of a sequence.
 struct PromptCut {
   int rows;

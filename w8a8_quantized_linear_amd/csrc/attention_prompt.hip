@@ -1,4 +1,4 @@
-// Attention over the paged 8-bit cache for many query rows: prompts and pieces of prompts.
+// Attention over the paged 8-bit cache for prompts and long pieces of prompts: many query rows, much work.
 //
 // The mathematics is that of attention.hip.  Here the arithmetic bounds the time, not the cache's bytes, so a
 // workgroup turns each tile of 64 tokens of codes into f16 once, in LDS, for all its query rows (32 a wave): keys
@@ -317,7 +317,7 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
 // 20,000, 16/4: 84 us in eight, 52 in sixteen.)
 PromptCut prompt_cut(int64_t seqs, int64_t rows, int64_t tokens, int heads, int dim, int64_t length) {
   const double by_dim = dim / 128.0;
-  const double seen = 1.0 - 0.5 * (double)std::min(tokens, length) / (double)length;
+  const double seen = seen_of(tokens, length);
   PromptCut best{0, 0};
   double least = 0.0;
   for (int tile = 128; tile <= 256; tile *= 2) {
