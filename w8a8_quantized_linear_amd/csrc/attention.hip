@@ -422,12 +422,14 @@ hipError_t launch_all(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t 
 int64_t kv_attention_splits(int64_t seqs, int64_t tokens, int q_heads, int heads, int dim, int page, int64_t width) {
   const int64_t rows = tokens * (q_heads / heads), most_tokens = width * page, head_tokens = seqs * heads * most_tokens;
   if (prompt_form(rows, tokens, head_tokens, most_tokens, dim)) return prompt_cut(seqs, rows, tokens, heads, dim, most_tokens).splits;
-  // a workgroup for each of the 256 CUs (32 sequences up to 2,270 tokens: 25.3 us, with twice as many 27.2 us, with
-  // four times 29.7 us; one of 131,072: 52.9, 55.5 and 59.0 us), but one piece alone up to 512 tokens of a full table (a
-  // step of 128 takes less than the combination's 3 us) and no piece below 256
+  // as many workgroups as make one round of the 256 CUs (32 sequences up to 2,270 tokens: 25.3 us, with twice as many
+  // 27.2 us; one of 131,072: 52.9 and 55.5 us; 5 of 4,043, 24/8 heads: 15.0 us in 6 pieces, 17.4 in 7, which are 280), two
+  // of them a CU for 64 dims, whose steps have half the bytes in flight (12 of 8,000, 32/4 heads: 16.9 and 14.3 us); but
+  // one piece alone up to 512 tokens of a full table (a step of 128 takes less than the combination's 3 us) and no piece
+  // below 256
   const int64_t tile = 16 * blocks_of(rows, head_tokens), one = seqs * heads * ((rows + tile - 1) / tile);
   if (most_tokens <= 512) return 1;
-  return std::max<int64_t>(1, std::min<int64_t>((256 + one - 1) / one, most_tokens / 256));
+  return std::max<int64_t>(1, std::min<int64_t>((dim == 64 ? 512 : 256) / one, most_tokens / 256));
 }
 
 hipError_t launch_kv_attention(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs, int64_t tokens,
