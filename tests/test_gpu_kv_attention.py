@@ -105,6 +105,34 @@ def long_table(table, seqs, rows, heads, page, seed=77):
     return torch.cat((table, more), 1)
 
 
+# two blocks of 16 rows a workgroup: 17 to 64 rows and tables for many tokens, in pieces and (many sequences) in one
+@pytest.mark.parametrize("lens,tokens,q_heads,heads,dim,page,width", (
+    ([700, 5, 0], 5, 10, 2, 64, 32, 700), ([1500, 129], 4, 16, 2, 128, 64, 400), ([3000], 3, 6, 1, 64, 128, 520),
+    ([333, 40, 1300], 9, 7, 1, 128, 16, 1500), ([9, 300] * 70, 5, 12, 2, 64, 16, 40), ([200] * 130, 17, 2, 2, 128, 64, 6)))
+def test_two_blocks_of_rows(lib, lens, tokens, q_heads, heads, dim, page, width):
+    assert len(lens) * heads * width * page > 256 * 256 and 16 < tokens * q_heads // heads <= 64
+    say(f"two blocks lens={lens[:3]} tokens={tokens} heads={q_heads}/{heads} dim={dim} page={page}")
+    table, pages = tables(lens, page, 0, 5)
+    more = torch.randint(-5, 10 ** 6, (len(lens), width - table.shape[1]), generator=torch.Generator().manual_seed(6), dtype=torch.int32)
+    table = torch.cat((table, more), 1)
+    cache = filled(lib, pages, heads, page, dim, 6)
+    q = rows_of(len(lens), tokens, q_heads, dim, 7, by=2.0)
+    check(attend(lib, q, cache, table, lens), q, cache, table, lens, dim ** -0.5, "two blocks")
+
+
+# eight waves on one piece, one piece of four waves, pieces: lengths about the limits of the rules, holes among the pages
+@pytest.mark.parametrize("dim,page", ((64, 16), (64, 128), (128, 32), (128, 64)))
+@pytest.mark.parametrize("seqs,heads,length", ((3, 2, 1024), (3, 2, 1040), (2, 4, 1536), (2, 4, 1600), (9, 15, 500), (9, 16, 640), (70, 4, 256), (5, 1, 130)))
+def test_forms_of_few_rows(lib, seqs, heads, length, dim, page):
+    say(f"few rows seqs={seqs} heads={heads} length={length} dim={dim} page={page}")
+    lens = [max(length - 37 * b, 0) if b % 4 else length for b in range(seqs)]
+    table, pages = tables(lens, page, 0, seqs)
+    table[0, 0] = -1
+    cache = filled(lib, pages, heads, page, dim, 3)
+    q = rows_of(seqs, 2, 2 * heads, dim, 4, by=2.0)
+    check(attend(lib, q, cache, table, lens), q, cache, table, lens, dim ** -0.5, "few rows")
+
+
 # the same shapes in the prompt form, whose pieces are then mostly empty, and shapes that are large enough by themselves
 @pytest.mark.parametrize("lens,tokens,q_heads,heads,dim,page", (
     ([700, 699], 65, 2, 2, 128, 32), ([513, 1, 64], 130, 8, 1, 64, 128), ([1300, 40, 0], 200, 4, 2, 64, 16),

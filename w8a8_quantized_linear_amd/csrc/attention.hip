@@ -24,31 +24,32 @@ namespace {
 
 using namespace kva;
 
-constexpr int kWaves = 4;
 constexpr int kTile = 32;                       // tokens of a wave's step: two runs of 16
-constexpr int kStep = kWaves * kTile;           // pieces of a sequence are whole steps of a workgroup
-static_assert(kPiece % kStep == 0, "pieces are whole steps");
+static_assert(kPiece % (4 * kTile) == 0, "pieces are whole steps of four waves");
 
 __device__ __forceinline__ float lane_value(float v, int lane) {
   return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
 }
 
 // One workgroup: 16 * NB query rows (tokens x the heads that share a cache head) against one piece of a
-// sequence; its waves take every fourth step of 32 tokens and meet in LDS.  Bound by the cache's bytes where the
+// sequence; its W waves take the steps of 32 tokens in turn and meet in LDS.  Bound by the cache's bytes where the
 // sequences are long, by latency where they are short (length -> table -> codes -> scores -> outputs), so a wave has
 // the next step's codes in flight while it computes, keeps the pages and scales of 64 blocks in a register each
 // (lane i: block i) instead of LDS, and waits for no other wave before the end.  MFMA 16x16x32 f16:
 //   S^T = K Q^T: a lane's 16 bytes of a key are two operands as they come from memory;
 //   O^T += V^T P^T: P^T is S^T's layout as it stands; V^T takes byte b of a lane's eight values as output block b,
 //   so one 8-byte piece per token serves all blocks and nothing is transposed through LDS.
-template <int DIM, int NB>
-__global__ void __launch_bounds__(256)
+// One token of 131,072 (32/8 heads of 128): 48 us and 4 for the pieces' joining (5.1 TB/s); 32 sequences of up to 2,270
+// (40/8 heads) 23 us; 298 tokens (16 heads of 64) 6.4 us, the length of the chain.  Codes two or three steps ahead were 3 to 8% slower.
+template <int DIM, int NB, int W>
+__global__ void __launch_bounds__(64 * W)
 kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tokens, int group, float scale,
                     int splits, int row_tiles, uint16_t* __restrict__ y, Partial part) {
   constexpr int DC = DIM / 64;                  // 16-byte pieces of a lane's key
   constexpr int DB = DIM / 16;                  // output blocks; bytes of a lane's value piece
-  __shared__ float red_max[kWaves][16], red_sum[kWaves][16];
-  __shared__ f32x4 red_out[kWaves][DB][64];
+  constexpr int OB = 4 * DB / W;                // outputs of a thread
+  __shared__ float red_max[W][16], red_sum[W][16];
+  __shared__ f32x4 red_out[W][DB][64];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 4, r = lane & 15;
@@ -264,9 +265,9 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
   while (t0 < end) {
 #pragma unroll
     for (int d = 0; d < 2; ++d) {
-      load_codes(codes[d ^ 1], t0 + kStep);
+      load_codes(codes[d ^ 1], t0 + W * kTile);
       step(codes[d], t0);
-      t0 += kStep;
+      t0 += W * kTile;
       if (t0 >= end) break;
       if ((t0 >> page_log) - base >= 64) {      // the next 64 blocks
         base += 64;
@@ -290,7 +291,7 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
     __syncthreads();
     float m = red_max[0][r];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, red_max[w][r]);
+    for (int w = 1; w < W; ++w) m = fmaxf(m, red_max[w][r]);
     const float ref = m == -INFINITY ? 0.0f : m;
     const float by = __builtin_amdgcn_exp2f(top[n] - ref);
 #pragma unroll
@@ -298,28 +299,28 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
     __syncthreads();
     float l = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) l += red_sum[w][r] * __builtin_amdgcn_exp2f(red_max[w][r] - ref);
-    // thread: lane's row r; wave w finishes i = w: dims DB (4 h + w) + 0 .. DB - 1
-    float o[DB];
+    for (int w = 0; w < W; ++w) l += red_sum[w][r] * __builtin_amdgcn_exp2f(red_max[w][r] - ref);
+    // thread: lane's row r; wave w finishes i = w % 4: OB of the dims DB (4 h + i) + 0 .. DB - 1
+    const int ob = OB * (wave / 4);
+    float o[OB];
 #pragma unroll
-    for (int b = 0; b < DB; ++b) {
+    for (int b = 0; b < OB; ++b) {
       o[b] = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) o[b] += red_out[w][b][lane][wave];
+      for (int w = 0; w < W; ++w) o[b] += red_out[w][ob + b][lane][wave % 4];
     }
     const int row = row0 + 16 * n + r;
     if (row >= rows) continue;
-    const int d0 = DB * (4 * h + wave);
+    const int d0 = DB * (4 * h + wave % 4) + ob;
     if (splits == 1) {
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
       uint16_t* dst = y + ((seq * tokens + row / group) * c.heads * group + head * group + row % group) * DIM + d0;
 #pragma unroll
-      for (int b = 0; b < DB; b += 4)
-        *reinterpret_cast<u32x2*>(dst + b) = u32x2{bf16x2_rne(o[b] * inv, o[b + 1] * inv), bf16x2_rne(o[b + 2] * inv, o[b + 3] * inv)};
+      for (int b = 0; b < OB; b += 2) *reinterpret_cast<uint32_t*>(dst + b) = bf16x2_rne(o[b] * inv, o[b + 1] * inv);
     } else {
       const int64_t index = ((seq * c.heads + head) * rows + row) * splits + split;
 #pragma unroll
-      for (int b = 0; b < DB; b += 4) *reinterpret_cast<f32x4*>(part.out + index * DIM + d0 + b) = f32x4{o[b], o[b + 1], o[b + 2], o[b + 3]};
+      for (int b = 0; b < OB; b += 2) *reinterpret_cast<float2*>(part.out + index * DIM + d0 + b) = float2{o[b], o[b + 1]};
       if (h == 0 && wave == 0) {
         part.stat[2 * index] = m;
         part.stat[2 * index + 1] = l;
@@ -381,6 +382,14 @@ kv_combine_kernel(int64_t all, int rows, int heads, int group, int splits, uint1
 // 30,000 of 4 heads 22.7 and 24.7 us; but 500 of 8 heads 12.7 and 9.2 us, 8 x 1,500 of 4 heads 14.8 and 12.4 us; four blocks
 // were never faster than two).
 int blocks_of(int64_t rows, int64_t head_tokens) { return rows > 16 && head_tokens > 256 * 256 ? 2 : 1; }
+// Eight waves on one piece where its workgroups are at most half the CUs: up to 1,536 tokens (1,024 for 128 dims) they are
+// done before four waves on several pieces and the pieces' joining (64 dims: 16 sequences of 1,000, 32/8 heads, 11.4 and 8.8
+// us, 7 x 4 tokens of 1,502 12.0 and 10.9; 128 dims: 1,000 tokens of 32/8 heads 11.7 and 11.5, 1,502 11.8 and 14.4); with more
+// workgroups four waves are better (500 tokens of 500, 8/8 heads: 9.5 against 10.2 us).
+bool eight_waves(int64_t rows, int64_t seq_heads, int64_t length, int dim) {
+  return length > 128 && length <= (dim == 64 ? 1536 : 1024) && blocks_of(rows, seq_heads * length) == 1 &&
+         seq_heads * ((rows + 15) / 16) <= 128;
+}
 // The prompt form, from 65 rows on and where every CU has more than 16 rows against 1,536 tokens that they see (at 128
 // dims): below, its few long workgroups take longer (500 tokens of 8/8 heads 17.7 against 9.4 us here, 40 of 500 of 32/8
 // 14.0 and 9.3, 64 of 2,000 22.3 and 18.4, 1,502 of 2/2 22.4 and 19.4, 636 of 16/2 of 64 18.7 and 10.5; but 20 tokens of
@@ -389,13 +398,13 @@ bool prompt_form(int64_t rows, int64_t tokens, int64_t head_tokens, int64_t leng
   return rows > 64 && (double)rows * (double)head_tokens * seen_of(tokens, length) * dim > 256.0 * 16 * 1536 * 128;
 }
 
-template <int DIM, int NB>
+template <int DIM, int NB, int W>
 hipError_t launch(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs, int64_t tokens, int group, float scale,
                   int64_t splits, uint16_t* y, Partial part, hipStream_t stream) {
   const int64_t rows = tokens * group, tiles = (rows + 16 * NB - 1) / (16 * NB);
   const int64_t blocks = seqs * c.heads * tiles * splits;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((kv_attention_kernel<DIM, NB>), dim3((unsigned)blocks), dim3(256), 0, stream, c, q, ldq, (int)tokens, group,
+  hipLaunchKernelGGL((kv_attention_kernel<DIM, NB, W>), dim3((unsigned)blocks), dim3(64 * W), 0, stream, c, q, ldq, (int)tokens, group,
                      scale, (int)splits, (int)tiles, y, part);
   return hipGetLastError();
 }
@@ -406,8 +415,9 @@ hipError_t launch_all(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t 
   const int64_t rows = tokens * group, all = seqs * c.heads * rows, head_tokens = seqs * c.heads * c.width * c.page;
   hipError_t e;
   if (prompt_form(rows, tokens, head_tokens, c.width * c.page, DIM)) e = launch_prompt<DIM>(c, q, ldq, seqs, tokens, group, scale, prompt_cut(seqs, rows, tokens, c.heads, DIM, c.width * c.page), y, part, stream);
-  else if (blocks_of(rows, head_tokens) == 1) e = launch<DIM, 1>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
-  else e = launch<DIM, 2>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
+  else if (eight_waves(rows, seqs * c.heads, c.width * c.page, DIM)) e = launch<DIM, 1, 8>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
+  else if (blocks_of(rows, head_tokens) == 1) e = launch<DIM, 1, 4>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
+  else e = launch<DIM, 2, 4>(c, q, ldq, seqs, tokens, group, scale, splits, y, part, stream);
   if (e != hipSuccess || splits == 1) return e;
   // a workgroup a row while those fit the GPU's 256 CUs a few times over
   const bool wide = all <= 2048;
@@ -428,7 +438,7 @@ int64_t kv_attention_splits(int64_t seqs, int64_t tokens, int q_heads, int heads
   // one piece alone up to 512 tokens of a full table (a step of 128 takes less than the combination's 3 us) and no piece
   // below 256
   const int64_t tile = 16 * blocks_of(rows, head_tokens), one = seqs * heads * ((rows + tile - 1) / tile);
-  if (most_tokens <= 512) return 1;
+  if (most_tokens <= 512 || eight_waves(rows, seqs * heads, most_tokens, dim)) return 1;
   return std::max<int64_t>(1, std::min<int64_t>((dim == 64 ? 512 : 256) / one, most_tokens / 256));
 }
 
