@@ -314,7 +314,9 @@ w8a8_status w8a8_w4_pack(const uint8_t* codes, const uint16_t* scales, int64_t N
  * one rounding.  x bf16 [M, K], bias bf16 [N] or NULL, y bf16 [M, N].  N % 8 == 0,
  * 0 <= M <= W8A8_W4_MAX_M.  Made for M up to 64; larger M is computed in blocks of
  * 32 or 64 tokens, each of which passes over the weight again.  A token's
- * result does not depend on the others in the call, nor on their number.  The
+ * result does not depend on the others in the call, nor on their number.  x is taken
+ * as finite, with 144 * sum|x| over a group inside fp32 (the sums run over codes with
+ * an offset that is taken out again); a token that is not spoils its own row only.  The
  * workspace holds fp32 partial sums where K is long and N small, so that K is cut;
  * w8a8_w4_workspace_bytes is 0, and workspace may be NULL, where it is not. */
 #define W8A8_W4_MAX_M (1 << 20)

@@ -271,6 +271,22 @@ def test_query_sizes(lib, by):
     run(lib, [50, 300], 1, 4, 2, 64, 32, seed=1, q_by=2 * by, scale=0.125 / by)
 
 
+@pytest.mark.parametrize("tokens,wide", ((1, False), (6, False), (6, True), (70, False), (70, True)))
+def test_a_query_that_is_not_finite_spoils_its_own_row_only(lib, tokens, wide):
+    lens, dim, page = [300, 100], 64, 32
+    table, pages = tables(lens, page, 2, 1)
+    if wide:
+        table = long_table(table, 2, 4 * tokens, 2, page)
+    cache = filled(lib, pages, 2, page, dim, 2)
+    q = rows_of(2, tokens, 8, dim, 3, by=2.0).clone()
+    clean = q.clone()
+    q[1, tokens // 2, 5, 7] = float("nan")
+    y = attend(lib, q, cache, table, lens)
+    assert torch.isnan(y[1, tokens // 2, 5].float()).all()
+    y[1, tokens // 2, 5] = attend(lib, clean, cache, table, lens)[1, tokens // 2, 5]
+    check(y, clean, cache, table, lens, dim ** -0.5, "beside a NaN")
+
+
 def test_zero_queries_average_the_values(lib):
     run(lib, [100, 3], 2, 4, 2, 64, 16, seed=1, q_by=0.0)
 

@@ -166,6 +166,17 @@ def test_quantized_weight_end_to_end(lib):
     assert float((y - ref).norm()) <= 1.5 * float(step) / 12 ** 0.5 * K ** 0.5 * (M * N) ** 0.5
 
 
+@pytest.mark.parametrize("M,N,K", ((3, 264, 640), (16, 4096, 384), (40, 1000, 1152), (256, 5120, 640)))
+def test_a_token_that_is_not_finite_spoils_its_own_row_only(lib, M, N, K):
+    y, (x, cp, sp, b) = run(lib, M, N, K, 64, True, 31)
+    for bad in (float("nan"), float("inf")):
+        z = x.clone()
+        z[M // 2, K // 3] = bad
+        out = lib.w8a8_w4_linear(z.cuda(), cp, sp, N, 64, b.cuda())
+        others = torch.arange(M, device="cuda") != M // 2
+        assert torch.equal(out[others], y[others]) and not torch.isfinite(out[M // 2].float()).any()
+
+
 def test_offsets_past_2_31_bytes(lib):
     """A packed weight of 2.2 GB: the rows on both sides of the 2^31-byte mark and the last ones."""
     K, N, group = 131072, 33600, 128
