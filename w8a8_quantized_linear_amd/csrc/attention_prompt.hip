@@ -106,13 +106,13 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
   auto token_of = [&](int i) { return (SHARED ? 8 * (stage & 1) : (64 / KL) * i) + k_row; };
   const int v_lane = (4 * v_half) * DIM + 4 * v_quad;
   int ids[KP];                                  // pages of the runs of the tile to be loaded next
-  u32x4 raw_k[KP], raw_v[2];                    // codes to be converted next
-  float run_k[KP], run_v;
+  u32x4 raw_k[2][KP], raw_v[2][2];              // codes of the next two tiles
+  float run_k[2][KP], run_v[2];
   auto load_ids = [&](int t0) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < KP; ++i) ids[i] = table[min((t0 + 16 * run_of(i)) >> page_log, (int)c.width - 1)];
   };
-  auto load_codes = [&](int t0) __attribute__((always_inline)) {
+  auto load_codes = [&](int d, int t0) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < KP; ++i) {
       const int t = t0 + 16 * run_of(i), named = __builtin_amdgcn_readfirstlane(ids[i]);
@@ -120,20 +120,20 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
       const int64_t id = real ? named : 0;
       const int64_t base = id * page_bytes + head_base + (int64_t)(t & (c.page - 1)) * DIM;
       if (keys) {
-        raw_k[i] = *reinterpret_cast<const u32x4*>(c.k_codes + base + token_of(i) * DIM + 16 * k_piece);
-        run_k[i] = real ? c.k_scale[id * c.heads + head] : 0.0f;
+        raw_k[d][i] = *reinterpret_cast<const u32x4*>(c.k_codes + base + token_of(i) * DIM + 16 * k_piece);
+        run_k[d][i] = real ? c.k_scale[id * c.heads + head] : 0.0f;
       }
       if (values && i == 0) {
         if (v_half < 2) {
           const int8_t* from = c.v_codes + base + v_lane;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) raw_v[j / 4][j % 4] = *reinterpret_cast<const uint32_t*>(from + (j % 4 + 8 * (j / 4)) * DIM);
+          for (int j = 0; j < 8; ++j) raw_v[d][j / 4][j % 4] = *reinterpret_cast<const uint32_t*>(from + (j % 4 + 8 * (j / 4)) * DIM);
         }
-        run_v = real ? c.v_scale[id * c.heads + head] : -1.0f;
+        run_v[d] = real ? c.v_scale[id * c.heads + head] : -1.0f;
       }
     }
   };
-  auto store = [&](int buf) __attribute__((always_inline)) {
+  auto store = [&](int n) __attribute__((always_inline)) {
     if (keys) {
 #pragma unroll
       for (int i = 0; i < KP; ++i) {
@@ -142,32 +142,32 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
         uint32_t two[2];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          f16_word(raw_k[i][j], two);
+          f16_word(raw_k[n][i][j], two);
           if (j < 2) lo[2 * j] = two[0], lo[2 * j + 1] = two[1];
           else hi[2 * j - 4] = two[0], hi[2 * j - 3] = two[1];
         }
-        k_lds[buf][t * KCH + (ch ^ (t & (KCH - 1)))] = lo;
-        k_lds[buf][t * KCH + ((ch + 1) ^ (t & (KCH - 1)))] = hi;
-        if (t % 16 == 0 && k_piece == 0) runs[buf][t / 16].k = run_k[i];
+        k_lds[n][t * KCH + (ch ^ (t & (KCH - 1)))] = lo;
+        k_lds[n][t * KCH + ((ch + 1) ^ (t & (KCH - 1)))] = hi;
+        if (t % 16 == 0 && k_piece == 0) runs[n][t / 16].k = run_k[n][i];
       }
     }
     if (values) {
       const int ch = 2 * stage + v_half;
-      const bool zeros = !(run_v >= 0x1p-90f);  // kLeastLog
+      const bool zeros = !(run_v[n] >= 0x1p-90f);  // kLeastLog
       if (v_half < 2) {
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           u32x4 a;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) a[j] = f16_bytes(raw_v[j / 2][2 * (j % 2) + 1], raw_v[j / 2][2 * (j % 2)], b);
+          for (int j = 0; j < 4; ++j) a[j] = f16_bytes(raw_v[n][j / 2][2 * (j % 2) + 1], raw_v[n][j / 2][2 * (j % 2)], b);
           const int d = 4 * v_quad + b;
-          v_lds[buf][d * (kTile / 8) + (ch ^ ((d ^ (d >> 2)) & 7))] = zeros ? u32x4{0, 0, 0, 0} : a;
+          v_lds[n][d * (kTile / 8) + (ch ^ ((d ^ (d >> 2)) & 7))] = zeros ? u32x4{0, 0, 0, 0} : a;
         }
       }
       if (lane == 0) {
-        runs[buf][stage].v_log = zeros ? kLeastLog : __log2f(run_v);
-        runs[buf][stage].v_inv = zeros ? 0x1p90f : 1.0f / run_v;
-        runs[buf][stage].real = run_v != -1.0f;
+        runs[n][stage].v_log = zeros ? kLeastLog : __log2f(run_v[n]);
+        runs[n][stage].v_inv = zeros ? 0x1p90f : 1.0f / run_v[n];
+        runs[n][stage].real = run_v[n] != -1.0f;
       }
     }
   };
@@ -179,109 +179,111 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
     for (int i = 0; i < 16; ++i) out[b][i] = 0.0f;
   float top = -INFINITY, sum = 0.0f;
 
-  // Of 8 waves the keys' convert the next tile before they multiply, the values' after it (their codes are loaded
-  // an iteration later), so that the two waves of a SIMD are out of step: one's products run under the other's softmax
-  // and conversions (four prompts of 1,502 tokens: 149 us, in step 160 us).
+  // Codes are loaded two tiles ahead (one ahead: 3% more for four prompts of 1,502 tokens, 5% for 400 tokens of 633).  Of 8
+  // waves the keys' convert the next tile before they multiply, the values' after it, so that the two waves of a SIMD are
+  // out of step: one's products run under the other's softmax and conversions (149 us, in step 160 us).
   const bool ahead = WAVES == 8 && keys;
   if (begin < end) {
     load_ids(begin);
-    load_codes(begin);
+    load_codes(0, begin);
     load_ids(begin + kTile);
+    load_codes(1, begin + kTile);               // (past the end: rows of a page that exists, not seen)
+    load_ids(begin + 2 * kTile);
     store(0);
-    if (ahead) {
-      load_codes(begin + kTile);                // (past the end: rows of a page that exists, not seen)
-      load_ids(begin + 2 * kTile);
-    }
     __syncthreads();
   }
-  for (int t0 = begin, buf = 0; t0 < end; t0 += kTile, buf ^= 1) {
-    const bool more = t0 + kTile < end;
-    if (more) {
-      if (ahead) store(buf ^ 1);
-      const int next = ahead ? t0 + 2 * kTile : t0 + kTile;
-      load_codes(next);
-      load_ids(next + kTile);
-    }
-    if (t0 < wave_end) {
-      f32x16 s[2];
+  for (int t0 = begin; t0 < end;) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+    for (int buf = 0; buf < 2; ++buf) {
+      if (buf && t0 >= end) break;
+      const bool more = t0 + kTile < end;
+      if (more) {
+        if (ahead) store(buf ^ 1);
+        load_codes(buf, t0 + 2 * kTile);
+        load_ids(t0 + 3 * kTile);
+      }
+      if (t0 < wave_end) {
+        f32x16 s[2];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
+          for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int t = 32 * b + r;
-          const u32x4 a = k_lds[buf][t * KCH + ((2 * k + h) ^ (t & (KCH - 1)))];
-          s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, qf[k]), s[b], 0, 0, 0);
+        for (int k = 0; k < KS; ++k) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const int t = 32 * b + r;
+            const u32x4 a = k_lds[buf][t * KCH + ((2 * k + h) ^ (t & (KCH - 1)))];
+            s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, qf[k]), s[b], 0, 0, 0);
+          }
         }
-      }
-      Run run[kSubs];
-      float factor[kSubs];
-      int real = 1;
-#pragma unroll
-      for (int u = 0; u < kSubs; ++u) {
-        run[u] = runs[buf][u];
-        factor[u] = run[u].k * qs;
-        real &= __builtin_amdgcn_readfirstlane(run[u].real);
-      }
-      if (t0 + kTile > all_seen || !real) {             // some row does not see some token
+        Run run[kSubs];
+        float factor[kSubs];
+        int real = 1;
 #pragma unroll
         for (int u = 0; u < kSubs; ++u) {
+          run[u] = runs[buf][u];
+          factor[u] = run[u].k * qs;
+          real &= __builtin_amdgcn_readfirstlane(run[u].real);
+        }
+        if (t0 + kTile > all_seen || !real) {             // some row does not see some token
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int key = t0 + 16 * u + 8 * (i / 4) + 4 * h + i % 4;
-            const bool seen = key < end && key <= last_key && run[u].real;
-            s[u / 2][8 * (u % 2) + i] = seen ? s[u / 2][8 * (u % 2) + i] * factor[u] : -INFINITY;
+          for (int u = 0; u < kSubs; ++u) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int key = t0 + 16 * u + 8 * (i / 4) + 4 * h + i % 4;
+              const bool seen = key < end && key <= last_key && run[u].real;
+              s[u / 2][8 * (u % 2) + i] = seen ? s[u / 2][8 * (u % 2) + i] * factor[u] : -INFINITY;
+            }
+            factor[u] = 1.0f;
           }
-          factor[u] = 1.0f;
         }
-      }
-      float m = -INFINITY;
+        float m = -INFINITY;
 #pragma unroll
-      for (int u = 0; u < kSubs; ++u) {
-        float mu = s[u / 2][8 * (u % 2)];
+        for (int u = 0; u < kSubs; ++u) {
+          float mu = s[u / 2][8 * (u % 2)];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) mu = fmaxf(mu, s[u / 2][8 * (u % 2) + i]);
-        m = fmaxf(m, __builtin_fmaf(mu, factor[u], run[u].v_log));
-      }
-      if (__any(m > top + kLazy)) {
-        const float next = fmaxf(max_halves(m), top), ref = next == -INFINITY ? 0.0f : next;
-        const float scaled = __builtin_amdgcn_exp2f(top - ref);
-        sum *= scaled;
-#pragma unroll
-        for (int b = 0; b < DB; ++b)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) out[b][i] *= scaled;
-        top = next;
-      }
-      const float ref = top == -INFINITY ? 0.0f : top, rest = kProbExp - ref;
-      u32x4 p[kSubs];
-#pragma unroll
-      for (int u = 0; u < kSubs; ++u) {
-        const float off = run[u].v_log + rest;
-        float add = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u / 2][8 * (u % 2) + i], factor[u], off));
-          const float b = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u / 2][8 * (u % 2) + i + 1], factor[u], off));
-          add += a + b;
-          p[u][i / 2] = f16_pair(a, b);
+          for (int i = 1; i < 8; ++i) mu = fmaxf(mu, s[u / 2][8 * (u % 2) + i]);
+          m = fmaxf(m, __builtin_fmaf(mu, factor[u], run[u].v_log));
         }
-        sum = __builtin_fmaf(add, run[u].v_inv, sum);
-      }
+        if (__any(m > top + kLazy)) {
+          const float next = fmaxf(max_halves(m), top), ref = next == -INFINITY ? 0.0f : next;
+          const float scaled = __builtin_amdgcn_exp2f(top - ref);
+          sum *= scaled;
 #pragma unroll
-      for (int u = 0; u < kSubs; ++u)
+          for (int b = 0; b < DB; ++b)
 #pragma unroll
-        for (int b = 0; b < DB; ++b) {
-          const int d = 32 * b + r;
-          const u32x4 a = v_lds[buf][d * (kTile / 8) + ((2 * u + h) ^ ((d ^ (d >> 2)) & 7))];
-          out[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, p[u]), out[b], 0, 0, 0);
+            for (int i = 0; i < 16; ++i) out[b][i] *= scaled;
+          top = next;
         }
+        const float ref = top == -INFINITY ? 0.0f : top, rest = kProbExp - ref;
+        u32x4 p[kSubs];
+#pragma unroll
+        for (int u = 0; u < kSubs; ++u) {
+          const float off = run[u].v_log + rest;
+          float add = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u / 2][8 * (u % 2) + i], factor[u], off));
+            const float b = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u / 2][8 * (u % 2) + i + 1], factor[u], off));
+            add += a + b;
+            p[u][i / 2] = f16_pair(a, b);
+          }
+          sum = __builtin_fmaf(add, run[u].v_inv, sum);
+        }
+#pragma unroll
+        for (int u = 0; u < kSubs; ++u)
+#pragma unroll
+          for (int b = 0; b < DB; ++b) {
+            const int d = 32 * b + r;
+            const u32x4 a = v_lds[buf][d * (kTile / 8) + ((2 * u + h) ^ ((d ^ (d >> 2)) & 7))];
+            out[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, p[u]), out[b], 0, 0, 0);
+          }
+      }
+      if (more && !ahead) store(buf ^ 1);
+      __syncthreads();
+      t0 += kTile;
     }
-    if (more && !ahead) store(buf ^ 1);
-    __syncthreads();
   }
 
   // ---- outputs: register i of block b is dim 32 b + 8 (i / 4) + 4 h + i % 4 ----
