@@ -133,7 +133,8 @@ __device__ __forceinline__ void store_outputs(f32x4 v, int64_t m, int64_t n, int
 // a wave has the next block's loads in flight while it multiplies.  x and the scales pass through an LDS area
 // of the wave's own: loaded straight into operands, a block of x takes 4 instructions that touch 16 rows
 // each (and with groups of 32 the scales 4 more per row block), which held 5 tokens of 17,408 x 5,120 to 27 us; as
-// XI instructions of 4 whole row pieces and one for the scales they take 15.6 us.
+// XI instructions of 4 whole row pieces and one for the scales they take 14.8 us.  1 token of
+// 5,120 x 34,816 takes 18.6 us (4.9 TB/s), 16 take 22.0 us.
 template <int XI, int RB, int GPB>
 __global__ void __launch_bounds__(64 * kSegs)
 w4_few_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, const uint16_t* __restrict__ s,
