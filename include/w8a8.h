@@ -355,7 +355,8 @@ w8a8_status w8a8_w4_linear(const uint16_t* x, const uint8_t* codes_packed, const
  * round-half-even(code * (old / new scale)), new ones round-half-even(x / scale).
  * A scale of a page that holds nothing from before is not read: a cache needs no
  * initialisation.  Values are taken as finite: a NaN or an infinity spoils the
- * codes of its page and head (of no other).
+ * codes of its page and head (of no other; attention of queries that see none of
+ * that page is as without it).
  * Filling a page in one call rounds each value once; token by token, a page's
  * earlier codes are rounded again whenever a larger value arrives (each time by
  * at most half a step of the new scale). */

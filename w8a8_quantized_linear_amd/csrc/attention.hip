@@ -184,10 +184,11 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
     u32x4 p[NB];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-      float factor[2], m = -INFINITY;
+      float factor[2], vlog[2], m = -INFINITY;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         factor[u] = rk[u] * qs[n];
+        vlog[u] = rlog[u];
         if (!whole) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -196,8 +197,10 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
             s[n][u][i] = seen ? s[n][u][i] * factor[u] : -INFINITY;
           }
           factor[u] = 1.0f;
+          // (a row that sees none of the run: its values' scale, which may be infinite, must not count)
+          if (t0 + 16 * u > last_key[n]) vlog[u] = kLeastLog;
         }
-        m = fmaxf(m, __builtin_fmaf(fmaxf(fmaxf(s[n][u][0], s[n][u][1]), fmaxf(s[n][u][2], s[n][u][3])), factor[u], rlog[u]));
+        m = fmaxf(m, __builtin_fmaf(fmaxf(fmaxf(s[n][u][0], s[n][u][1]), fmaxf(s[n][u][2], s[n][u][3])), factor[u], vlog[u]));
       }
       if (__any(m > top[n] + kLazy)) {
         const float next = fmaxf(max_quarters(m), top[n]), ref = next == -INFINITY ? 0.0f : next;
@@ -211,7 +214,7 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const bool some = rv[u] > 0.0f;         // (zeros: codes of zero, whatever they are)
-        const float off = rlog[u] + (kProbExp - ref);
+        const float off = vlog[u] + (kProbExp - ref);
         float add = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {

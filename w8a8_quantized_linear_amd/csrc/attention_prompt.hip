@@ -236,6 +236,8 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
               s[u / 2][8 * (u % 2) + i] = seen ? s[u / 2][8 * (u % 2) + i] * factor[u] : -INFINITY;
             }
             factor[u] = 1.0f;
+            // (a row that sees none of the run: its values' scale, which may be infinite, must not count)
+            if (t0 + 16 * u > last_key) run[u].v_log = kLeastLog;
           }
         }
         float m = -INFINITY;
