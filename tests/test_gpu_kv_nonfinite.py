@@ -1,11 +1,12 @@
-"""Attention beside pages whose scales are not finite: against 64 bits, with the tolerance of test_gpu_kv_attention.py."""
+"""Attention beside pages whose scales are not finite, and softmax scales of every sign: against 64 bits, with the
+tolerance of test_gpu_kv_attention.py."""
 import numpy as np
 import pytest
 import torch
 
 import plain_decode as P
 from parity import say
-from test_gpu_kv_attention import attend, host, long_table
+from test_gpu_kv_attention import attend, check, host, long_table
 from test_gpu_kv_cache import filled, rows_of, tables
 
 pytestmark = pytest.mark.gpu
@@ -66,3 +67,43 @@ def test_an_infinite_value_appended_last(lib):
     assert torch.isinf(cache.v_scale[table[0, 4].long()]).all()
     y = attend(lib, q, cache, table, lens)
     assert torch.isfinite(y[:, :-1].float()).all()
+
+
+# one row, rows in one and two blocks, and the prompt form
+FORMS = ((1, False), (6, False), (12, True), (70, True))
+
+
+@pytest.mark.parametrize("scale", (0.0, -0.125, -2.0))
+@pytest.mark.parametrize("tokens,wide", FORMS)
+def test_softmax_scales_that_are_not_positive(lib, tokens, wide, scale):
+    """0 averages what a query sees; a negative scale is the positive one with the queries' signs turned, bit for bit.
+    (Against 64 bits while the scores stay small: with -2, probabilities below f16's range are all that some elements
+    have, which the tolerance has no term for.)"""
+    lens, dim, page = [300, 100], 64, 32
+    table, pages = tables(lens, page, 2, 1)
+    if wide:
+        table = long_table(table, 2, 4 * tokens, 2, page)
+    cache = filled(lib, pages, 2, page, dim, 2)
+    q = rows_of(2, tokens, 8, dim, 3, by=2.0)
+    y = attend(lib, q, cache, table, lens, scale)
+    assert torch.equal(y, attend(lib, -q, cache, table, lens, -scale))
+    if scale > -1:
+        check(y, q, cache, table, lens, scale, f"scale {scale}")
+
+
+@pytest.mark.parametrize("bad", (float("inf"), -float("inf")))
+@pytest.mark.parametrize("tokens,wide", FORMS)
+def test_an_infinite_query_spoils_its_own_row_only(lib, tokens, wide, bad):
+    """(Its scores are infinities of both signs or NaN, so its own outputs are NaN.)"""
+    lens, dim, page = [300, 100], 64, 32
+    table, pages = tables(lens, page, 2, 1)
+    if wide:
+        table = long_table(table, 2, 4 * tokens, 2, page)
+    cache = filled(lib, pages, 2, page, dim, 2)
+    q = rows_of(2, tokens, 8, dim, 3, by=2.0).clone()
+    clean = q.clone()
+    q[1, tokens // 2, 5, 7] = bad
+    y = attend(lib, q, cache, table, lens)
+    assert torch.isnan(y[1, tokens // 2, 5].float()).all()
+    y[1, tokens // 2, 5] = attend(lib, clean, cache, table, lens)[1, tokens // 2, 5]
+    check(y, clean, cache, table, lens, dim ** -0.5, "beside an infinity")
