@@ -312,7 +312,7 @@ w8a8_status w8a8_w4_pack(const uint8_t* codes, const uint16_t* scales, int64_t N
 
 /* y[m][n] = bf16( sum over groups of scale * sum(x * code) + bias[n] ), fp32 sums,
  * one rounding.  x bf16 [M, K], bias bf16 [N] or NULL, y bf16 [M, N].  N % 8 == 0,
- * 0 <= M <= W8A8_W4_MAX_M.  Made for M up to 64; larger M is computed in blocks of
+ * N <= W8A8_W4_MAX_N, 0 <= M <= W8A8_W4_MAX_M, M * N <= 2^40.  Made for M up to 64; larger M is computed in blocks of
  * 32 or 64 tokens, each of which passes over the weight again.  A token's
  * result does not depend on the others in the call, nor on their number.  x is taken
  * as finite, with 144 * sum|x| over a group inside fp32 (the sums run over codes with
@@ -320,6 +320,7 @@ w8a8_status w8a8_w4_pack(const uint8_t* codes, const uint16_t* scales, int64_t N
  * workspace holds fp32 partial sums where K is long and N small, so that K is cut;
  * w8a8_w4_workspace_bytes is 0, and workspace may be NULL, where it is not. */
 #define W8A8_W4_MAX_M (1 << 20)
+#define W8A8_W4_MAX_N ((1 << 28) - 32)
 size_t w8a8_w4_workspace_bytes(int64_t M, int64_t N, int64_t K);
 w8a8_status w8a8_w4_linear(const uint16_t* x, const uint8_t* codes_packed, const uint16_t* scales_packed,
                            const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K, int group,
@@ -357,6 +358,7 @@ w8a8_status w8a8_w4_linear(const uint16_t* x, const uint8_t* codes_packed, const
  * initialisation.  Values are taken as finite: a NaN or an infinity spoils the
  * codes of its page and head (of no other; attention of queries that see none of
  * that page is as without it).
+ * (tokens / page + 2) * heads < 2^23, and that times seqs < 2^30.
  * Filling a page in one call rounds each value once; token by token, a page's
  * earlier codes are rounded again whenever a larger value arrives (each time by
  * at most half a step of the new scale). */
@@ -366,7 +368,7 @@ w8a8_status w8a8_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, in
                            int64_t dim, int64_t page, hipStream_t stream);
 
 /* The sequences as bf16: k, v [seqs, length, heads, dim] = bf16(code * scale), zeros
- * from a sequence's length on. */
+ * from a sequence's length on.  length * dim <= 2^35 - 2048, seqs * length * heads * dim < 2^42. */
 w8a8_status w8a8_kv_read(const int8_t* k_codes, const float* k_scale, const int8_t* v_codes, const float* v_scale,
                          int64_t pages, const int32_t* table, int64_t width, const int32_t* lens, int64_t seqs,
                          int64_t length, int64_t heads, int64_t dim, int64_t page, uint16_t* k, uint16_t* v,

@@ -405,11 +405,13 @@ template <int DIM, int NB, int W>
 hipError_t launch(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs, int64_t tokens, int group, float scale,
                   int64_t splits, uint16_t* y, Partial part, hipStream_t stream) {
   const int64_t rows = tokens * group, tiles = (rows + 16 * NB - 1) / (16 * NB);
-  const int64_t blocks = seqs * c.heads * tiles * splits;
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((kv_attention_kernel<DIM, NB, W>), dim3((unsigned)blocks), dim3(64 * W), 0, stream, c, q, ldq, (int)tokens, group,
-                     scale, (int)splits, (int)tiles, y, part);
-  return hipGetLastError();
+  const int64_t blocks = c.heads * tiles * splits;              // of a sequence
+  return in_launches(seqs, blocks, 64 * W, [&](int64_t b, int64_t n) {
+    hipLaunchKernelGGL((kv_attention_kernel<DIM, NB, W>), dim3((unsigned)(n * blocks)), dim3(64 * W), 0, stream, c.from(b),
+                       q + b * tokens * ldq, ldq, (int)tokens, group, scale, (int)splits, (int)tiles, y + b * c.heads * rows * DIM,
+                       part.from(b * c.heads * rows * splits, DIM));
+    return hipGetLastError();
+  });
 }
 
 template <int DIM>

@@ -79,6 +79,7 @@ __device__ __forceinline__ float sum_quarters(float v) {
 struct Partial {
   float* out;
   float* stat;
+  Partial from(int64_t index, int dim) const { return out ? Partial{out + index * dim, stat + 2 * index} : *this; }
 };
 
 // The part of `length` tokens that the last `tokens` of them see on average.

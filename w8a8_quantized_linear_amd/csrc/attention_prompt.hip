@@ -347,12 +347,15 @@ template <int DIM>
 hipError_t launch_prompt(const KvCache& c, const uint16_t* q, int64_t ldq, int64_t seqs, int64_t tokens, int group,
                          float scale, PromptCut cut, uint16_t* y, Partial part, hipStream_t stream) {
   const int rows = cut.rows;
-  const int64_t tiles = (tokens * group + rows - 1) / rows, total = seqs * c.heads * tiles * cut.splits;
-  if (total > 0x7fffffff) return hipErrorInvalidValue;
+  const int64_t tiles = (tokens * group + rows - 1) / rows, blocks = c.heads * tiles * cut.splits;      // of a sequence
+  const int64_t row = (int64_t)c.heads * tokens * group;                                                // rows of y
   const auto kernel = rows == 256 ? kv_prompt_kernel<DIM, 8> : kv_prompt_kernel<DIM, 4>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)total), dim3(2 * rows), 0, stream, c, q, ldq, (int)tokens, group, scale, (int)cut.splits,
-                     (int)tiles, (int)total, y, part);
-  return hipGetLastError();
+  return in_launches(seqs, blocks, 2 * rows, [&](int64_t b, int64_t n) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(n * blocks)), dim3(2 * rows), 0, stream, c.from(b), q + b * tokens * ldq, ldq, (int)tokens,
+                       group, scale, (int)cut.splits, (int)tiles, (int)(n * blocks), y + b * row * DIM,
+                       part.from(b * row * cut.splits, DIM));
+    return hipGetLastError();
+  });
 }
 
 template hipError_t launch_prompt<64>(const KvCache&, const uint16_t*, int64_t, int64_t, int64_t, int, float, PromptCut,

@@ -6,6 +6,23 @@
 
 namespace w8a8 {
 
+// Workgroups of one launch: a grid has fewer than 2^32 work items along x, and a launch past that reports
+// success and runs the remainder only.  What does not fit goes out in several launches.
+constexpr int64_t most_blocks(int threads) { return 0xffffffffLL / threads; }
+
+// launch(first, count) over `all` parts of `blocks` workgroups each, as many parts at a time as fit; an error if one
+// alone does not.
+template <typename F>
+hipError_t in_launches(int64_t all, int64_t blocks, int threads, F launch) {
+  const int64_t most = most_blocks(threads) / blocks;
+  if (most < 1) return hipErrorInvalidValue;
+  for (int64_t first = 0; first < all; first += most) {
+    const hipError_t e = launch(first, all - first < most ? all - first : most);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 // 4-bit weights (w4.hip).  Row-major codes [N, K / 2] and bf16 scales [N, K / group];
 // packed: blocks of 16 rows x 128 columns (layout in w8a8.h), rows rounded up to 16.
 hipError_t launch_w4_quantize(const uint16_t* w, int64_t N, int64_t K, int group, uint8_t* codes,
@@ -28,6 +45,12 @@ struct KvCache {
   const int32_t* lens;    // [seqs] tokens held, the newest call's included
   int64_t pages, width;
   int heads, dim, page;
+  KvCache from(int64_t seq) const {   // the sequences from `seq` on
+    KvCache c = *this;
+    c.table += seq * width;
+    c.lens += seq;
+    return c;
+  }
 };
 
 // New rows k, v (kv_cache.hip): token t of sequence b at k + (b * tokens + t) * ldk.

@@ -81,7 +81,8 @@ w8a8_status w8a8_w4_linear(const uint16_t* x, const uint8_t* codes_packed, const
                            void* workspace, size_t workspace_bytes, hipStream_t stream) {
   w8a8_status st = check_w4_shape(N, K, group);
   if (st != W8A8_OK) return st;
-  if (M < 0 || M > W8A8_W4_MAX_M || N < 1 || N % 8 != 0) return W8A8_ERR_BAD_SHAPE;
+  if (M < 0 || M > W8A8_W4_MAX_M || N < 1 || N % 8 != 0 || N > W8A8_W4_MAX_N) return W8A8_ERR_BAD_SHAPE;
+  if (M > ((int64_t)1 << 40) / N) return W8A8_ERR_BAD_SHAPE;
   if (M == 0) return W8A8_OK;
   const size_t need = w8a8_w4_workspace_bytes(M, N, K);
   if (workspace_bytes < need) return W8A8_ERR_BAD_ARGUMENT;
@@ -101,7 +102,8 @@ w8a8_status w8a8_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, in
   if (st != W8A8_OK) return st;
   if (tokens < 0 || tokens > W8A8_KV_MAX_TOKENS) return W8A8_ERR_BAD_SHAPE;
   if (!ld_ok(ldk, heads * dim) || !ld_ok(ldv, heads * dim)) return W8A8_ERR_BAD_SHAPE;
-  if (seqs * ((tokens + page - 2) / page + 1) * heads * 2 > 0x7fffffff) return W8A8_ERR_BAD_SHAPE;
+  const int64_t blocks = ((tokens + page - 2) / page + 1) * heads * 2;       // workgroups of a sequence
+  if (seqs * blocks > 0x7fffffff || blocks > w8a8::most_blocks(256)) return W8A8_ERR_BAD_SHAPE;
   if (seqs == 0 || tokens == 0) return W8A8_OK;
   if (!k || !v || !k_codes || !k_scale || !v_codes || !v_scale || !table || !lens) return W8A8_ERR_NULL_POINTER;
   if (!aligned16(k) || !aligned16(v) || !aligned16(k_codes) || !aligned16(k_scale) || !aligned16(v_codes) ||
@@ -120,6 +122,7 @@ w8a8_status w8a8_kv_read(const int8_t* k_codes, const float* k_scale, const int8
   if (st != W8A8_OK) return st;
   if (length < 0 || length > W8A8_KV_MAX_LENGTH) return W8A8_ERR_BAD_SHAPE;
   if (seqs > 0 && length > (((int64_t)0x7fffffff << 8) / (heads * (dim / 8))) / seqs) return W8A8_ERR_BAD_SHAPE;
+  if (length > 2048 / dim * w8a8::most_blocks(256)) return W8A8_ERR_BAD_SHAPE;
   if (seqs == 0 || length == 0) return W8A8_OK;
   if (!k || !v || !k_codes || !k_scale || !v_codes || !v_scale || !table || !lens) return W8A8_ERR_NULL_POINTER;
   if (!aligned16(k) || !aligned16(v) || !aligned16(k_codes) || !aligned16(k_scale) || !aligned16(v_codes) ||

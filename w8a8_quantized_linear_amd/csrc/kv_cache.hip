@@ -161,25 +161,26 @@ kv_read_kernel(KvCache c, int64_t length, int chunks, uint16_t* __restrict__ k, 
 
 hipError_t launch_kv_append(const KvCache& c, const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
                             int64_t seqs, int64_t tokens, hipStream_t stream) {
-  const int64_t touched = (tokens + c.page - 2) / c.page + 1;
-  const int64_t blocks = seqs * touched * c.heads * 2;
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  if (c.dim == 64)
-    hipLaunchKernelGGL((kv_append_kernel<64>), dim3((unsigned)blocks), dim3(256), 0, stream, c, k, ldk, v, ldv, tokens, (unsigned)touched);
-  else
-    hipLaunchKernelGGL((kv_append_kernel<128>), dim3((unsigned)blocks), dim3(256), 0, stream, c, k, ldk, v, ldv, tokens, (unsigned)touched);
-  return hipGetLastError();
+  const int64_t touched = (tokens + c.page - 2) / c.page + 1, blocks = touched * c.heads * 2;     // of a sequence
+  const auto kernel = c.dim == 64 ? kv_append_kernel<64> : kv_append_kernel<128>;
+  return in_launches(seqs, blocks, 256, [&](int64_t b, int64_t n) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(n * blocks)), dim3(256), 0, stream, c.from(b), k + b * tokens * ldk, ldk,
+                       v + b * tokens * ldv, ldv, tokens, (unsigned)touched);
+    return hipGetLastError();
+  });
 }
 
 hipError_t launch_kv_read(const KvCache& c, int64_t seqs, int64_t length, uint16_t* k, uint16_t* v,
                           hipStream_t stream) {
   const int tokens = 2048 / c.dim;              // of a workgroup
-  const int64_t chunks = (length + tokens - 1) / tokens;
-  if (chunks * seqs > 0x7fffffff) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)(chunks * seqs), (unsigned)((c.heads + kReadHeads - 1) / kReadHeads));
+  const int64_t chunks = (length + tokens - 1) / tokens, row = length * c.heads * c.dim;
+  const unsigned head_groups = (unsigned)((c.heads + kReadHeads - 1) / kReadHeads);
   const auto kernel = c.dim == 64 ? kv_read_kernel<64> : kv_read_kernel<128>;
-  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, c, length, (int)chunks, k, v);
-  return hipGetLastError();
+  return in_launches(seqs, chunks, 256, [&](int64_t b, int64_t n) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(n * chunks), head_groups), dim3(256), 0, stream, c.from(b), length, (int)chunks,
+                       k + b * row, v + b * row);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace w8a8

@@ -623,24 +623,31 @@ hipError_t launch_many(const Linear& a, int waves) {
 
 hipError_t launch_w4_quantize(const uint16_t* w, int64_t N, int64_t K, int group, uint8_t* codes,
                               uint16_t* scales, hipStream_t stream) {
-  const int64_t chunks = N * K / 8, blocks = (chunks + 255) / 256;
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(w4_quantize_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, w, chunks, group / 8,
-                     reinterpret_cast<uint32_t*>(codes), scales);
-  return hipGetLastError();
+  constexpr int kPart = 2048;        // rows
+  const int64_t parts = (N + kPart - 1) / kPart, each = kPart * (K / 8) / 256;     // (K % 128 == 0: whole workgroups)
+  return in_launches(parts, each, 256, [&](int64_t p, int64_t n) {
+    const int64_t row = p * kPart, chunks = std::min(n * kPart, N - row) * K / 8;
+    hipLaunchKernelGGL(w4_quantize_kernel, dim3((unsigned)((chunks + 255) / 256)), dim3(256), 0, stream, w + row * K, chunks, group / 8,
+                       reinterpret_cast<uint32_t*>(codes + row * (K / 2)), scales + row * (K / group));
+    return hipGetLastError();
+  });
 }
 
 hipError_t launch_w4_pack(const uint8_t* codes, const uint16_t* scales, int64_t N, int64_t K, int group,
                           uint8_t* codes_packed, uint16_t* scales_packed, hipStream_t stream) {
-  const int64_t rows = (N + kRows - 1) / kRows * kRows, words = rows * K / 8, total = rows * (K / group);
-  if ((words + 255) / 256 > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(w4_pack_codes_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, stream,
-                     reinterpret_cast<const uint32_t*>(codes), N, K, words, reinterpret_cast<uint32_t*>(codes_packed));
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(w4_pack_scales_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, stream, scales, N,
-                     K / group, total, scales_packed);
-  return hipGetLastError();
+  constexpr int kPart = 2048;        // rows, whole packed blocks
+  const int64_t rows = (N + kRows - 1) / kRows * kRows, parts = (rows + kPart - 1) / kPart, each = kPart * (K / 8) / 256;
+  return in_launches(parts, each, 256, [&](int64_t p, int64_t n) {
+    const int64_t row = p * kPart, count = std::min(n * kPart, rows - row), words = count * K / 8, total = count * (K / group);
+    hipLaunchKernelGGL(w4_pack_codes_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, stream,
+                       reinterpret_cast<const uint32_t*>(codes + row * (K / 2)), N - row, K, words,
+                       reinterpret_cast<uint32_t*>(codes_packed + row * (K / 2)));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(w4_pack_scales_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, stream, scales + row * (K / group),
+                       N - row, K / group, total, scales_packed + row * (K / group));
+    return hipGetLastError();
+  });
 }
 
 // Splits of K: one launch is faster unless a weight is long and narrow, where too few workgroups would each walk a
