@@ -104,7 +104,7 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
   };
   auto take_logs = [&]() {                      // (apart from the loads, so as not to wait for them)
     v_log = v_scale > 0.0f ? __log2f(v_scale) : kLeastLog;
-    v_inv = v_scale > 0.0f ? 1.0f / v_scale : 0x1p90f;
+    v_inv = kSumBy * (v_scale > 0.0f ? 1.0f / v_scale : 0x1p90f);
   };
 
   struct Codes {
@@ -316,7 +316,7 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
     if (row >= rows) continue;
     const int d0 = DB * (4 * h + wave % 4) + ob;
     if (splits == 1) {
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      const float inv = l > 0.0f ? kSumBy / l : 0.0f;
       uint16_t* dst = y + ((seq * tokens + row / group) * c.heads * group + head * group + row % group) * DIM + d0;
 #pragma unroll
       for (int b = 0; b < OB; b += 2) *reinterpret_cast<uint32_t*>(dst + b) = bf16x2_rne(o[b] * inv, o[b + 1] * inv);
@@ -374,7 +374,7 @@ kv_combine_kernel(int64_t all, int rows, int heads, int group, int splits, uint1
       l += red_sum[g];
     }
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l > 0.0f ? kSumBy / l : 0.0f;
   const int64_t row = index % rows, seq = index / rows / heads, head = index / rows % heads;
   uint16_t* dst = y + ((seq * (rows / group) + row / group) * heads * group + head * group + row % group) * DIM + 4 * col;
   *reinterpret_cast<u32x2*>(dst) = u32x2{bf16x2_rne(o[0] * inv, o[1] * inv), bf16x2_rne(o[2] * inv, o[3] * inv)};

@@ -17,8 +17,10 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr float kLazy = 8.0f;                   // log2 of how far p * scale may pass the running maximum
 constexpr float kProbExp = 7.0f;                // p' < 2^(kLazy + kProbExp); f16 ends at 2^16
-constexpr float kLeastLog = -90.0f;             // values' scales below 2^this count as zero (the sum of p' / scale
-                                                // over 2^30 tokens has to stay in fp32's range)
+constexpr float kLeastLog = -90.0f;             // values' scales below 2^this count as zero
+constexpr float kSumBy = 0x1p-8f;               // sums are held times this: p' / scale < 2^(15 + 90), over 2^30 tokens
+                                                // 2^135, past fp32's range without it (and 2^-8 / scale keeps 13 bits
+                                                // up to a scale of 2^128)
 constexpr int kPiece = 128;                     // pieces of a sequence are whole multiples of this
 
 // Tokens of each of the `splits` pieces of a sequence.

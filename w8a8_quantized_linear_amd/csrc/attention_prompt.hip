@@ -25,7 +25,7 @@ constexpr int kSubs = kTile / 16;               // 16-token runs: no page bounda
 struct Run {
   float k;           // the keys' scale
   float v_log;       // log2 of the values' scale (zeros: kLeastLog)
-  float v_inv;       // 1 / it
+  float v_inv;       // kSumBy / the scale
   int real;          // 0: the table names no page
 };
 
@@ -166,7 +166,7 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
       }
       if (lane == 0) {
         runs[n][stage].v_log = zeros ? kLeastLog : __log2f(run_v[n]);
-        runs[n][stage].v_inv = zeros ? 0x1p90f : 1.0f / run_v[n];
+        runs[n][stage].v_inv = kSumBy * (zeros ? 0x1p90f : 1.0f / run_v[n]);
         runs[n][stage].real = run_v[n] != -1.0f;
       }
     }
@@ -291,7 +291,7 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
   // ---- outputs: register i of block b is dim 32 b + 8 (i / 4) + 4 h + i % 4 ----
   sum = sum_halves(sum);
   if (row0 + r >= rows) return;
-  const float by = splits == 1 ? (sum > 0.0f ? 1.0f / sum : 0.0f) : 1.0f;
+  const float by = splits == 1 ? (sum > 0.0f ? kSumBy / sum : 0.0f) : 1.0f;
   const int64_t index = ((seq * c.heads + head) * rows + row) * splits + split;
   uint16_t* dst = y + ((seq * tokens + row / group) * c.heads * group + head * group + row % group) * DIM;
 #pragma unroll
