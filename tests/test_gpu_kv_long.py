@@ -1,10 +1,12 @@
-"""Attention of long sequences: at the end of the running sum's range."""
+"""Attention where a piece of a sequence is many times what is held at once of the page table, where many pieces meet,
+and at the end of the running sum's range: against 64 bits, with the tolerance of test_gpu_kv_attention.py."""
 import numpy as np
 import pytest
 import torch
 
 from parity import say
-from test_gpu_kv_attention import attend
+from test_gpu_kv_attention import attend, check
+from test_gpu_kv_cache import filled, rows_of, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -15,6 +17,38 @@ def lib():
         pytest.fail("GPU tests need a HIP device")
     import w8a8_quantized_linear_amd as lib
     return lib
+
+
+# Pages of 16 tokens, 64 of which a wave holds at once: one long sequence among so many short ones that it is read in
+# one piece (4,500 tokens: 282 pages) or two (219 pages each, the second from page 219 on), by four waves, one
+# block of rows or two (17 rows and more)
+@pytest.mark.parametrize("tokens,q_heads", ((1, 4), (1, 40), (5, 16), (17, 4)))
+@pytest.mark.parametrize("dim,seqs,length", ((128, 33, 4500), (128, 32, 7000), (64, 66, 4500), (64, 64, 7000)))
+def test_pieces_of_many_pages(lib, dim, seqs, length, tokens, q_heads):
+    heads, page = 4, 16
+    say(f"pieces of many pages dim={dim} seqs={seqs} length={length} tokens={tokens} heads={q_heads}/{heads}")
+    lens = [int(n) for n in np.random.RandomState(seqs).randint(0, 60, seqs)]
+    lens[seqs // 2] = length
+    table, pages = tables(lens, page, 0, 11)
+    need = lib.kv_attention_workspace_bytes(seqs, tokens, q_heads, heads, dim, page, table.shape[1])
+    most = 2 if length == 7000 else 1
+    assert need <= 4 * seqs * tokens * q_heads * most * (dim + 2) + 255      # no more pieces than meant
+    cache = filled(lib, pages, heads, page, dim, 12)
+    q = rows_of(seqs, tokens, q_heads, dim, 13, by=2.0)
+    check(attend(lib, q, cache, table, lens), q, cache, table, lens, dim ** -0.5, "many pages")
+
+
+@pytest.mark.parametrize("lens,q_heads,heads,dim,page", (
+    ([30000], 1, 1, 128, 16), ([30000, 17000], 5, 1, 64, 32), ([131072], 2, 1, 128, 128), ([131072], 1, 1, 64, 16), ([90001], 4, 2, 64, 64)))
+def test_more_than_64_pieces(lib, lens, q_heads, heads, dim, page):
+    """One token over up to 131,072 others, in 65 pieces and more, all of them with keys."""
+    say(f"many pieces lens={lens} heads={q_heads}/{heads} dim={dim} page={page}")
+    table, pages = tables(lens, page, 0, 21)
+    need = lib.kv_attention_workspace_bytes(len(lens), 1, q_heads, heads, dim, page, table.shape[1])
+    assert need >= 4 * len(lens) * q_heads * 65 * (dim + 2)
+    cache = filled(lib, pages, heads, page, dim, 22)
+    q = rows_of(len(lens), 1, q_heads, dim, 23, by=2.0)
+    check(attend(lib, q, cache, table, lens), q, cache, table, lens, dim ** -0.5, "many pieces")
 
 
 def test_the_sum_over_a_long_sequence_of_small_values(lib):
