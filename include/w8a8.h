@@ -317,8 +317,9 @@ w8a8_status w8a8_w4_pack(const uint8_t* codes, const uint16_t* scales, int64_t N
  * result does not depend on the others in the call, nor on their number.  x is taken
  * as finite, with 144 * sum|x| over a group inside fp32 (the sums run over codes with
  * an offset that is taken out again); a token that is not spoils its own row only.  The
- * workspace holds fp32 partial sums where K is long and N small, so that K is cut;
- * w8a8_w4_workspace_bytes is 0, and workspace may be NULL, where it is not. */
+ * workspace holds fp32 partial sums where K is long and N small, so that K is cut,
+ * of up to 1,024 tokens at a time; w8a8_w4_workspace_bytes is 0, and workspace may be
+ * NULL, where it is not. */
 #define W8A8_W4_MAX_M (1 << 20)
 #define W8A8_W4_MAX_N ((1 << 28) - 32)
 size_t w8a8_w4_workspace_bytes(int64_t M, int64_t N, int64_t K);

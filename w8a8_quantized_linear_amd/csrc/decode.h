@@ -32,7 +32,10 @@ hipError_t launch_w4_pack(const uint8_t* codes, const uint16_t* scales, int64_t 
 hipError_t launch_w4_linear(const uint16_t* x, const uint8_t* codes_packed, const uint16_t* scales_packed,
                             const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K, int group,
                             void* workspace, hipStream_t stream);
-int w4_splits(int64_t N, int64_t K);   // parts of K whose fp32 sums [splits][M][N] the workspace holds (1: none)
+// Parts of K whose fp32 sums [splits][min(M, kSplitTokens)][N] the workspace holds (1: none): more tokens are served
+// kSplitTokens at a time.
+constexpr int64_t kSplitTokens = 1024;
+int w4_splits(int64_t N, int64_t K);
 
 // A paged cache of int8 codes as the kernels see it (pointers of w8a8.h's cache
 // arguments): code pages [pages][heads][page][dim], scales [pages][heads].

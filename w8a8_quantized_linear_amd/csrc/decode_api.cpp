@@ -50,7 +50,8 @@ size_t w8a8_w4_scale_bytes(int64_t N, int64_t K, int group) {
 size_t w8a8_w4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K <= 0 || M > W8A8_W4_MAX_M || N > kMaxRows || K > W8A8_MAX_K) return 0;
   const int splits = w8a8::w4_splits(N, K);
-  return splits == 1 ? 0 : align256((size_t)splits * (size_t)M * (size_t)N * sizeof(float));
+  const int64_t tokens = M < w8a8::kSplitTokens ? M : w8a8::kSplitTokens;
+  return splits == 1 ? 0 : align256((size_t)splits * (size_t)tokens * (size_t)N * sizeof(float));
 }
 
 w8a8_status w8a8_w4_quantize(const uint16_t* w, int64_t N, int64_t K, int group, uint8_t* codes, uint16_t* scales,

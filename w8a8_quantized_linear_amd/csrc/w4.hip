@@ -658,10 +658,11 @@ int w4_splits(int64_t N, int64_t K) {
   return blocks <= 512 && K / kCols >= 96 ? 3 : 1;
 }
 
-hipError_t launch_w4_linear(const uint16_t* x, const uint8_t* codes_packed, const uint16_t* scales_packed,
-                            const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K, int group,
-                            void* workspace, hipStream_t stream) {
-  const Linear a{x, codes_packed, scales_packed, bias, y, static_cast<float*>(workspace), M, N, K, group, w4_splits(N, K), stream};
+namespace {
+
+// Up to kSplitTokens tokens, any number where K is not cut.
+hipError_t launch_tokens(const Linear& a) {
+  const int64_t M = a.M, N = a.N;
   const int64_t blocks = (N + kRows - 1) / kRows;
   hipError_t e;
   if (M <= 16) {
@@ -699,9 +700,24 @@ hipError_t launch_w4_linear(const uint16_t* x, const uint8_t* codes_packed, cons
     else e = rb == 2 ? launch_mid<2>(a) : rb == 3 ? launch_mid<3>(a) : launch_mid<4>(a);
   }
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL(w4_combine_kernel, dim3((unsigned)((M * N / 4 + 255) / 256)), dim3(256), 0, stream, a.part, bias, y, M, N,
+  hipLaunchKernelGGL(w4_combine_kernel, dim3((unsigned)((M * N / 4 + 255) / 256)), dim3(256), 0, a.stream, a.part, a.bias, a.y, M, N,
                      a.splits);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_w4_linear(const uint16_t* x, const uint8_t* codes_packed, const uint16_t* scales_packed,
+                            const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K, int group,
+                            void* workspace, hipStream_t stream) {
+  const int splits = w4_splits(N, K);
+  const int64_t most = splits == 1 ? M : kSplitTokens;
+  for (int64_t m = 0; m < M; m += most) {
+    const hipError_t e = launch_tokens({x + m * K, codes_packed, scales_packed, bias, y + m * N, static_cast<float*>(workspace),
+                                        std::min(most, M - m), N, K, group, splits, stream});
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace w8a8
