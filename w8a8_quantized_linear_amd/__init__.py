@@ -539,7 +539,8 @@ def w8a8_w4_linear(x, codes_packed, scales_packed, N: int, group: int, bias=None
 
 # --------------------------- few tokens: a paged 8-bit cache and attention ---
 class KVCache(NamedTuple):
-    """Pages of keys and values: codes int8 [pages, heads, page, dim], scales fp32 [pages, heads]."""
+    """Pages of keys and values: codes int8 [pages, heads, page, dim], scales fp32 [pages, heads]; each begins at a
+    multiple of 16 bytes.  (Tables and lengths may be any contiguous views.)"""
     k_codes: torch.Tensor
     v_codes: torch.Tensor
     k_scale: torch.Tensor

@@ -85,9 +85,14 @@ PyObject* result(w8a8_status st, const at::Tensor& y) {
   return st == W8A8_OK ? THPVariable_Wrap(y) : PyLong_FromLong(st);
 }
 
+// The C entry points take 16-byte aligned pointers; a table or lengths that begin elsewhere (table[1:], lens[1:])
+// are copied, a few bytes per sequence, on the current stream.
+at::Tensor aligned(const at::Tensor& t) { return reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 ? t.clone() : t; }
+
 // A cache with its page table and lengths.
 struct Cache {
-  const at::Tensor *k, *v, *ks, *vs, *table, *lens;
+  const at::Tensor *k, *v, *ks, *vs;
+  at::Tensor table, lens;
   int64_t pages, heads, page, dim, seqs, width;
   int device;
 
@@ -97,21 +102,21 @@ struct Cache {
     v = &want(PyTuple_GET_ITEM(cache, 1), at::kChar, "cache.v_codes", 4, device);
     ks = &want(PyTuple_GET_ITEM(cache, 2), at::kFloat, "cache.k_scale", 2, device);
     vs = &want(PyTuple_GET_ITEM(cache, 3), at::kFloat, "cache.v_scale", 2, device);
-    table = &want(table_, at::kInt, "table", 2, device);
-    lens = &want(lens_, at::kInt, "lens", 1, device);
+    table = aligned(want(table_, at::kInt, "table", 2, device));
+    lens = aligned(want(lens_, at::kInt, "lens", 1, device));
     const auto shape = k->sizes();
     if (v->sizes() != shape || ks->sizes() != shape.slice(0, 2) || vs->sizes() != shape.slice(0, 2))
       fail(PyExc_ValueError, "the cache's tensors disagree on pages, heads, page or dim");
-    if (table->size(0) != lens->size(0)) fail(PyExc_ValueError, "table and lens disagree on the number of sequences");
+    if (table.size(0) != lens.size(0)) fail(PyExc_ValueError, "table and lens disagree on the number of sequences");
     pages = shape[0], heads = shape[1], page = shape[2], dim = shape[3];
-    seqs = table->size(0), width = table->size(1);
+    seqs = table.size(0), width = table.size(1);
   }
   int8_t* k_codes() const { return static_cast<int8_t*>(k->data_ptr()); }
   int8_t* v_codes() const { return static_cast<int8_t*>(v->data_ptr()); }
   float* k_scale() const { return static_cast<float*>(ks->data_ptr()); }
   float* v_scale() const { return static_cast<float*>(vs->data_ptr()); }
-  const int32_t* table_ptr() const { return static_cast<const int32_t*>(table->data_ptr()); }
-  const int32_t* lens_ptr() const { return static_cast<const int32_t*>(lens->data_ptr()); }
+  const int32_t* table_ptr() const { return static_cast<const int32_t*>(table.data_ptr()); }
+  const int32_t* lens_ptr() const { return static_cast<const int32_t*>(lens.data_ptr()); }
 };
 
 // bf16 [seqs, tokens, heads, dim] whose tokens are rows a fixed distance apart (a slice of a wider projection
