@@ -336,7 +336,9 @@ w8a8_status w8a8_w4_linear(const uint16_t* x, const uint8_t* codes_packed, const
  *   lens              int32 [seqs]: tokens a sequence holds, those of the newest
  *                     append included
  * Token p of a sequence is row p % page of page table[p / page].  A negative
- * length counts as 0, one past width * page as width * page.  Table entries
+ * length counts as 0.  Positions follow the lengths as given, also past
+ * width * page, where the table ends: new tokens there are dropped, queries
+ * there see the keys that the table names.  Table entries
  * outside [0, pages) name no page: append drops the tokens that fall there, read
  * gives zeros, attention sees no keys there.  Which pages are whose is the
  * caller's: sequences may share pages that are only read, but two sequences of one
