@@ -316,7 +316,9 @@ w8a8_status w8a8_w4_pack(const uint8_t* codes, const uint16_t* scales, int64_t N
  * 32 or 64 tokens, each of which passes over the weight again.  A token's
  * result does not depend on the others in the call, nor on their number.  x is taken
  * as finite, with 144 * sum|x| over a group inside fp32 (the sums run over codes with
- * an offset that is taken out again); a token that is not spoils its own row only.  The
+ * an offset that is taken out again); a token that is not spoils its own row only.  So a
+ * group's rounding is that of sums up to 144 * sum|x|, about 2^-17 * sum|x| * scale, also
+ * of elements whose codes are 0.  The
  * workspace holds fp32 partial sums where K is long and N small, so that K is cut,
  * of up to 1,024 tokens at a time; w8a8_w4_workspace_bytes is 0, and workspace may be
  * NULL, where it is not. */
