@@ -3,12 +3,13 @@ the 4-bit ones, with the paged 8-bit cache and its attention between them.
 
 What it computes, for x [seqs, tokens, hidden] (the newest tokens of each sequence):
 
-    q, k, v = x Wqkv^T            k and v appended to the cache, q attends to it
+    q, k, v = norm1(x) Wqkv^T     q, k = rotate(q, k); k and v appended to the cache, q attends to it
     x = x + attention Wo^T
-    x = x + (silu(x Wgate^T) * (x Wup^T)) Wdown^T
+    h = norm2(x)
+    x = x + (silu(h Wgate^T) * (h Wup^T)) Wdown^T
 
-Norms and the rotation of q and k by position are the caller's (they are elementwise and not part of this
-library).  Each weight is held twice: int8 for calls of many tokens (one GEMM serves all of them), and
+Norms and the rotation of q and k by position are functions that the caller gives (they are elementwise and not part
+of this library); without them the layer leaves them out.  Each weight is held twice: int8 for calls of many tokens (one GEMM serves all of them), and
 4-bit codes for calls of few, which are bound by the weights' bytes.  Nothing below synchronizes or reads
 device memory on the host, so a step may be captured into a HIP graph and replayed while `lens` grows.
 
@@ -16,7 +17,7 @@ device memory on the host, so a step may be captured into a HIP graph and replay
 """
 from __future__ import annotations
 
-from typing import Optional
+from typing import Callable, Optional, Tuple
 
 import torch
 
@@ -44,29 +45,38 @@ class Projection:
 
 class DecoderLayer:
     """wqkv bf16 [(q_heads + 2 heads) * dim, hidden], wo [hidden, q_heads * dim], wgateup [2 ffn, hidden],
-    wdown [hidden, ffn]; calls of up to `few` tokens in all sequences use 4-bit weights in groups of `group`."""
+    wdown [hidden, ffn]; calls of up to `few` tokens in all sequences use 4-bit weights in groups of `group`.
+    norm1 and norm2: bf16 [tokens, hidden] -> the same, before the attention and before the MLP."""
 
-    def __init__(self, wqkv, wo, wgateup, wdown, q_heads: int, heads: int, dim: int, group: int = 64, few: int = 32):
+    def __init__(self, wqkv, wo, wgateup, wdown, q_heads: int, heads: int, dim: int, group: int = 64, few: int = 32,
+                 norm1: Optional[Callable[[torch.Tensor], torch.Tensor]] = None,
+                 norm2: Optional[Callable[[torch.Tensor], torch.Tensor]] = None):
+        self.norm1, self.norm2 = norm1, norm2
         self.q_heads, self.heads, self.dim, self.ffn = q_heads, heads, dim, wdown.shape[1]
         if wqkv.shape[0] != (q_heads + 2 * heads) * dim or wo.shape[1] != q_heads * dim or wgateup.shape[0] != 2 * self.ffn:
             raise ValueError("weights and head counts disagree")
         self.qkv, self.o, self.gateup, self.down = (Projection(w, group, few) for w in (wqkv, wo, wgateup, wdown))
 
     def __call__(self, x: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor,
-                 scale: Optional[float] = None) -> torch.Tensor:
-        """x bf16 [seqs, tokens, hidden] -> the same shape; lens counts these tokens already."""
+                 scale: Optional[float] = None,
+                 rotate: Optional[Callable[[torch.Tensor, torch.Tensor], Tuple[torch.Tensor, torch.Tensor]]] = None) -> torch.Tensor:
+        """x bf16 [seqs, tokens, hidden] -> the same shape; lens counts these tokens already.  rotate: (q, k), bf16
+        [seqs, tokens, heads, dim] each, at positions lens - tokens .. lens - 1 -> the same, rotated."""
         seqs, tokens, hidden = x.shape
         rows = x.reshape(seqs * tokens, hidden)
-        qkv = self.qkv(rows).view(seqs, tokens, self.q_heads + 2 * self.heads, self.dim)
+        qkv = self.qkv(rows if self.norm1 is None else self.norm1(rows)).view(seqs, tokens, self.q_heads + 2 * self.heads, self.dim)
         q, k, v = qkv.split((self.q_heads, self.heads, self.heads), dim=2)      # slices: none is copied
+        if rotate is not None:
+            q, k = rotate(q, k)
         w8a8_kv_append(k, v, cache, table, lens)
         a = w8a8_kv_attention(q, cache, table, lens, scale)
         rows = rows + self.o(a.view(seqs * tokens, -1))
+        h = rows if self.norm2 is None else self.norm2(rows)
         if rows.shape[0] <= self.gateup.few:
-            h = self.gateup(rows)
+            h = self.gateup(h)
             h = w8a8_swiglu(h[:, :self.ffn], h[:, self.ffn:])
         else:
-            h = w8a8_gateup_swiglu_packed(rows, self.gateup.w8, self.ffn, self.gateup.s8)
+            h = w8a8_gateup_swiglu_packed(h, self.gateup.w8, self.ffn, self.gateup.s8)
         return (rows + self.down(h)).view(seqs, tokens, hidden)
 
 
