@@ -1,4 +1,4 @@
-"""The decoder layer with the caller's norms and rotation of q and k."""
+"""The decoder layer with the caller's norms and rotation of q and k, and calls without a token."""
 import pytest
 import torch
 
@@ -59,3 +59,13 @@ def test_norms_and_rotation(lib, few):
         bare = DecoderLayer(*ws, Q_HEADS, HEADS, DIM, GROUP, few)
         assert not torch.equal(bare(x, paged(lib, 2, 20)[0], table, torch.full_like(lens, tokens)), y)
         done += tokens
+
+
+@pytest.mark.parametrize("seqs,tokens", ((0, 1), (2, 0)))
+def test_a_call_without_a_token(lib, seqs, tokens):
+    from w8a8_quantized_linear_amd.decode import DecoderLayer
+    layer = DecoderLayer(*[w.cuda() for w in weights(5)], Q_HEADS, HEADS, DIM, GROUP)
+    cache, table = paged(lib, 2, 20)
+    lens = torch.full((seqs,), 5, dtype=torch.int32, device="cuda")
+    x = torch.zeros(seqs, tokens, HIDDEN, dtype=torch.bfloat16, device="cuda")
+    assert layer(x, cache, table[:seqs], lens).shape == (seqs, tokens, HIDDEN)

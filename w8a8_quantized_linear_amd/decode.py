@@ -70,7 +70,7 @@ class DecoderLayer:
             q, k = rotate(q, k)
         w8a8_kv_append(k, v, cache, table, lens)
         a = w8a8_kv_attention(q, cache, table, lens, scale)
-        rows = rows + self.o(a.view(seqs * tokens, -1))
+        rows = rows + self.o(a.view(seqs * tokens, self.q_heads * self.dim))
         h = rows if self.norm2 is None else self.norm2(rows)
         if rows.shape[0] <= self.gateup.few:
             h = self.gateup(h)
