@@ -8,7 +8,8 @@ allocate outputs as torch tensors on the current device, pass raw device
 pointers plus ``torch.cuda.current_stream()`` to the C call and turn a non-OK
 status into an exception.  Every step of the computation runs in the library's
 HIP kernels; there is no fallback.  Importing this package without the built
-library raises immediately.
+library raises immediately; the few-token calls raise without _binding.so, the
+compiled part of the binding.
 
 Conventions: bf16 tensors are ``torch.bfloat16``; int8 codes ``torch.int8``;
 E4M3FN codes ``torch.uint8`` (raw codes; view as ``torch.float8_e4m3fn`` if
@@ -38,13 +39,23 @@ __all__ = [
 ]
 
 LIB_PATH = Path(__file__).resolve().parent / "libw8a8.so"
-if not LIB_PATH.exists() or not LIB_PATH.with_name("_binding.so").exists():
+if not LIB_PATH.exists():
     raise ImportError(
-        f"{LIB_PATH} or _binding.so beside it is not built; run `python w8a8_quantized_linear_amd/build.py` "
+        f"{LIB_PATH} is not built; run `python w8a8_quantized_linear_amd/build.py` "
         "(hipcc, gfx950) first -- there is no non-HIP fallback")
 
 _lib = ctypes.CDLL(str(LIB_PATH))
-from . import _binding  # noqa: E402  (the calls for few tokens, which cost less than ctypes' marshalling)
+try:                     # the calls for few tokens, which cost less than ctypes' marshalling
+    from . import _binding
+except ImportError as _why:
+    class _Missing:
+        """Stands for the compiled part where it does not load: its calls raise, those through ctypes work."""
+        why = _why
+
+        def __getattr__(self, name):
+            raise ImportError("this call needs _binding.so beside libw8a8.so; run "
+                              "`python w8a8_quantized_linear_amd/build.py` with torch installed") from self.why
+    _binding = _Missing()
 _P, _I64, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 _SIGS = {
     "w8a8_status_string": (ctypes.c_char_p, [_I]),

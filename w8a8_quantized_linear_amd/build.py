@@ -1,5 +1,5 @@
-"""Build ``libw8a8.so`` (the C-ABI library) for gfx950 with hipcc, and the compiled
-part of its Python binding with the host compiler, in-tree.
+"""Build ``libw8a8.so`` (the C-ABI library) for gfx950 with hipcc, and, where torch is installed,
+the compiled part of its Python binding with the host compiler, in-tree.
 
     python w8a8_quantized_linear_amd/build.py
 
@@ -10,6 +10,7 @@ and the correctly rounded fp32 divide the quantizer relies on.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
@@ -105,16 +106,20 @@ def _link_binding(obj: Path) -> None:
 
 
 def build() -> Path:
-    """Build libw8a8.so (the library), _binding.so (the compiled part of its Python binding) and
-    probe/libw8a8_probe.so (measurement aids)."""
+    """Build libw8a8.so (the library), probe/libw8a8_probe.so (measurement aids) and _binding.so (the
+    compiled part of the Python binding; left out without torch, which the library by itself does not need)."""
     BUILD_DIR.mkdir(exist_ok=True)
     jobs = [(src, CSRC, "") for src in SOURCES] + [(src, PROBE_DIR, "probe_") for src in PROBE_SOURCES]
+    torch = importlib.util.find_spec("torch") is not None
     with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = ex.submit(_compile_binding) if torch else None
         objs = list(ex.map(lambda j: _compile(*j), jobs))
     _link(objs[:len(SOURCES)], LIB)
-    _link_binding(binding.result())
     _link(objs[len(SOURCES):], PROBE_LIB)
+    if binding is None:
+        print("torch is not installed: _binding.so is left out", file=sys.stderr)
+    else:
+        _link_binding(binding.result())
     return LIB
 
 
