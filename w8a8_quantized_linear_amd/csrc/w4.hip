@@ -250,6 +250,7 @@ w4_few_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, con
 }
 
 __device__ __forceinline__ void lds_barrier() {       // __syncthreads would wait for the loads in flight, too
+  asm volatile("" ::: "memory");                      // (no store moves below the wait, no load above the barrier)
   __builtin_amdgcn_s_waitcnt(0xc07f);                 // lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
