@@ -104,7 +104,7 @@ kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int 
   };
   auto take_logs = [&]() {                      // (apart from the loads, so as not to wait for them)
     v_log = v_scale > 0.0f ? __log2f(v_scale) : kLeastLog;
-    v_inv = kSumBy * (v_scale > 0.0f ? 1.0f / v_scale : 0x1p90f);
+    v_inv = v_scale > 0.0f ? kSumBy / v_scale : kSumBy * 0x1p90f;
   };
 
   struct Codes {

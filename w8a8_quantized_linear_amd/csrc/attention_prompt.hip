@@ -166,7 +166,7 @@ kv_prompt_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tok
       }
       if (lane == 0) {
         runs[n][stage].v_log = zeros ? kLeastLog : __log2f(run_v[n]);
-        runs[n][stage].v_inv = kSumBy * (zeros ? 0x1p90f : 1.0f / run_v[n]);
+        runs[n][stage].v_inv = zeros ? kSumBy * 0x1p90f : kSumBy / run_v[n];
         runs[n][stage].real = run_v[n] != -1.0f;
       }
     }
