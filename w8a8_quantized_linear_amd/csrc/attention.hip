@@ -40,7 +40,7 @@ __device__ __forceinline__ float lane_value(float v, int lane) {
 //   O^T += V^T P^T: P^T is S^T's layout as it stands; V^T takes byte b of a lane's eight values as output block b,
 //   so one 8-byte piece per token serves all blocks and nothing is transposed through LDS.
 // One token of 131,072 (32/8 heads of 128): 48 us and 4 for the pieces' joining (5.1 TB/s); 32 sequences of up to 2,270
-// (40/8 heads) 23 us; 298 tokens (16 heads of 64) 6.4 us, the length of the chain.  Codes two or three steps ahead were 3 to 8% slower.
+// (40/8 heads) 23 us; 298 tokens (16 heads of 64) 5.7 us, the length of the chain.  Codes two or three steps ahead were 3 to 8% slower.
 template <int DIM, int NB, int W>
 __global__ void __launch_bounds__(64 * W)
 kv_attention_kernel(KvCache c, const uint16_t* __restrict__ q, int64_t ldq, int tokens, int group, float scale,

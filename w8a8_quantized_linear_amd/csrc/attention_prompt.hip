@@ -10,7 +10,8 @@
 // The units overlap only in part (two waves of a SIMD, one with products and one with multiply-adds, together take
 // 0.71 of the sum of their times; products and exponentials overlap fully, measured), so ~1,500 is what a tile
 // could take; it takes about 2,600: two waves a SIMD leave waits for LDS, for the products and at the barrier.  Four
-// prompts of 1,502 tokens (40/8 heads of 128) take 142 us (651 TFLOP/s), 500 tokens behind 12,016 (32/8) 120 us (803).
+// prompts of 1,502 tokens (40/8 heads of 128) take 140 us (660 TFLOP/s), 500 tokens behind 12,016 (32/8) 120 us (800);
+// at 64 dims, with half the products for the same softmax, 98 us (471) and 90 us (535).
 #include <algorithm>
 
 #include "attention_math.h"

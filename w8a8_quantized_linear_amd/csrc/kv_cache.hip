@@ -12,7 +12,7 @@
 //
 // Bound: memory traffic (append 2 bytes read and 1 written per value, read 1 and 2) and, for single tokens,
 // latency.  8 sequences of 1,502 tokens (8 heads of 128): append 17.8 us (4.1 TB/s), read 16.2 us (4.6 TB/s; a copy of
-// 2 GiB reaches 4.9); one token for each of 61 sequences of up to 299 tokens 4.2 us, their read 8.9 us.
+// 2 GiB reaches 4.9); one token for each of 61 sequences of up to 299 tokens 4.5 us, their read 8.6 us.
 #include "decode.h"
 #include "epilogue_math.h"
 #include "quant_math.h"
