@@ -53,3 +53,21 @@ def test_append(lib):
     for a, b in zip(big, small):
         assert torch.equal(a, b)
     assert not torch.equal(small.k_codes, filled(lib, len(held), HEADS, PAGE, DIM, 4).k_codes)
+
+
+def test_read(lib):
+    """2^20 sequences of 257 positions, 17 workgroups each: keys and values of 69 GB, read in two launches of 986,895
+    sequences at most."""
+    seqs, length, page, dim = 1 << 20, 257, 128, 128
+    say(f"read of {seqs} sequences of {length}")
+    cache = filled(lib, 5, 1, page, dim, 5)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    table = torch.randint(0, 5, (seqs, 3), generator=g, device="cuda").to(torch.int32)
+    lens = torch.randint(0, 300, (seqs,), generator=g, device="cuda").to(torch.int32)
+    k, v = lib.w8a8_kv_read(cache, table, lens, length)
+    for a in (0, 61679, 986892, seqs - 8):
+        few = slice(a, a + 8)
+        for big, small in zip((k, v), lib.w8a8_kv_read(cache, table[few].clone(), lens[few].clone(), length)):
+            assert torch.equal(big[few], small), a
+    del k, v
+    torch.cuda.empty_cache()
