@@ -69,7 +69,7 @@ typedef enum {
   W8A8_ERR_NULL_POINTER = 1,       /* a required pointer is NULL (bias may be NULL) */
   W8A8_ERR_BAD_SHAPE = 2,          /* M < 0, N or K out of range or not a multiple as required */
   W8A8_ERR_MISALIGNED = 3,         /* a pointer is not 16-byte aligned */
-  W8A8_ERR_BAD_ARGUMENT = 4,       /* rot_block not 0/128, or the workspace is too small */
+  W8A8_ERR_BAD_ARGUMENT = 4,       /* a scalar argument outside its values (rot_block: 0 or 128), or the workspace is too small */
   W8A8_ERR_UNSUPPORTED_DEVICE = 5, /* no HIP device, or the current device is not gfx950 */
   W8A8_ERR_LAUNCH = 6,             /* the kernel launch itself failed (hipGetLastError) */
   W8A8_ERR_SCRATCH_TOO_SMALL = 7   /* w8a8_linear_packed_noalloc: the call needs more than
@@ -402,6 +402,93 @@ w8a8_status w8a8_kv_attention(const uint16_t* q, int64_t ldq, const int8_t* k_co
                               int64_t width, const int32_t* lens, int64_t seqs, int64_t tokens, int64_t q_heads,
                               int64_t heads, int64_t dim, int64_t page, float scale, uint16_t* y, void* workspace,
                               size_t workspace_bytes, hipStream_t stream);
+
+/* ---- around the projections: root-mean-square norm, after the residual's addition ----
+ * For rows x [M, K] bf16, residual bf16 [M, K] or NULL, weight bf16 [K]:
+ *   h = bf16(x + residual) (fp32 sum; h = x without a residual)
+ *   z = h * weight,  r = 1 / sqrt(mean(h^2) + eps),  y = z * r
+ * with fp32 sums.  `h`, if not NULL, receives h [M, K] (what the next addition takes); it may be the
+ * residual's buffer or x's (in place).  Outputs:
+ *   w8a8_rmsnorm               y bf16 [M, K]; it may be x's buffer
+ *   ..._quantize               int8 codes, s_tok fp32 [M] = amax|y| / 127
+ *   ..._quantize_fp8           E4M3FN codes, s_tok fp32 [M] = amax|y| / 448
+ *   ..._quantize_block         E4M3FN codes, a scale for each 128 columns, amax|y| / 448 of those
+ * The codes are those of w8a8_quantize_act* for the values z, which are common multiples of y: y is not
+ * rounded to bf16 on the way.  rot_block == 128: codes of y turned by the normalized transform in blocks of
+ * 128, in fp32.  Row-major codes are [M, K], their block scales [M, K / 128]; the _packed forms write the
+ * packed layout (padding rows untouched), with block scales [K / 128][w8a8_block_scale_stride(M)].
+ * A row of zeros gives zeros.  A row with a NaN or an infinity, or whose h^2 leave fp32's range
+ * (|h| beyond about 2^60), spoils its own row only.
+ * 1 <= K <= W8A8_MAX_K, K % 8 == 0 (codes: K % 32 == 0; packed: K % 64 == 0; rot_block or block scales:
+ * K % 128 == 0); eps finite and positive (W8A8_ERR_BAD_ARGUMENT otherwise). */
+w8a8_status w8a8_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps, uint16_t* h,
+                         uint16_t* y, int64_t M, int64_t K, hipStream_t stream);
+w8a8_status w8a8_rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps,
+                                  int rot_block, uint16_t* h, int8_t* q, float* s_tok, int64_t M, int64_t K,
+                                  hipStream_t stream);
+w8a8_status w8a8_rmsnorm_quantize_packed(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps,
+                                         int rot_block, uint16_t* h, int8_t* q_packed, float* s_tok, int64_t M,
+                                         int64_t K, hipStream_t stream);
+w8a8_status w8a8_rmsnorm_quantize_fp8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps,
+                                      int rot_block, uint16_t* h, uint8_t* q, float* s_tok, int64_t M, int64_t K,
+                                      hipStream_t stream);
+w8a8_status w8a8_rmsnorm_quantize_fp8_packed(const uint16_t* x, const uint16_t* residual, const uint16_t* weight,
+                                             float eps, int rot_block, uint16_t* h, uint8_t* q_packed, float* s_tok,
+                                             int64_t M, int64_t K, hipStream_t stream);
+w8a8_status w8a8_rmsnorm_quantize_block(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps,
+                                        uint16_t* h, uint8_t* q, float* s, int64_t M, int64_t K, hipStream_t stream);
+w8a8_status w8a8_rmsnorm_quantize_block_packed(const uint16_t* x, const uint16_t* residual, const uint16_t* weight,
+                                               float eps, uint16_t* h, uint8_t* q_packed, float* s, int64_t M,
+                                               int64_t K, hipStream_t stream);
+
+/* ---- around the attention: rotary positions of queries and keys ------------------
+ * q rows [seqs * tokens] of [q_heads, dim] and k rows of [heads, dim], bf16, ldq and ldk elements apart
+ * (>= heads * dim, a multiple of 8: slices of one projection), as w8a8_kv_append and w8a8_kv_attention take
+ * them; row i of a sequence is at position p = lens - tokens + i (a negative length counts as 0).  The
+ * first `rotary` values of each head are turned in pairs, (i, i + rotary / 2) or, with `interleaved`,
+ * (2i, 2i + 1):
+ *   (a, b) -> amplitude * (a cos t - b sin t, b cos t + a sin t),  t = p * f_i,
+ * in fp32, rounded once; the rest of the head, and rows at p < 0, are copied.  turns[i] is
+ * round(2^64 * f_i / (2 pi)) mod 2^64: frequencies as fractions of a turn, so that angles keep 2^-32 of a turn at
+ * every position (f_i's own error, times p, comes on top).  q_out and k_out: rows of their own strides, or q and k
+ * themselves (in place: same pointer and stride).  heads may be 0 (queries alone; k and k_out are not read then).
+ * dim % 16 == 0, 16 <= dim <= 256; rotary % 16 == 0, 16 <= rotary <= dim; q_heads and heads up to
+ * W8A8_KV_MAX_HEADS, q_heads >= 1; seqs and tokens as for the cache, seqs * tokens < 2^31; amplitude finite. */
+w8a8_status w8a8_rope(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint64_t* turns, int64_t rotary,
+                      int interleaved, float amplitude, const int32_t* lens, int64_t seqs, int64_t tokens, int64_t q_heads,
+                      int64_t heads, int64_t dim, uint16_t* q_out, int64_t ldq_out, uint16_t* k_out, int64_t ldk_out,
+                      hipStream_t stream);
+
+/* ---- E4M3 projections with block scales ------------------------------------------
+ * Codes E4M3FN; an activation's value is code * s of its token and 128 columns, a weight's code * s of its block of
+ * 128 x 128 (rows past N are not counted).  scale = amax / 448 (fp32 IEEE division), code as w8a8_quantize_act_fp8's;
+ * a block of zeros has scale 0 and codes 0. */
+
+/* Row stride of the scales that go with packed codes of M rows: M rounded up to a multiple of 32 (0 outside 1 .. 2^42). */
+int64_t w8a8_block_scale_stride(int64_t M);
+
+/* x bf16 [M, K] -> codes [M, K], s fp32 [M, K / 128]; packed: s [K / 128][w8a8_block_scale_stride(M)] (padding
+ * untouched in both).  K % 128 == 0, M * K <= 2^42. */
+w8a8_status w8a8_quantize_act_block(const uint16_t* x, int64_t M, int64_t K, uint8_t* q, float* s, hipStream_t stream);
+w8a8_status w8a8_quantize_act_block_packed(const uint16_t* x, int64_t M, int64_t K, uint8_t* q_packed, float* s,
+                                           hipStream_t stream);
+/* w bf16 [N, K] -> codes [N, K] (lay them out with w8a8_pack_weight), s fp32 [ceil(N / 128), K / 128]. */
+w8a8_status w8a8_quantize_weight_block(const uint16_t* w, int64_t N, int64_t K, uint8_t* q, float* s, hipStream_t stream);
+
+/* y[m][n] = bf16( sum_b s[b][m] * s_w[n / 128][b] * sum_{k in b} q[m][k] * w[n][k] + bias[n] ).  The inner sums run on
+ * the E4M3 matrix instructions, which drop what lies 2^-13 below the largest of a group of their products (1.4e-5 of
+ * the output's rms on normal values, 4e-5 with outliers of 20 times); the sum over blocks is fp32, rounded once.
+ * Which form multiplies, and with it the order of the sum over blocks, depends on M, N and K.
+ * M * N <= 2^40, N <= 2^28 - 32, M <= 2^30; a token that is not finite spoils its own row only. */
+w8a8_status w8a8_fp8_block_gemm_packed(const uint8_t* q_packed, const float* s, const uint8_t* w_packed, const float* s_w,
+                                       const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K,
+                                       hipStream_t stream);
+
+/* x is quantized into the workspace, then multiplied.  The workspace holds the packed codes and their scales. */
+size_t w8a8_fp8_block_workspace_bytes(int64_t M, int64_t K);   /* 0 for M <= 0 or K <= 0 */
+w8a8_status w8a8_fp8_block_linear_packed(const uint16_t* x, const uint8_t* w_packed, const float* s_w, const uint16_t* bias,
+                                         uint16_t* y, int64_t M, int64_t N, int64_t K, void* workspace,
+                                         size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,6 +1,7 @@
 """Python binding of the MI355X W8A8 quantized projection library (``libw8a8.so``),
-with its operators for few tokens: 4-bit-weight projections, a paged 8-bit cache
-of keys and values, and attention over it.
+with its operators for few tokens (4-bit-weight projections, a paged 8-bit cache
+of keys and values, attention over it) and those around them (norms, rotary
+positions, E4M3 projections with block scales).
 
 The functions below carry the names of the C entry points declared in
 ``include/w8a8.h`` and only marshal arguments: they check dtypes/devices,
@@ -8,8 +9,8 @@ allocate outputs as torch tensors on the current device, pass raw device
 pointers plus ``torch.cuda.current_stream()`` to the C call and turn a non-OK
 status into an exception.  Every step of the computation runs in the library's
 HIP kernels; there is no fallback.  Importing this package without the built
-library raises immediately; the few-token calls raise without _binding.so, the
-compiled part of the binding.
+library raises immediately; the calls of a few microseconds raise without
+_binding.so, the compiled part of the binding.
 
 Conventions: bf16 tensors are ``torch.bfloat16``; int8 codes ``torch.int8``;
 E4M3FN codes ``torch.uint8`` (raw codes; view as ``torch.float8_e4m3fn`` if
@@ -19,8 +20,9 @@ aligned and on the current CUDA (HIP) device.
 from __future__ import annotations
 
 import ctypes
+import math
 from pathlib import Path
-from typing import NamedTuple, Optional, Tuple
+from typing import List, NamedTuple, Optional, Tuple
 
 import torch
 
@@ -36,6 +38,11 @@ __all__ = [
     "w8a8_w4_quantize", "w8a8_w4_pack", "w8a8_w4_linear", "w4_code_bytes", "w4_scale_bytes",
     "w4_workspace_bytes", "KVCache", "kv_cache",
     "w8a8_kv_append", "w8a8_kv_read", "w8a8_kv_attention", "kv_attention_workspace_bytes",
+    "w8a8_rmsnorm", "w8a8_rmsnorm_quantize", "w8a8_rmsnorm_quantize_packed", "w8a8_rmsnorm_quantize_fp8",
+    "w8a8_rmsnorm_quantize_fp8_packed", "w8a8_rmsnorm_quantize_block", "w8a8_rmsnorm_quantize_block_packed",
+    "Rope", "rope_frequencies", "rope", "w8a8_rope",
+    "block_scale_stride", "w8a8_quantize_act_block", "w8a8_quantize_act_block_packed", "w8a8_quantize_weight_block",
+    "fp8_block_workspace_bytes", "w8a8_fp8_block_gemm_packed", "w8a8_fp8_block_linear_packed",
 ]
 
 LIB_PATH = Path(__file__).resolve().parent / "libw8a8.so"
@@ -45,7 +52,7 @@ if not LIB_PATH.exists():
         "(hipcc, gfx950) first -- there is no non-HIP fallback")
 
 _lib = ctypes.CDLL(str(LIB_PATH))
-try:                     # the calls for few tokens, which cost less than ctypes' marshalling
+try:                     # the calls of a few microseconds, which cost less than ctypes' marshalling
     from . import _binding
 except ImportError as _why:
     class _Missing:
@@ -90,6 +97,12 @@ _SIGS = {
     "w8a8_w4_pack": (_I, [_P, _P, _I64, _I64, _I, _P, _P, _P]),
     "w8a8_w4_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "w8a8_kv_attention_workspace_bytes": (_SZ, [_I64] * 7),
+    "w8a8_block_scale_stride": (_I64, [_I64]),
+    "w8a8_quantize_act_block": (_I, [_P, _I64, _I64, _P, _P, _P]),
+    "w8a8_quantize_act_block_packed": (_I, [_P, _I64, _I64, _P, _P, _P]),
+    "w8a8_quantize_weight_block": (_I, [_P, _I64, _I64, _P, _P, _P]),
+    "w8a8_fp8_block_workspace_bytes": (_SZ, [_I64, _I64]),
+    "w8a8_fp8_block_gemm_packed": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -592,3 +605,183 @@ def w8a8_kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens
     and values first).  scale defaults to dim^-0.5.  Queries that see no key give zeros."""
     y = _binding.kv_attention(q, cache, table, lens, scale, workspace, out, _raw_stream(_raw_device()))
     return y if type(y) is not int else _check(y, "w8a8_kv_attention")
+
+
+# --------------------------------- around the projections: RMS norm ----------
+def _norm(name, form, packed, x, weight, residual, eps, rot_block, h, out, scales):
+    got = _binding.rmsnorm(x, weight, residual, eps, form, rot_block, packed, h, out, scales, _raw_stream(_raw_device()))
+    return got if type(got) is not int else _check(got, name)
+
+
+def w8a8_rmsnorm(x, weight, residual=None, eps: float = 1e-6, out=None, h=None):
+    """(y, h): h = x + residual (bf16 [M, K]; None without a residual), y = h / sqrt(mean(h^2) + eps) * weight bf16 [M, K].
+    h may be given: a tensor of its own, or the residual itself (updated in place)."""
+    got = _norm("w8a8_rmsnorm", 0, False, x, weight, residual, eps, 0, h, out, None)
+    return got[0], got[2]
+
+
+def w8a8_rmsnorm_quantize(x, weight, residual=None, eps: float = 1e-6, rot_block: int = 0, h=None, out=None):
+    """The norm's values y as int8 codes with one scale a token: (q int8 [M, K], s fp32 [M], h); y is not rounded to bf16 first.
+    rot_block = 128 turns y by the normalized Walsh-Hadamard transform in blocks of 128.  out = (q, s)."""
+    return _norm("w8a8_rmsnorm_quantize", 1, False, x, weight, residual, eps, rot_block, h, *(out or (None, None)))
+
+
+def w8a8_rmsnorm_quantize_packed(x, weight, residual=None, eps: float = 1e-6, rot_block: int = 0, h=None, out=None):
+    """w8a8_rmsnorm_quantize with the codes in the packed layout (flat), as w8a8_gemm_dequant_packed takes them."""
+    return _norm("w8a8_rmsnorm_quantize_packed", 1, True, x, weight, residual, eps, rot_block, h, *(out or (None, None)))
+
+
+def w8a8_rmsnorm_quantize_fp8(x, weight, residual=None, eps: float = 1e-6, rot_block: int = 0, h=None, out=None):
+    """The norm's values as E4M3FN codes with one scale a token: (q uint8 [M, K], s fp32 [M], h)."""
+    return _norm("w8a8_rmsnorm_quantize_fp8", 2, False, x, weight, residual, eps, rot_block, h, *(out or (None, None)))
+
+
+def w8a8_rmsnorm_quantize_fp8_packed(x, weight, residual=None, eps: float = 1e-6, rot_block: int = 0, h=None, out=None):
+    """w8a8_rmsnorm_quantize_fp8 with the codes in the packed layout (flat), as w8a8_fp8_gemm_dequant_packed takes them."""
+    return _norm("w8a8_rmsnorm_quantize_fp8_packed", 2, True, x, weight, residual, eps, rot_block, h, *(out or (None, None)))
+
+
+def w8a8_rmsnorm_quantize_block(x, weight, residual=None, eps: float = 1e-6, h=None, out=None):
+    """The norm's values as E4M3FN codes with a scale for each 128 columns: (q uint8 [M, K], s fp32 [M, K / 128], h)."""
+    return _norm("w8a8_rmsnorm_quantize_block", 3, False, x, weight, residual, eps, 0, h, *(out or (None, None)))
+
+
+def w8a8_rmsnorm_quantize_block_packed(x, weight, residual=None, eps: float = 1e-6, h=None, out=None):
+    """w8a8_rmsnorm_quantize_block as w8a8_fp8_block_gemm_packed takes it: codes in the packed layout (flat), scales
+    [K / 128, block_scale_stride(M)]."""
+    return _norm("w8a8_rmsnorm_quantize_block_packed", 3, True, x, weight, residual, eps, 0, h, *(out or (None, None)))
+
+
+# ------------------------------- around the attention: rotary positions ------
+class Rope(NamedTuple):
+    """How positions turn the first 2 * len(turns) values of a head: turns int64, pair i's frequency f_i as
+    round(2^64 f_i / (2 pi)) mod 2^64 (two's complement); interleaved: pairs (2i, 2i + 1) instead of (i, i + half); amplitude:
+    what the turned values are multiplied by."""
+    turns: torch.Tensor
+    interleaved: bool = False
+    amplitude: float = 1.0
+
+
+def rope_frequencies(rotary: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0, original: int = 4096,
+                     low: float = 1.0, high: float = 4.0, fast: float = 32.0, slow: float = 1.0) -> Tuple[List[float], float]:
+    """Frequencies f_i = base^(-2i / rotary) in radians a position, i < rotary / 2, and the amplitude, for contexts `factor` times
+    the `original` length:
+
+    None          as they are
+    "linear"      f / factor
+    "ntk"         base * factor^(rotary / (rotary - 2)) as base: the slowest f divided by factor, the fastest kept
+    "wavelength"  by the turns g = original f / (2 pi) that a pair makes over the original length: f above `high` turns, f / factor
+                  below `low`, between them in proportion to (g - low) / (high - low)
+    "yarn"        f between `fast` turns and f / factor below `slow`, in proportion to the index i between the (whole) indices
+                  at which a pair makes these turns; amplitude 0.1 ln(factor) + 1"""
+    if rotary < 2 or rotary % 2:
+        raise ValueError(f"rotary: expected an even number, got {rotary}")
+    if not (base > 0 and math.isfinite(base) and factor > 0 and math.isfinite(factor) and original > 0):
+        raise ValueError("base, factor and original must be positive and finite")
+    if scaling == "ntk" and rotary > 2:
+        base *= factor ** (rotary / (rotary - 2))
+    f = [base ** (-2 * i / rotary) for i in range(rotary // 2)]
+    if scaling in (None, "ntk"):
+        return f, 1.0
+    if scaling == "linear":
+        return [v / factor for v in f], 1.0
+    if scaling == "wavelength":
+        if not high > low:
+            raise ValueError("high must be above low")
+        keep = [min(1.0, max(0.0, (original * v / (2 * math.pi) - low) / (high - low))) for v in f]
+        return [v * g + v / factor * (1 - g) for v, g in zip(f, keep)], 1.0
+    if scaling == "yarn":
+        if not (fast > 0 and slow > 0) or base == 1:
+            raise ValueError("fast and slow must be positive, and base not 1")
+        first, last = (rotary * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base)) for turns in (fast, slow))
+        first, last = max(math.floor(first), 0), min(math.ceil(last), rotary - 1)
+        part = [min(1.0, max(0.0, (i - first) / max(last - first, 1e-3))) for i in range(rotary // 2)]
+        return [v / factor * g + v * (1 - g) for v, g in zip(f, part)], 0.1 * math.log(factor) + 1.0
+    raise ValueError(f"scaling: expected None, 'linear', 'ntk', 'wavelength' or 'yarn', got {scaling!r}")
+
+
+def rope(rotary: int, base: float = 10000.0, interleaved: bool = False, device=None, **scaling) -> Rope:
+    """The plan of w8a8_rope for the first `rotary` values of a head (a multiple of 16); keywords as rope_frequencies."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    f, amplitude = rope_frequencies(rotary, base, **scaling)
+    turns = [round(v / (2 * math.pi) * 2.0 ** 64) % (1 << 64) for v in f]
+    return Rope(torch.tensor([v - (1 << 64) if v >> 63 else v for v in turns], dtype=torch.int64, device=device), interleaved, amplitude)
+
+
+def w8a8_rope(q, k, lens, rope: Rope, out=None):
+    """(q, k): q bf16 [seqs, tokens, q_heads, dim] and k bf16 [seqs, tokens, heads, dim] (or None) turned by their positions
+    lens - tokens .. lens - 1 (lens int32 [seqs], as for the cache); both may be slices of one projection.  out = (q, k) gives the
+    outputs: tensors or slices of the same shapes, or q and k themselves (in place)."""
+    turns, interleaved, amplitude = rope
+    q_out, k_out = out if out is not None else (None, None)
+    got = _binding.rope(q, k, lens, turns, interleaved, amplitude, q_out, k_out, _raw_stream(_raw_device()))
+    return got if type(got) is not int else _check(got, "w8a8_rope")
+
+
+# ------------------------------------ E4M3 projections with block scales -----
+def block_scale_stride(M: int) -> int:
+    return int(_lib.w8a8_block_scale_stride(M))
+
+
+def w8a8_quantize_act_block(x: torch.Tensor, out=None):
+    """x bf16 [M, K] -> (E4M3FN codes uint8 [M, K], s fp32 [M, K / 128]): a scale for each token and 128 columns."""
+    _want(x, torch.bfloat16, "x", 2)
+    M, K = x.shape
+    q0, s0 = out if out is not None else (None, None)
+    q = _out(q0, torch.uint8, M * K, "q", x.device, shape=(M, K))
+    s = _out(s0, torch.float32, M * (K // 128), "s", x.device, shape=(M, K // 128))
+    _check(_lib.w8a8_quantize_act_block(_ptr(x), M, K, _ptr(q), _ptr(s), _stream()), "w8a8_quantize_act_block")
+    return q, s
+
+
+def w8a8_quantize_act_block_packed(x: torch.Tensor, out=None):
+    """The same in the layouts that w8a8_fp8_block_gemm_packed takes: codes packed (flat), s [K / 128, block_scale_stride(M)]."""
+    _want(x, torch.bfloat16, "x", 2)
+    M, K = x.shape
+    q0, s0 = out if out is not None else (None, None)
+    q = _out(q0, torch.uint8, packed_bytes(M, K), "q", x.device)
+    s = _out(s0, torch.float32, K // 128 * block_scale_stride(M), "s", x.device, shape=(K // 128, block_scale_stride(M)))
+    _check(_lib.w8a8_quantize_act_block_packed(_ptr(x), M, K, _ptr(q), _ptr(s), _stream()), "w8a8_quantize_act_block_packed")
+    return q, s
+
+
+def w8a8_quantize_weight_block(w: torch.Tensor):
+    """w bf16 [N, K] -> (E4M3FN codes uint8 [N, K], s fp32 [ceil(N / 128), K / 128]): a scale for each block of 128 x 128.
+    w8a8_pack_weight lays the codes out, once, at load time."""
+    _want(w, torch.bfloat16, "w", 2)
+    N, K = w.shape
+    q = torch.empty((N, K), dtype=torch.uint8, device=w.device)
+    s = torch.empty((-(-N // 128), K // 128), dtype=torch.float32, device=w.device)
+    _check(_lib.w8a8_quantize_weight_block(_ptr(w), N, K, _ptr(q), _ptr(s), _stream()), "w8a8_quantize_weight_block")
+    return q, s
+
+
+def w8a8_fp8_block_gemm_packed(q_packed, s, w_packed, s_w, M: int, N: int, K: int, bias=None, out=None):
+    """y bf16 [M, N] from packed E4M3FN codes of M tokens and N weight rows and their block scales."""
+    _want(q_packed, torch.uint8, "q_packed", 1)
+    _want(w_packed, torch.uint8, "w_packed", 1)
+    _want(s, torch.float32, "s", 2)
+    _want(s_w, torch.float32, "s_w", 2)
+    if bias is not None:
+        _want(bias, torch.bfloat16, "bias", 1)
+    if q_packed.numel() < packed_bytes(M, K) or w_packed.numel() < packed_bytes(N, K):
+        raise ValueError("packed operands smaller than packed_bytes(rows, K)")
+    if tuple(s.shape) != (K // 128, block_scale_stride(M)) or tuple(s_w.shape) != (-(-N // 128), K // 128):
+        raise ValueError("inconsistent shapes")
+    if bias is not None and bias.shape[0] != N:
+        raise ValueError("bias length must equal N")
+    y = _out(out, torch.bfloat16, M * N, "out", q_packed.device, shape=(M, N))
+    _check(_lib.w8a8_fp8_block_gemm_packed(_ptr(q_packed), _ptr(s), _ptr(w_packed), _ptr(s_w), _ptr(bias), _ptr(y), M, N, K,
+                                           _stream()), "w8a8_fp8_block_gemm_packed")
+    return y
+
+
+def fp8_block_workspace_bytes(M: int, K: int) -> int:
+    return int(_lib.w8a8_fp8_block_workspace_bytes(M, K))
+
+
+def w8a8_fp8_block_linear_packed(x, w_packed, N: int, s_w, bias=None, workspace=None, out=None):
+    """y bf16 [M, N] = x bf16 [M, K] . w^T + bias: x quantized to E4M3FN with a scale for each token and 128 columns, the weight
+    [N, K] packed (w8a8_pack_weight) with a scale for each block of 128 x 128 (w8a8_quantize_weight_block)."""
+    y = _binding.fp8_block_linear(x, w_packed, N, s_w, bias, workspace, out, _raw_stream(_raw_device()))
+    return y if type(y) is not int else _check(y, "w8a8_fp8_block_linear_packed")

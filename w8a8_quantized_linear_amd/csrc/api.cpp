@@ -163,7 +163,7 @@ const char* w8a8_status_string(w8a8_status s) {
     case W8A8_ERR_NULL_POINTER: return "W8A8_ERR_NULL_POINTER: a required pointer is NULL";
     case W8A8_ERR_BAD_SHAPE: return "W8A8_ERR_BAD_SHAPE: M, N or K outside the supported range";
     case W8A8_ERR_MISALIGNED: return "W8A8_ERR_MISALIGNED: a pointer is not 16-byte aligned";
-    case W8A8_ERR_BAD_ARGUMENT: return "W8A8_ERR_BAD_ARGUMENT: rot_block not 0/128 or workspace too small";
+    case W8A8_ERR_BAD_ARGUMENT: return "W8A8_ERR_BAD_ARGUMENT: a scalar argument outside its values (rot_block: 0 or 128), or workspace too small";
     case W8A8_ERR_UNSUPPORTED_DEVICE: return "W8A8_ERR_UNSUPPORTED_DEVICE: no gfx950 HIP device is current";
     case W8A8_ERR_LAUNCH: return "W8A8_ERR_LAUNCH: kernel launch failed";
     case W8A8_ERR_SCRATCH_TOO_SMALL:

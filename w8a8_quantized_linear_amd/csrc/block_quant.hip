@@ -1,0 +1,79 @@
+// E4M3 codes with block scales: one for each 128 columns of an activation's row, one for each 128 x 128 block of a
+// weight.  scale = amax / 448, code = the nearest E4M3 value to x / scale; a block of zeros has scale 0 and codes 0.
+#include "decode.h"
+#include "layer.h"
+#include "layer_math.h"
+
+namespace w8a8 {
+namespace {
+
+using namespace lm;
+
+constexpr int kThreads = 256;
+
+// 8 columns a thread, so that 16 lanes hold a block: two bytes read and one written a value, nothing shared.
+__global__ void __launch_bounds__(kThreads)
+quantize_block(const uint16_t* __restrict__ x, int64_t M, int64_t K, bool packed, uint8_t* __restrict__ q, float* __restrict__ s_out,
+               int64_t first, int64_t blocks) {
+  const int64_t j = (first + blockIdx.x) * kThreads + threadIdx.x;
+  const int64_t per_row = K / 8, row = j / per_row, e = j % per_row * 8;
+  const bool in = row < M;                           // (16 lanes together: K / 8 is a multiple of 16)
+  float v[8];
+  widen8(*reinterpret_cast<const u32x4*>(x + (in ? row * K + e : 0)), v);
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+  const float s = max16(m) / 448.0f;
+  const qm::QuotientScale qs = qm::quotient_scale(s);
+  qm::apply_prefactor(v, qs);
+  const u32x2 c = e4m3_codes8(v, qs);
+  if (!in) return;
+  if ((threadIdx.x & 15) == 0) s_out[packed ? e / kScaleBlock * block_scale_stride(M) + row : row * (K / kScaleBlock) + e / kScaleBlock] = s;
+  *reinterpret_cast<u32x2*>(q + code_at(row, e, K, packed)) = c;
+}
+
+// A workgroup for each 128 x 128 block: thread t holds rows t / 16 + 16 i, columns 8 (t % 16).
+__global__ void __launch_bounds__(kThreads)
+quantize_weight_block(const uint16_t* __restrict__ w, int64_t N, int64_t K, uint8_t* __restrict__ q, float* __restrict__ s_out, int64_t first) {
+  const int64_t block = first + blockIdx.x, per_row = K / kScaleBlock;
+  const int64_t n0 = block / per_row * kScaleBlock + threadIdx.x / 16, k0 = block % per_row * kScaleBlock + threadIdx.x % 16 * 8;
+  float v[8][8], m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    widen8(*reinterpret_cast<const u32x4*>(w + min(n0 + 16 * i, N - 1) * K + k0), v[i]);    // (past N: the last row again)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[i][e]));
+  }
+  __shared__ float red[kThreads / 64];
+  m = max64(m);
+  if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = m;
+  __syncthreads();
+  const float s = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])) / 448.0f;
+  const qm::QuotientScale qs = qm::quotient_scale(s);
+  if (threadIdx.x == 0) s_out[block] = s;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    qm::apply_prefactor(v[i], qs);
+    if (n0 + 16 * i < N) *reinterpret_cast<u32x2*>(q + (n0 + 16 * i) * K + k0) = e4m3_codes8(v[i], qs);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_quantize_block(const uint16_t* x, int64_t M, int64_t K, bool packed, uint8_t* q, float* s, hipStream_t stream) {
+  const int64_t blocks = (M * (K / 8) + kThreads - 1) / kThreads;
+  return in_launches(blocks, 1, kThreads, [&](int64_t first, int64_t count) {
+    hipLaunchKernelGGL(quantize_block, dim3((unsigned)count), dim3(kThreads), 0, stream, x, M, K, packed, q, s, first, blocks);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_quantize_weight_block(const uint16_t* w, int64_t N, int64_t K, uint8_t* q, float* s, hipStream_t stream) {
+  const int64_t blocks = (N + kScaleBlock - 1) / kScaleBlock * (K / kScaleBlock);
+  return in_launches(blocks, 1, kThreads, [&](int64_t first, int64_t count) {
+    hipLaunchKernelGGL(quantize_weight_block, dim3((unsigned)count), dim3(kThreads), 0, stream, w, N, K, q, s, first);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace w8a8
