@@ -134,6 +134,8 @@ hipError_t launch_norm(const Norm&, hipStream_t) { return hipErrorUnknown; }
 hipError_t launch_rope(const Rope&, hipStream_t) { return hipErrorUnknown; }
 hipError_t launch_quantize_block(const uint16_t*, int64_t, int64_t, bool, uint8_t*, float*, hipStream_t) { return hipErrorUnknown; }
 hipError_t launch_quantize_weight_block(const uint16_t*, int64_t, int64_t, uint8_t*, float*, hipStream_t) { return hipErrorUnknown; }
+bool block_fused_fits(int64_t m, int64_t, int64_t) { return m == 1; }
+hipError_t launch_block_fused(const uint16_t*, const uint8_t*, const float*, const uint16_t*, uint16_t*, int64_t, int64_t, int64_t, hipStream_t) { return hipErrorUnknown; }
 hipError_t launch_block_gemm(const uint8_t*, const float*, const uint8_t*, const float*, const uint16_t*, uint16_t*, int64_t, int64_t, int64_t,
                              hipStream_t) { return hipErrorUnknown; }
 }

@@ -30,12 +30,13 @@ CXX = os.environ.get("CXX", "g++")
 ARCH = "gfx950"
 SOURCES = ["quantize.hip", "gemm.hip", "swiglu.hip", "short.hip", "scratch.hip", "api.cpp",
            "w4.hip", "kv_cache.hip", "attention.hip", "attention_prompt.hip", "decode_api.cpp",
-           "norm.hip", "rope.hip", "block_quant.hip", "block_gemm.hip", "layer_api.cpp"]
+           "norm.hip", "rope.hip", "block_quant.hip", "block_few.hip", "block_gemm.hip", "layer_api.cpp"]
 # Per-source flags.  The quantizer's fp64 matrix instructions (the rotation's
 # cross-quarter transform) take the VGPR form: their results feed vector
 # instructions, and results in accumulation registers would cost two copies per
 # value and, at 12,016 x 17,408, the third wave per SIMD.
-EXTRA = {"quantize.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# So do the products of the block-scaled GEMM, each of which is scaled into its sum.
+EXTRA = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for src in ("quantize.hip", "block_few.hip", "block_gemm.hip")}
 # measurement aids for the benchmark and the design tests (not the library's C ABI)
 PROBE_DIR = PKG / "probe"
 PROBE_SOURCES = ["mfma_probe.hip", "fp8_contraction.hip", "f64_mfma_layout.hip", "stream_probe.hip",

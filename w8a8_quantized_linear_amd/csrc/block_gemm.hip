@@ -1,75 +1,238 @@
-// Product of E4M3 codes with block scales, y = x W^T + b.
+// Product of E4M3 codes with block scales, y = x W^T + b, for many tokens.
 //
 // What it computes: y[m][n] = bf16(sum over blocks b of 128 columns of s[b][m] * sw[n / 128][b] * (sum over the block of
-// q[m][k] * w[n][k]) + bias[n]): the inner sums on the E4M3 matrix instructions, the outer one in fp32.
+// q[m][k] * w[n][k]) + bias[n]): the inner sums on the E4M3 matrix instructions (block_math.h), the outer one in fp32.
 //
-// The instruction (v_mfma_f32_16x16x128_f8f6f4 and its 32x32x64 form) does not sum like fp32 throughout: measured on the
-// device, products that lie 2^-13 below the largest of their group of products lose what is below that, toward zero,
-// while groups and the accumulator meet in fp32.  On normal values that is 1.4e-5 of the output's rms (4e-5 with
-// outliers twenty times as large), against 1.6e-3 that rounding the output to bf16 makes and about 4e-2 of quantizing
-// both operands; widening to bf16 instead would sum in fp32 at half the rate.  A block starts from zero, so that nothing
-// is lost against the sum so far.
+// A workgroup of WGM x WGN waves owns BM tokens x BN weight rows; a wave accumulates 16 TM tokens x 16 TN rows.  One stage is
+// one block of 128 columns of both operands, 128 bytes a row, which two LDS buffers take in turn by direct-to-LDS loads;
+// each product starts from zero and is multiplied into the sums by s * sw, four multiply-adds a lane beside 32 cycles
+// of the matrix unit.
+//
+// A stage's products run over the weight operands, each with all token operands of the wave, which stay in registers.
+// Before the last weight operand's products the wave has read all of the stage: there it waits until the next stage has
+// landed and every wave is as far (one barrier a stage), then issues the loads of the stage after it, into the
+// buffer that is free now, and replaces each token operand by the next stage's behind its last product.
+#include <type_traits>
+
+#include "block_math.h"
 #include "decode.h"
 #include "layer.h"
-#include "layer_math.h"
 
 namespace w8a8 {
 namespace {
 
 using namespace lm;
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
+constexpr int kXcds = 8, kCus = 256;
 
-// 128 columns of 16 weight rows and 16 tokens: lane l holds columns 32 (l / 16) .. + 31 of row l % 16 of both, and gets
-// token l % 16, weight rows 4 (l / 16) .. + 3.
-__device__ __forceinline__ f32x4 mfma128(i32x8 w, i32x8 x) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 127, 0, 127);
+template <int B, int E, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (B < E) {
+    f(std::integral_constant<int, B>{});
+    static_for<B + 1, E>(f);
+  }
 }
 
-// 32 bytes of a packed row: columns 128 b + 32 h ...
-__device__ __forceinline__ i32x8 operand(const uint8_t* __restrict__ p, int64_t row, int64_t b, int h, int64_t K) {
-  const uint8_t* at = p + code_at(row, 128 * b + 32 * h, K, true);
-  i32x8 v;
-  reinterpret_cast<u32x4*>(&v)[0] = *reinterpret_cast<const u32x4*>(at);
-  reinterpret_cast<u32x4*>(&v)[1] = *reinterpret_cast<const u32x4*>(at + 16);
-  return v;
+// 16 bytes a lane from a buffer straight into LDS, lane i's at l + 16 i (l uniform over the wave).
+__device__ __forceinline__ void lds_load16(Buffer p, uint32_t at, uint32_t from, uint8_t* l) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(p, (__attribute__((address_space(3))) void*)l, 16, (int)at, (int)from, 0, 0);
+#endif
 }
 
-// One wave for 16 tokens and 16 weight rows, operands straight from memory.
-__global__ void __launch_bounds__(64)
-block_gemm_simple(const uint8_t* __restrict__ q, const float* __restrict__ s, const uint8_t* __restrict__ w, const float* __restrict__ sw,
-                  const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, int64_t M, int64_t N, int64_t K, int64_t first, int64_t tiles_n) {
-  const int l = threadIdx.x, c = l % 16, h = l / 16;
-  const int64_t tile = first + blockIdx.x, m = tile / tiles_n * 16 + c, n0 = tile % tiles_n * 16;
-  const int64_t mr = min(m, M - 1), s_ld = block_scale_stride(M);
-  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t b = 0; b < K / kScaleBlock; ++b) {
-    const f32x4 part = mfma128(operand(w, min(n0 + c, N - 1), b, h, K), operand(q, mr, b, h, K));
-    const float by = s[b * s_ld + mr] * sw[n0 / kScaleBlock * (K / kScaleBlock) + b];
+// Tiles are walked in groups of kGroupM token tiles, a contiguous range of them on each XCD, so that the workgroups that
+// run at once on an XCD share panels in its L2.
+constexpr int kGroupM = 4;
+__device__ __forceinline__ void tile_of(uint32_t t, uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm, uint32_t& tn) {
+  const uint32_t per_group = kGroupM * tiles_n, group = t / per_group, first = group * kGroupM, in = t - group * per_group;
+  const uint32_t size = min((uint32_t)kGroupM, tiles_m - first);
+  tm = first + in % size;
+  tn = in / size;
+}
+
+// Rows of 128 bytes in LDS, eight pieces of 16: piece c of row r at c ^ (r & 7), so that the 16 rows that an operand's read
+// takes piece by piece spread over the banks.
+__device__ __forceinline__ int lds_piece(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+
+template <int BM, int BN, int WGM, int WGN>
+__global__ void __launch_bounds__(64 * WGM * WGN)
+block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uint8_t* __restrict__ w, const float* __restrict__ sw,
+           const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, int64_t M, int64_t N, int K, uint32_t tiles_m, uint32_t tiles_n, uint32_t first) {
+  constexpr int NT = 64 * WGM * WGN, WTM = BM / WGM, WTN = BN / WGN, TM = WTM / 16, TN = WTN / 16;
+  constexpr int A_LOADS = BM * 8 / NT, B_LOADS = BN * 8 / NT, STAGE = (BM + BN) * 128;
+  static_assert(A_LOADS * NT == BM * 8 && B_LOADS * NT == BN * 8, "whole loads");
+  static_assert(WTN <= 128 && 128 % WTN == 0, "a wave's weight rows have one scale");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, h = lane >> 4;
+  const int wm = wave % WGM, wn = wave / WGM;
+  uint32_t tile_m, tile_n;
+  tile_of(first + (uint32_t)xcd_order(blockIdx.x, gridDim.x), tiles_m, tiles_n, tile_m, tile_n);
+  tile_m = __builtin_amdgcn_readfirstlane(tile_m), tile_n = __builtin_amdgcn_readfirstlane(tile_n);
+  const int64_t mb = (int64_t)tile_m * BM, nb = (int64_t)tile_n * BN, s_ld = block_scale_stride(M);
+  const int blocks = K / kScaleBlock;
+
+  // loads: thread t of round i fills the 16 bytes at LDS place 16 (i NT + t), piece (t % 8) ^ row of row (i NT + t) / 8; rows past the
+  // last one are the last one again (their sums are not stored)
+  const Buffer abuf = buffer(q + mb * K), bbuf = buffer(w + nb * K);
+  uint32_t a_at[A_LOADS], b_at[B_LOADS];
+  auto place = [&](int64_t r, int p) -> uint32_t { return (uint32_t)(r / 32) * 32 * (uint32_t)K + (uint32_t)(r % 32) * 64 + (p >> 2) * 2048 + (p & 3) * 16; };
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(part[i], by, acc[i]);
+  for (int i = 0; i < A_LOADS; ++i) {
+    const int r = (i * NT + tid) / 8;
+    a_at[i] = place(min((int64_t)r, M - 1 - mb), (tid & 7) ^ (r & 7));
   }
-  const int64_t n = n0 + 4 * h;
-  if (m >= M || n >= N) return;
-  if (bias) {
-    float b4[4];
-    bf16x4(*reinterpret_cast<const uint2*>(bias + n), b4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] += b4[i];
+  for (int i = 0; i < B_LOADS; ++i) {
+    const int r = (i * NT + tid) / 8;
+    b_at[i] = place(min((int64_t)r, N - 1 - nb), (tid & 7) ^ (r & 7));
   }
-  *reinterpret_cast<uint2*>(y + m * N + n) = make_uint2(bf16x2_rne(acc[0], acc[1]), bf16x2_rne(acc[2], acc[3]));
+  auto issue = [&](int b) __attribute__((always_inline)) {
+    uint8_t* to = lds + (b & 1) * STAGE + wave * 1024;
+    const uint32_t from = (uint32_t)min(b, blocks - 1) * 4096;
+#pragma unroll
+    for (int i = 0; i < A_LOADS; ++i) lds_load16(abuf, a_at[i], from, to + i * NT * 16);
+#pragma unroll
+    for (int i = 0; i < B_LOADS; ++i) lds_load16(bbuf, b_at[i], from, to + BM * 128 + i * NT * 16);
+  };
+
+  // scales: this lane's token of each token operand; one of the weight
+  const Buffer sbuf = buffer(s + mb);
+  uint32_t s_at[TM];
+#pragma unroll
+  for (int j = 0; j < TM; ++j) s_at[j] = (uint32_t)min((int64_t)(wm * WTM + 16 * j + c), M - 1 - mb) * 4;
+  const float* swp = sw + min(nb + wn * WTN, N - 1) / kScaleBlock * blocks;
+
+  auto read = [&](int b, int row, int part) __attribute__((always_inline)) -> i32x8 {
+    // pieces h and 4 + h of the row: columns 16 h .. + 15 and 64 + 16 h .. + 15
+    const uint8_t* at = lds + (b & 1) * STAGE + part;
+    const u32x4 u = *reinterpret_cast<const u32x4*>(at + lds_piece(row, h)), v = *reinterpret_cast<const u32x4*>(at + lds_piece(row, 4 + h));
+    return i32x8{(int)u[0], (int)u[1], (int)u[2], (int)u[3], (int)v[0], (int)v[1], (int)v[2], (int)v[3]};
+  };
+  auto read_x = [&](int b, int j) __attribute__((always_inline)) { return read(b, wm * WTM + 16 * j + c, 0); };
+  auto read_w = [&](int b, int i) __attribute__((always_inline)) { return read(b, wn * WTN + 16 * i + c, BM * 128); };
+
+  // Product u of a stage (weight operand u / TM, token operand u % TM) is added to the sums behind product u + kLag: an instruction that
+  // reads a product's result too early waits for it.  The last kLag of a stage are added in the next.
+  constexpr int P = TM * TN, kLag = 3, kParts = 4;
+  static_assert(TN >= 2 && TM > kLag, "products in flight");
+  f32x4 acc[TN][TM], part[kParts];
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+#pragma unroll
+    for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) part[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  i32x8 xr[TM], wr[2];
+  float by[TM], raw[TM], late[kLag];
+  auto add = [&](auto u_c, float f) __attribute__((always_inline)) {
+    constexpr int u = decltype(u_c)::value;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[u / TM][u % TM][e] = __builtin_fmaf(part[u % kParts][e], f, acc[u / TM][u % TM][e]);
+  };
+
+  // this wave's loads have landed and its LDS reads are done, and so for every wave
+  auto landed = [&]() __attribute__((always_inline)) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0), lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+  };
+
+  issue(0);
+#pragma unroll
+  for (int j = 0; j < TM; ++j) by[j] = 0.0f, raw[j] = load_scale(sbuf, s_at[j], 0);
+  float sb = swp[0];
+  // (loaded here, in front of the second stage's loads: behind them, the wait for the scales would be one for that stage)
+#pragma unroll
+  for (int j = 0; j < TM; ++j) asm volatile("" : "+v"(raw[j]));
+  landed();
+  issue(1);
+#pragma unroll
+  for (int j = 0; j < TM; ++j) xr[j] = read_x(0, j);
+  wr[0] = read_w(0, 0);
+  for (int b = 0; b < blocks; ++b) {
+#pragma unroll
+    for (int j = 0; j < kLag; ++j) late[j] = by[TM - kLag + j];
+#pragma unroll
+    for (int j = 0; j < TM; ++j) by[j] = raw[j] * sb;
+    const int next = min(b + 1, blocks - 1);
+    sb = swp[next];
+#pragma unroll
+    for (int j = 0; j < TM; ++j) raw[j] = load_scale(sbuf, s_at[j], (uint32_t)(next * s_ld) * 4);
+    static_for<0, P>([&](auto u_c) __attribute__((always_inline)) {
+      constexpr int u = decltype(u_c)::value, i = u / TM, j = u % TM;
+      if constexpr (i == TN - 1 && j == 0) {
+        landed();
+        issue(b + 2);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      part[u % kParts] = mfma128(wr[i & 1], xr[j]);
+      if constexpr (u >= kLag) add(std::integral_constant<int, u - kLag>{}, by[(u - kLag) % TM]);
+      else add(std::integral_constant<int, P - kLag + u>{}, late[u]);
+      if constexpr (j == 0) wr[(i + 1) & 1] = i < TN - 1 ? read_w(b, i + 1) : read_w(b + 1, 0);
+      if constexpr (i == TN - 1) xr[j] = read_x(b + 1, j);
+    });
+  }
+  static_for<0, kLag>([&](auto u_c) __attribute__((always_inline)) {
+    constexpr int u = decltype(u_c)::value;
+    add(std::integral_constant<int, P - kLag + u>{}, by[TM - kLag + u]);
+  });
+
+  // Outputs through LDS: a product leaves 8 bytes of each of 16 rows a store, so a wave lays its rows out first, pieces of 16 bytes at c
+  // ^ row, and stores runs of whole row segments.
+  constexpr int PIECES = WTN / 8, ROWS = 64 / PIECES, REGION = WTM * WTN * 2;
+  static_assert(REGION * WGM * WGN <= 2 * STAGE, "outputs fit the stages");
+  float bias4[TN][4];
+#pragma unroll
+  for (int i = 0; i < TN; ++i) {
+    const int64_t n = min(nb + wn * WTN + 16 * i + 4 * h, N - 4);
+    if (bias) bf16x4(*reinterpret_cast<const uint2*>(bias + n), bias4[i]);
+    else bias4[i][0] = bias4[i][1] = bias4[i][2] = bias4[i][3] = 0.0f;
+  }
+  landed();   // (nothing lands in LDS behind this)
+  uint8_t* region = lds + wave * REGION;
+#pragma unroll
+  for (int j = 0; j < TM; ++j)
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      const f32x4 v = acc[i][j];
+      const uint2 o = make_uint2(bf16x2_rne(v[0] + bias4[i][0], v[1] + bias4[i][1]), bf16x2_rne(v[2] + bias4[i][2], v[3] + bias4[i][3]));
+      *reinterpret_cast<uint2*>(region + (16 * j + c) * (WTN * 2) + (((2 * i + (h >> 1)) ^ (c % PIECES)) * 16) + (h & 1) * 8) = o;
+    }
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0)
+  __builtin_amdgcn_wave_barrier();
+  const int piece = lane % PIECES;
+#pragma unroll
+  for (int r = 0; r < WTM; r += ROWS) {
+    const int row = r + lane / PIECES;
+    const int64_t m = mb + wm * WTM + row, n = nb + wn * WTN + 8 * piece;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(region + row * (WTN * 2) + ((piece ^ (row % 16 % PIECES)) * 16));
+    if (m < M && n < N) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y + m * N + n));
+  }
+}
+
+template <int BM, int BN, int WGM, int WGN>
+hipError_t launch(const uint8_t* q, const float* s, const uint8_t* w, const float* sw, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N,
+                  int64_t K, hipStream_t stream) {
+  const int64_t tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;   // (fewer than 2^27 together)
+  return in_launches(tiles_m * tiles_n, 1, 64 * WGM * WGN, [&](int64_t first, int64_t count) {
+    hipLaunchKernelGGL((block_tile<BM, BN, WGM, WGN>), dim3((unsigned)count), dim3(64 * WGM * WGN), 0, stream, q, s, w, sw, bias, y, M, N, (int)K,
+                       (uint32_t)tiles_m, (uint32_t)tiles_n, (uint32_t)first);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace
 
-hipError_t launch_block_gemm(const uint8_t* q, const float* s, const uint8_t* w, const float* sw, const uint16_t* bias, uint16_t* y,
-                             int64_t M, int64_t N, int64_t K, hipStream_t stream) {
-  const int64_t tiles_n = (N + 15) / 16;
-  return in_launches((M + 15) / 16 * tiles_n, 1, 64, [&](int64_t first, int64_t count) {
-    hipLaunchKernelGGL(block_gemm_simple, dim3((unsigned)count), dim3(64), 0, stream, q, s, w, sw, bias, y, M, N, K, first, tiles_n);
-    return hipGetLastError();
-  });
+hipError_t launch_block_gemm(const uint8_t* q, const float* s, const uint8_t* w, const float* sw, const uint16_t* bias, uint16_t* y, int64_t M,
+                             int64_t N, int64_t K, hipStream_t stream) {
+  if (M <= kFewTokens) return launch_block_few(q, s, w, sw, bias, y, M, N, K, stream);
+  auto tiles = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((N + bn - 1) / bn); };
+  if (tiles(256, 256) >= kCus) return launch<256, 256, 2, 2>(q, s, w, sw, bias, y, M, N, K, stream);
+  return launch<128, 128, 2, 2>(q, s, w, sw, bias, y, M, N, K, stream);
 }
 
 }  // namespace w8a8

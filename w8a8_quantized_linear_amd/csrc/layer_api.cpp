@@ -164,6 +164,7 @@ w8a8_status w8a8_fp8_block_linear_packed(const uint16_t* x, const uint8_t* w_pac
   if (!aligned16(x) || !aligned16(w_packed) || !aligned16(s_w) || !aligned16(bias) || !aligned16(y) || !aligned16(workspace))
     return W8A8_ERR_MISALIGNED;
   if ((st = check_device()) != W8A8_OK) return st;
+  if (w8a8::block_fused_fits(M, N, K)) return launched(w8a8::launch_block_fused(x, w_packed, s_w, bias, y, M, N, K, stream));
   uint8_t* q = static_cast<uint8_t*>(workspace);
   float* s = reinterpret_cast<float*>(q + align256((size_t)w8a8::block_scale_stride(M) * (size_t)K));
   st = launched(w8a8::launch_quantize_block(x, M, K, true, q, s, stream));
