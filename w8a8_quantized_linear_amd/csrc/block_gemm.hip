@@ -4,14 +4,16 @@
 // q[m][k] * w[n][k]) + bias[n]): the inner sums on the E4M3 matrix instructions (block_math.h), the outer one in fp32.
 //
 // A workgroup of WGM x WGN waves owns BM tokens x BN weight rows; a wave accumulates 16 TM tokens x 16 TN rows.  One stage is
-// one block of 128 columns of both operands, 128 bytes a row, which two LDS buffers take in turn by direct-to-LDS loads;
+// one block of 128 columns of both operands, 128 bytes a row, and the tokens' scales, which NST LDS buffers take in turn by direct-to-LDS
+// loads;
 // each product starts from zero and is multiplied into the sums by s * sw, four multiply-adds a lane beside 32 cycles
 // of the matrix unit.
 //
-// A stage's products run over the weight operands, each with all token operands of the wave, which stay in registers.
-// Before the last weight operand's products the wave has read all of the stage: there it waits until the next stage has
-// landed and every wave is as far (one barrier a stage), then issues the loads of the stage after it, into the
-// buffer that is free now, and replaces each token operand by the next stage's behind its last product.
+// A stage's products run over the weight operands, each with all token operands of the wave, which stay in registers;
+// weight operands are read two ahead.  Two weight operands before its end the wave has read all of the stage: there it waits until
+// the next stage has landed and every wave is as far (one barrier a stage), then issues the loads of the stage behind it into
+// the buffer that is free now, one or two beside each product (in one go, both waves of a SIMD left the matrix unit idle meanwhile), and
+// replaces each token operand by the next stage's behind its last product.
 #include <type_traits>
 
 #include "block_math.h"
@@ -23,7 +25,7 @@ namespace {
 
 using namespace lm;
 
-constexpr int kXcds = 8, kCus = 256;
+constexpr int kCus = 256;
 
 template <int B, int E, typename F>
 __device__ __forceinline__ void static_for(F&& f) {
@@ -33,11 +35,23 @@ __device__ __forceinline__ void static_for(F&& f) {
   }
 }
 
-// 16 bytes a lane from a buffer straight into LDS, lane i's at l + 16 i (l uniform over the wave).
+// 16 (4) bytes a lane from a buffer straight into LDS, lane i's at l + 16 i (4 i); l is uniform over the wave.
 __device__ __forceinline__ void lds_load16(Buffer p, uint32_t at, uint32_t from, uint8_t* l) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __builtin_amdgcn_raw_ptr_buffer_load_lds(p, (__attribute__((address_space(3))) void*)l, 16, (int)at, (int)from, 0, 0);
 #endif
+}
+__device__ __forceinline__ void lds_load4(Buffer p, uint32_t at, uint32_t from, uint8_t* l) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(p, (__attribute__((address_space(3))) void*)l, 4, (int)at, (int)from, 0, 0);
+#endif
+}
+
+// Until at most n of this wave's vector memory operations are in flight, and its LDS operations are done.
+template <int n>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(n >= 0 && n < 64, "vmcnt's range");
+  __builtin_amdgcn_s_waitcnt((n & 15) | (7 << 4) | ((n >> 4) << 14));
 }
 
 // Tiles are walked in groups of kGroupM token tiles, a contiguous range of them on each XCD, so that the workgroups that
@@ -50,19 +64,23 @@ __device__ __forceinline__ void tile_of(uint32_t t, uint32_t tiles_m, uint32_t t
   tn = in / size;
 }
 
-// Rows of 128 bytes in LDS, eight pieces of 16: piece c of row r at c ^ (r & 7), so that the 16 rows that an operand's read
-// takes piece by piece spread over the banks.
-__device__ __forceinline__ int lds_piece(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+// Rows of 128 bytes in LDS, eight pieces of 16: piece c of row r at c ^ (r / 2 % 8).  16 lanes of a read take the same piece of 16
+// consecutive rows in one cycle; even and odd rows lie in the two halves of the 64 banks, and the key spreads each half's
+// eight rows over its eight pieces (with r % 8 as the key, rows r and r + 8 meet and a read takes twice as long: 2,270 x 5,120 x
+// 34,816 378 us).
+__device__ __forceinline__ int lds_key(int r) { return (r >> 1) & 7; }
+__device__ __forceinline__ int lds_piece(int r, int c) { return r * 128 + ((c ^ lds_key(r)) << 4); }
 
-template <int BM, int BN, int WGM, int WGN>
+template <int BM, int BN, int WGM, int WGN, int NST>
 __global__ void __launch_bounds__(64 * WGM * WGN)
 block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uint8_t* __restrict__ w, const float* __restrict__ sw,
            const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, int64_t M, int64_t N, int K, uint32_t tiles_m, uint32_t tiles_n, uint32_t first) {
   constexpr int NT = 64 * WGM * WGN, WTM = BM / WGM, WTN = BN / WGN, TM = WTM / 16, TN = WTN / 16;
-  constexpr int A_LOADS = BM * 8 / NT, B_LOADS = BN * 8 / NT, STAGE = (BM + BN) * 128;
+  constexpr int A_LOADS = BM * 8 / NT, B_LOADS = BN * 8 / NT, SCALES = (BM + BN) * 128;
+  constexpr int STAGE = SCALES + BM * 4, LOADS = A_LOADS + B_LOADS + 1;
   static_assert(A_LOADS * NT == BM * 8 && B_LOADS * NT == BN * 8, "whole loads");
   static_assert(WTN <= 128 && 128 % WTN == 0, "a wave's weight rows have one scale");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NST * STAGE];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, h = lane >> 4;
   const int wm = wave % WGM, wn = wave / WGM;
   uint32_t tile_m, tile_n;
@@ -71,7 +89,7 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
   const int64_t mb = (int64_t)tile_m * BM, nb = (int64_t)tile_n * BN, s_ld = block_scale_stride(M);
   const int blocks = K / kScaleBlock;
 
-  // loads: thread t of round i fills the 16 bytes at LDS place 16 (i NT + t), piece (t % 8) ^ row of row (i NT + t) / 8; rows past the
+  // loads: thread t of round i fills the 16 bytes at LDS place 16 (i NT + t), piece (t % 8) ^ key of row (i NT + t) / 8; rows past the
   // last one are the last one again (their sums are not stored)
   const Buffer abuf = buffer(q + mb * K), bbuf = buffer(w + nb * K);
   uint32_t a_at[A_LOADS], b_at[B_LOADS];
@@ -79,42 +97,48 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
 #pragma unroll
   for (int i = 0; i < A_LOADS; ++i) {
     const int r = (i * NT + tid) / 8;
-    a_at[i] = place(min((int64_t)r, M - 1 - mb), (tid & 7) ^ (r & 7));
+    a_at[i] = place(min((int64_t)r, M - 1 - mb), (tid & 7) ^ lds_key(r));
   }
 #pragma unroll
   for (int i = 0; i < B_LOADS; ++i) {
     const int r = (i * NT + tid) / 8;
-    b_at[i] = place(min((int64_t)r, N - 1 - nb), (tid & 7) ^ (r & 7));
+    b_at[i] = place(min((int64_t)r, N - 1 - nb), (tid & 7) ^ lds_key(r));
   }
-  auto issue = [&](int b) __attribute__((always_inline)) {
-    uint8_t* to = lds + (b & 1) * STAGE + wave * 1024;
-    const uint32_t from = (uint32_t)min(b, blocks - 1) * 4096;
-#pragma unroll
-    for (int i = 0; i < A_LOADS; ++i) lds_load16(abuf, a_at[i], from, to + i * NT * 16);
-#pragma unroll
-    for (int i = 0; i < B_LOADS; ++i) lds_load16(bbuf, b_at[i], from, to + BM * 128 + i * NT * 16);
-  };
-
-  // scales: this lane's token of each token operand; one of the weight
+  // and the tokens' scales, 64 a wave (of waves beyond the tokens the same ones again: every wave issues as many loads)
   const Buffer sbuf = buffer(s + mb);
-  uint32_t s_at[TM];
-#pragma unroll
-  for (int j = 0; j < TM; ++j) s_at[j] = (uint32_t)min((int64_t)(wm * WTM + 16 * j + c), M - 1 - mb) * 4;
+  const int s_wave = wave % (BM / 64);
+  const uint32_t s_at = (uint32_t)min((int64_t)(64 * s_wave + lane), M - 1 - mb) * 4;
+  // load t of the stage of block b
+  auto issue_one = [&](auto t_c, int b, int to_stage) __attribute__((always_inline)) {
+    constexpr int t = decltype(t_c)::value;
+    uint8_t* to = lds + to_stage * STAGE;
+    const int block = min(b, blocks - 1);               // (past the last one: again, not used)
+    if constexpr (t < A_LOADS) lds_load16(abuf, a_at[t], (uint32_t)block * 4096, to + wave * 1024 + t * NT * 16);
+    else if constexpr (t < A_LOADS + B_LOADS)
+      lds_load16(bbuf, b_at[t - A_LOADS], (uint32_t)block * 4096, to + BM * 128 + wave * 1024 + (t - A_LOADS) * NT * 16);
+    else lds_load4(sbuf, s_at, (uint32_t)(block * s_ld) * 4, to + SCALES + s_wave * 256);
+  };
+  auto issue = [&](int b, int to_stage) __attribute__((always_inline)) {
+    static_for<0, LOADS>([&](auto t_c) __attribute__((always_inline)) { issue_one(t_c, b, to_stage); });
+  };
   const float* swp = sw + min(nb + wn * WTN, N - 1) / kScaleBlock * blocks;
 
-  auto read = [&](int b, int row, int part) __attribute__((always_inline)) -> i32x8 {
+  auto read = [&](int stage, int row, int part) __attribute__((always_inline)) -> i32x8 {
     // pieces h and 4 + h of the row: columns 16 h .. + 15 and 64 + 16 h .. + 15
-    const uint8_t* at = lds + (b & 1) * STAGE + part;
+    const uint8_t* at = lds + stage * STAGE + part;
     const u32x4 u = *reinterpret_cast<const u32x4*>(at + lds_piece(row, h)), v = *reinterpret_cast<const u32x4*>(at + lds_piece(row, 4 + h));
     return i32x8{(int)u[0], (int)u[1], (int)u[2], (int)u[3], (int)v[0], (int)v[1], (int)v[2], (int)v[3]};
   };
-  auto read_x = [&](int b, int j) __attribute__((always_inline)) { return read(b, wm * WTM + 16 * j + c, 0); };
-  auto read_w = [&](int b, int i) __attribute__((always_inline)) { return read(b, wn * WTN + 16 * i + c, BM * 128); };
+  auto read_x = [&](int stage, int j) __attribute__((always_inline)) { return read(stage, wm * WTM + 16 * j + c, 0); };
+  auto read_w = [&](int stage, int i) __attribute__((always_inline)) { return read(stage, wn * WTN + 16 * i + c, BM * 128); };
+  auto read_s = [&](int stage, int j) __attribute__((always_inline)) {
+    return *reinterpret_cast<const float*>(lds + stage * STAGE + SCALES + (wm * WTM + 16 * j + c) * 4);
+  };
 
   // Product u of a stage (weight operand u / TM, token operand u % TM) is added to the sums behind product u + kLag: an instruction that
   // reads a product's result too early waits for it.  The last kLag of a stage are added in the next.
-  constexpr int P = TM * TN, kLag = 3, kParts = 4;
-  static_assert(TN >= 2 && TM > kLag, "products in flight");
+  constexpr int P = TM * TN, kLag = 3, kParts = 4, kTail = 2 * TM;
+  static_assert(TN >= 4 && TN % 4 == 0 && TM > kLag, "products in flight, weight operands two ahead");
   f32x4 acc[TN][TM], part[kParts];
 #pragma unroll
   for (int i = 0; i < TN; ++i)
@@ -122,58 +146,56 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
     for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < kParts; ++i) part[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  i32x8 xr[TM], wr[2];
-  float by[TM], raw[TM], late[kLag];
+  i32x8 xr[TM], wr[4];
+  float by[TM], raw[TM];
   auto add = [&](auto u_c, float f) __attribute__((always_inline)) {
     constexpr int u = decltype(u_c)::value;
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[u / TM][u % TM][e] = __builtin_fmaf(part[u % kParts][e], f, acc[u / TM][u % TM][e]);
   };
 
-  // this wave's loads have landed and its LDS reads are done, and so for every wave
+  // the next stage has landed (the stages behind it may still be on their way) and this wave's LDS reads are done, and so for every wave
   auto landed = [&]() __attribute__((always_inline)) {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0), lgkmcnt(0)
+    wait_loads<(NST - 2) * LOADS>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
   };
 
-  issue(0);
 #pragma unroll
-  for (int j = 0; j < TM; ++j) by[j] = 0.0f, raw[j] = load_scale(sbuf, s_at[j], 0);
-  float sb = swp[0];
-  // (loaded here, in front of the second stage's loads: behind them, the wait for the scales would be one for that stage)
-#pragma unroll
-  for (int j = 0; j < TM; ++j) asm volatile("" : "+v"(raw[j]));
+  for (int b = 0; b < NST - 1; ++b) issue(b, b);
   landed();
-  issue(1);
+  issue(NST - 1, NST - 1);
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int j = 0; j < TM; ++j) xr[j] = read_x(0, j);
+  for (int j = 0; j < TM; ++j) by[j] = 0.0f, raw[j] = read_s(0, j), xr[j] = read_x(0, j);
   wr[0] = read_w(0, 0);
+  wr[1] = read_w(0, 1);
+  float sb = swp[0];
+  int now = 0;                                            // buffer of stage b
   for (int b = 0; b < blocks; ++b) {
-#pragma unroll
-    for (int j = 0; j < kLag; ++j) late[j] = by[TM - kLag + j];
-#pragma unroll
-    for (int j = 0; j < TM; ++j) by[j] = raw[j] * sb;
-    const int next = min(b + 1, blocks - 1);
-    sb = swp[next];
-#pragma unroll
-    for (int j = 0; j < TM; ++j) raw[j] = load_scale(sbuf, s_at[j], (uint32_t)(next * s_ld) * 4);
+    const int then = now + 1 == NST ? 0 : now + 1;
+    const float sb_next = swp[min(b + 1, blocks - 1)];
     static_for<0, P>([&](auto u_c) __attribute__((always_inline)) {
-      constexpr int u = decltype(u_c)::value, i = u / TM, j = u % TM;
-      if constexpr (i == TN - 1 && j == 0) {
-        landed();
-        issue(b + 2);
-      }
+      constexpr int u = decltype(u_c)::value, i = u / TM, j = u % TM, t = u - (P - kTail);
+      if constexpr (t == 0) landed();
       __builtin_amdgcn_sched_barrier(0);
-      part[u % kParts] = mfma128(wr[i & 1], xr[j]);
-      if constexpr (u >= kLag) add(std::integral_constant<int, u - kLag>{}, by[(u - kLag) % TM]);
-      else add(std::integral_constant<int, P - kLag + u>{}, late[u]);
-      if constexpr (j == 0) wr[(i + 1) & 1] = i < TN - 1 ? read_w(b, i + 1) : read_w(b + 1, 0);
-      if constexpr (i == TN - 1) xr[j] = read_x(b + 1, j);
+      part[u % kParts] = mfma128(wr[i % 4], xr[j]);
+      if constexpr (u < kLag) {
+        add(std::integral_constant<int, P - kLag + u>{}, by[TM - kLag + u]);
+      } else {
+        if constexpr (u - kLag < TM) by[u - kLag] = raw[u - kLag] * sb;
+        add(std::integral_constant<int, u - kLag>{}, by[(u - kLag) % TM]);
+      }
+      if constexpr (j == 0) wr[(i + 2) % 4] = i < TN - 2 ? read_w(now, i + 2) : read_w(then, i + 2 - TN);
+      if constexpr (i == TN - 1) xr[j] = read_x(then, j), raw[j] = read_s(then, j);
+      if constexpr (t >= 0)
+        static_for<t * LOADS / kTail, (t + 1) * LOADS / kTail>([&](auto l_c) __attribute__((always_inline)) { issue_one(l_c, b + NST, now); });
     });
+    sb = sb_next;
+    now = then;
   }
   static_for<0, kLag>([&](auto u_c) __attribute__((always_inline)) {
     constexpr int u = decltype(u_c)::value;
@@ -183,7 +205,7 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
   // Outputs through LDS: a product leaves 8 bytes of each of 16 rows a store, so a wave lays its rows out first, pieces of 16 bytes at c
   // ^ row, and stores runs of whole row segments.
   constexpr int PIECES = WTN / 8, ROWS = 64 / PIECES, REGION = WTM * WTN * 2;
-  static_assert(REGION * WGM * WGN <= 2 * STAGE, "outputs fit the stages");
+  static_assert(REGION * WGM * WGN <= NST * STAGE, "outputs fit the stages");
   float bias4[TN][4];
 #pragma unroll
   for (int i = 0; i < TN; ++i) {
@@ -191,7 +213,10 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
     if (bias) bf16x4(*reinterpret_cast<const uint2*>(bias + n), bias4[i]);
     else bias4[i][0] = bias4[i][1] = bias4[i][2] = bias4[i][3] = 0.0f;
   }
-  landed();   // (nothing lands in LDS behind this)
+  asm volatile("" ::: "memory");
+  wait_loads<0>();                                        // nothing lands in LDS behind this
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
   uint8_t* region = lds + wave * REGION;
 #pragma unroll
   for (int j = 0; j < TM; ++j)
@@ -214,12 +239,12 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
   }
 }
 
-template <int BM, int BN, int WGM, int WGN>
+template <int BM, int BN, int WGM, int WGN, int NST>
 hipError_t launch(const uint8_t* q, const float* s, const uint8_t* w, const float* sw, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N,
                   int64_t K, hipStream_t stream) {
   const int64_t tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;   // (fewer than 2^27 together)
   return in_launches(tiles_m * tiles_n, 1, 64 * WGM * WGN, [&](int64_t first, int64_t count) {
-    hipLaunchKernelGGL((block_tile<BM, BN, WGM, WGN>), dim3((unsigned)count), dim3(64 * WGM * WGN), 0, stream, q, s, w, sw, bias, y, M, N, (int)K,
+    hipLaunchKernelGGL((block_tile<BM, BN, WGM, WGN, NST>), dim3((unsigned)count), dim3(64 * WGM * WGN), 0, stream, q, s, w, sw, bias, y, M, N, (int)K,
                        (uint32_t)tiles_m, (uint32_t)tiles_n, (uint32_t)first);
     return hipGetLastError();
   });
@@ -231,8 +256,8 @@ hipError_t launch_block_gemm(const uint8_t* q, const float* s, const uint8_t* w,
                              int64_t N, int64_t K, hipStream_t stream) {
   if (M <= kFewTokens) return launch_block_few(q, s, w, sw, bias, y, M, N, K, stream);
   auto tiles = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((N + bn - 1) / bn); };
-  if (tiles(256, 256) >= kCus) return launch<256, 256, 2, 2>(q, s, w, sw, bias, y, M, N, K, stream);
-  return launch<128, 128, 2, 2>(q, s, w, sw, bias, y, M, N, K, stream);
+  if (tiles(256, 256) >= kCus) return launch<256, 256, 4, 2, 2>(q, s, w, sw, bias, y, M, N, K, stream);
+  return launch<128, 128, 1, 2, 2>(q, s, w, sw, bias, y, M, N, K, stream);
 }
 
 }  // namespace w8a8
