@@ -14,6 +14,7 @@
 // the next stage has landed and every wave is as far (one barrier a stage), then issues the loads of the stage behind it into
 // the buffer that is free now, one or two beside each product (in one go, both waves of a SIMD left the matrix unit idle meanwhile), and
 // replaces each token operand by the next stage's behind its last product.
+#include <algorithm>
 #include <type_traits>
 
 #include "block_math.h"
@@ -26,6 +27,13 @@ namespace {
 using namespace lm;
 
 constexpr int kCus = 256;
+
+// A read-only value at an address that is uniform over the wave, by a scalar load: it is not counted with the loads of the stages.
+__device__ __forceinline__ float uniform_load(const float* p) {
+  const uint64_t u = reinterpret_cast<uint64_t>(p);
+  const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(u >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)u);
+  return *reinterpret_cast<const __attribute__((address_space(4))) float*>(at);
+}
 
 template <int B, int E, typename F>
 __device__ __forceinline__ void static_for(F&& f) {
@@ -71,62 +79,84 @@ __device__ __forceinline__ void tile_of(uint32_t t, uint32_t tiles_m, uint32_t t
 __device__ __forceinline__ int lds_key(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ int lds_piece(int r, int c) { return r * 128 + ((c ^ lds_key(r)) << 4); }
 
-template <int BM, int BN, int WGM, int WGN, int NST>
+// WALK: a workgroup for each CU, which walks over tiles of its XCD's range; the stages run on from one tile into the next, whose first
+// ones load while this tile's outputs leave.  Otherwise a workgroup for each tile.
+template <int BM, int BN, int WGM, int WGN, int NST, bool WALK>
 __global__ void __launch_bounds__(64 * WGM * WGN)
 block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uint8_t* __restrict__ w, const float* __restrict__ sw,
            const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, int64_t M, int64_t N, int K, uint32_t tiles_m, uint32_t tiles_n, uint32_t first) {
   constexpr int NT = 64 * WGM * WGN, WTM = BM / WGM, WTN = BN / WGN, TM = WTM / 16, TN = WTN / 16;
   constexpr int A_LOADS = BM * 8 / NT, B_LOADS = BN * 8 / NT, SCALES = (BM + BN) * 128;
-  constexpr int STAGE = SCALES + BM * 4, LOADS = A_LOADS + B_LOADS + 1;
+  constexpr int STAGE = SCALES + BM * 4, LOADS = A_LOADS + B_LOADS + 1, AREA = WALK ? 2048 : 0, BIAS = WALK ? BN * 2 : 0;
   static_assert(A_LOADS * NT == BM * 8 && B_LOADS * NT == BN * 8, "whole loads");
   static_assert(WTN <= 128 && 128 % WTN == 0, "a wave's weight rows have one scale");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[NST * STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NST * STAGE + WGM * WGN * AREA + 2 * BIAS];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, h = lane >> 4;
   const int wm = wave % WGM, wn = wave / WGM;
-  uint32_t tile_m, tile_n;
-  tile_of(first + (uint32_t)xcd_order(blockIdx.x, gridDim.x), tiles_m, tiles_n, tile_m, tile_n);
-  tile_m = __builtin_amdgcn_readfirstlane(tile_m), tile_n = __builtin_amdgcn_readfirstlane(tile_n);
-  const int64_t mb = (int64_t)tile_m * BM, nb = (int64_t)tile_n * BN, s_ld = block_scale_stride(M);
+  const int64_t s_ld = block_scale_stride(M);
   const int blocks = K / kScaleBlock;
 
-  // loads: thread t of round i fills the 16 bytes at LDS place 16 (i NT + t), piece (t % 8) ^ key of row (i NT + t) / 8; rows past the
-  // last one are the last one again (their sums are not stored)
-  const Buffer abuf = buffer(q + mb * K), bbuf = buffer(w + nb * K);
-  uint32_t a_at[A_LOADS], b_at[B_LOADS];
-  auto place = [&](int64_t r, int p) -> uint32_t { return (uint32_t)(r / 32) * 32 * (uint32_t)K + (uint32_t)(r % 32) * 64 + (p >> 2) * 2048 + (p & 3) * 16; };
-#pragma unroll
-  for (int i = 0; i < A_LOADS; ++i) {
-    const int r = (i * NT + tid) / 8;
-    a_at[i] = place(min((int64_t)r, M - 1 - mb), (tid & 7) ^ lds_key(r));
+  // this workgroup's tiles: `at`, at + step, ... below `end`
+  uint32_t at, end, step = 1;
+  if constexpr (WALK) {
+    const uint32_t tiles = tiles_m * tiles_n, q8 = tiles / 8, r8 = tiles % 8, xcd = blockIdx.x % 8, begin = xcd * q8 + min(xcd, r8);
+    at = begin + blockIdx.x / 8, end = begin + q8 + (xcd < r8 ? 1 : 0), step = gridDim.x / 8;
+    if (at >= end) return;
+  } else {
+    at = first + (uint32_t)xcd_order(blockIdx.x, gridDim.x), end = at + 1;
   }
+  // Loads of a tile: thread t of round i fills the 16 bytes at LDS place 16 (i NT + t), piece (t % 8) ^ key of row (i NT + t) / 8; rows
+  // past the last one are the last one again (their sums are not stored).  And the tokens' scales, 64 a wave (of waves beyond
+  // the tokens the same ones again: every wave issues as many loads).
+  Buffer abuf, bbuf, sbuf;
+  uint32_t a_at[A_LOADS], b_at[B_LOADS], s_at;
+  int64_t load_m, load_n;                                 // its first token and weight row
+  const float* load_sw;                                   // the scales of its weight rows of this wave, by block of columns
+  int aimed = 0;                                          // tiles aimed at
+  const int s_wave = wave % (BM / 64), bias_wave = wave % (BN / 128);
+  auto place = [&](uint32_t r, int p) -> uint32_t { return r / 32 * 32 * (uint32_t)K + r % 32 * 64 + (p >> 2) * 2048 + (p & 3) * 16; };
+  auto aim = [&](uint32_t t) __attribute__((always_inline)) {
+    uint32_t tm, tn;
+    tile_of(t, tiles_m, tiles_n, tm, tn);
+    load_m = (int64_t)__builtin_amdgcn_readfirstlane(tm) * BM, load_n = (int64_t)__builtin_amdgcn_readfirstlane(tn) * BN;
+    abuf = buffer(q + load_m * K), bbuf = buffer(w + load_n * K), sbuf = buffer(s + load_m);
+    load_sw = sw + min(load_n + wn * WTN, N - 1) / kScaleBlock * blocks;
+    const uint32_t m_last = (uint32_t)min(M - 1 - load_m, (int64_t)BM), n_last = (uint32_t)min(N - 1 - load_n, (int64_t)BN);
+    int id = tid;
+    if constexpr (WALK) asm volatile("" : "+v"(id));      // (what follows from it is computed again, not kept in registers)
 #pragma unroll
-  for (int i = 0; i < B_LOADS; ++i) {
-    const int r = (i * NT + tid) / 8;
-    b_at[i] = place(min((int64_t)r, N - 1 - nb), (tid & 7) ^ lds_key(r));
-  }
-  // and the tokens' scales, 64 a wave (of waves beyond the tokens the same ones again: every wave issues as many loads)
-  const Buffer sbuf = buffer(s + mb);
-  const int s_wave = wave % (BM / 64);
-  const uint32_t s_at = (uint32_t)min((int64_t)(64 * s_wave + lane), M - 1 - mb) * 4;
-  // load t of the stage of block b
-  auto issue_one = [&](auto t_c, int b, int to_stage) __attribute__((always_inline)) {
+    for (int i = 0; i < A_LOADS; ++i) {
+      const uint32_t r = (i * NT + id) / 8;
+      a_at[i] = place(min(r, m_last), (id & 7) ^ lds_key(r));
+    }
+#pragma unroll
+    for (int i = 0; i < B_LOADS; ++i) {
+      const uint32_t r = (i * NT + id) / 8;
+      b_at[i] = place(min(r, n_last), (id & 7) ^ lds_key(r));
+    }
+    const int lane = id & 63;
+    s_at = min((uint32_t)(64 * s_wave + lane), m_last) * 4;
+    // walking, the tile's bias goes to LDS too (two places in turn; pairs of columns, those past N the last pair)
+    if (WALK && bias)
+      lds_load4(buffer(bias + load_n), min((uint32_t)(128 * bias_wave + 2 * lane), n_last - 1) * 2, 0,
+                lds + NST * STAGE + WGM * WGN * AREA + (aimed & 1) * BIAS + bias_wave * 256);
+    ++aimed;
+  };
+  uint32_t load_at = at;
+  int load_b = 0;                                         // the block to load, of tile load_at
+  auto issue_one = [&](auto t_c, int to_stage) __attribute__((always_inline)) {   // load t of that stage
     constexpr int t = decltype(t_c)::value;
     uint8_t* to = lds + to_stage * STAGE;
-    const int block = min(b, blocks - 1);               // (past the last one: again, not used)
-    if constexpr (t < A_LOADS) lds_load16(abuf, a_at[t], (uint32_t)block * 4096, to + wave * 1024 + t * NT * 16);
+    if constexpr (t < A_LOADS) lds_load16(abuf, a_at[t], (uint32_t)load_b * 4096, to + wave * 1024 + t * NT * 16);
     else if constexpr (t < A_LOADS + B_LOADS)
-      lds_load16(bbuf, b_at[t - A_LOADS], (uint32_t)block * 4096, to + BM * 128 + wave * 1024 + (t - A_LOADS) * NT * 16);
-    else lds_load4(sbuf, s_at, (uint32_t)(block * s_ld) * 4, to + SCALES + s_wave * 256);
+      lds_load16(bbuf, b_at[t - A_LOADS], (uint32_t)load_b * 4096, to + BM * 128 + wave * 1024 + (t - A_LOADS) * NT * 16);
+    else lds_load4(sbuf, s_at, (uint32_t)(load_b * s_ld) * 4, to + SCALES + s_wave * 256);
   };
-  auto issue = [&](int b, int to_stage) __attribute__((always_inline)) {
-    static_for<0, LOADS>([&](auto t_c) __attribute__((always_inline)) { issue_one(t_c, b, to_stage); });
-  };
-  const float* swp = sw + min(nb + wn * WTN, N - 1) / kScaleBlock * blocks;
 
   auto read = [&](int stage, int row, int part) __attribute__((always_inline)) -> i32x8 {
     // pieces h and 4 + h of the row: columns 16 h .. + 15 and 64 + 16 h .. + 15
-    const uint8_t* at = lds + stage * STAGE + part;
-    const u32x4 u = *reinterpret_cast<const u32x4*>(at + lds_piece(row, h)), v = *reinterpret_cast<const u32x4*>(at + lds_piece(row, 4 + h));
+    const uint8_t* p = lds + stage * STAGE + part;
+    const u32x4 u = *reinterpret_cast<const u32x4*>(p + lds_piece(row, h)), v = *reinterpret_cast<const u32x4*>(p + lds_piece(row, 4 + h));
     return i32x8{(int)u[0], (int)u[1], (int)u[2], (int)u[3], (int)v[0], (int)v[1], (int)v[2], (int)v[3]};
   };
   auto read_x = [&](int stage, int j) __attribute__((always_inline)) { return read(stage, wm * WTM + 16 * j + c, 0); };
@@ -134,27 +164,31 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
   auto read_s = [&](int stage, int j) __attribute__((always_inline)) {
     return *reinterpret_cast<const float*>(lds + stage * STAGE + SCALES + (wm * WTM + 16 * j + c) * 4);
   };
-
   // Product u of a stage (weight operand u / TM, token operand u % TM) is added to the sums behind product u + kLag: an instruction that
   // reads a product's result too early waits for it.  The last kLag of a stage are added in the next.
   constexpr int P = TM * TN, kLag = 3, kParts = 4, kTail = 2 * TM;
   static_assert(TN >= 4 && TN % 4 == 0 && TM > kLag, "products in flight, weight operands two ahead");
   f32x4 acc[TN][TM], part[kParts];
-#pragma unroll
-  for (int i = 0; i < TN; ++i)
-#pragma unroll
-    for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < kParts; ++i) part[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   i32x8 xr[TM], wr[4];
   float by[TM], raw[TM];
+  auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) part[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < TM; ++j) by[j] = 0.0f;
+  };
   auto add = [&](auto u_c, float f) __attribute__((always_inline)) {
     constexpr int u = decltype(u_c)::value;
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[u / TM][u % TM][e] = __builtin_fmaf(part[u % kParts][e], f, acc[u / TM][u % TM][e]);
   };
 
-  // the next stage has landed (the stages behind it may still be on their way) and this wave's LDS reads are done, and so for every wave
+  // The next stage has landed (the stages behind it may still be on their way) and this wave's LDS reads are done, and so for every
+  // wave.
   auto landed = [&]() __attribute__((always_inline)) {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
@@ -164,90 +198,169 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
     asm volatile("" ::: "memory");
   };
 
+  // Outputs: a product leaves 8 bytes of each of 16 rows a store, so a wave lays rows out in LDS first, pieces of 16 bytes at c ^ row, and
+  // stores runs of whole row segments.  Walking, in 16 rows x 64 columns of an area of its own; otherwise all at once in the stages' place.
+  auto outputs = [&](int64_t mb, int64_t nb, int tile) __attribute__((always_inline)) {
+    const uint32_t m_left = (uint32_t)min(M - mb, (int64_t)BM), n_left = (uint32_t)min(N - nb, (int64_t)BN);
+    float bias4[WALK ? 1 : TN][4];
+    if constexpr (!WALK) {
+      const int h = lane >> 4;
 #pragma unroll
-  for (int b = 0; b < NST - 1; ++b) issue(b, b);
-  landed();
-  issue(NST - 1, NST - 1);
+      for (int i = 0; i < TN; ++i) {
+        if (bias) bf16x4(*reinterpret_cast<const uint2*>(bias + min(nb + wn * WTN + 16 * i + 4 * h, N - 4)), bias4[i]);
+        else bias4[i][0] = bias4[i][1] = bias4[i][2] = bias4[i][3] = 0.0f;
+      }
+    }
+    int lane_ = lane;
+    if constexpr (WALK) asm volatile("" : "+v"(lane_));   // (as above)
+    const int lane = lane_, c = lane & 15, h = lane >> 4;
+    const uint8_t* biases = lds + NST * STAGE + WGM * WGN * AREA + (tile & 1) * BIAS;
+    auto lay = [&](uint8_t* to, auto i_c, auto j_c, int pieces) __attribute__((always_inline)) {   // block (i, j) at column 16 i of its row
+      constexpr int i = decltype(i_c)::value, j = decltype(j_c)::value;
+      float b4[4];
+      if constexpr (WALK) {
+        bf16x4(*reinterpret_cast<const uint2*>(biases + (wn * WTN + 16 * i + 4 * h) * 2), b4);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b4[e] = bias4[i][e];
+      }
+      const f32x4 v = acc[i][j];
+      const uint2 o = make_uint2(bf16x2_rne(v[0] + b4[0], v[1] + b4[1]), bf16x2_rne(v[2] + b4[2], v[3] + b4[3]));
+      *reinterpret_cast<uint2*>(to + c * pieces * 16 + (((2 * i + (h >> 1)) ^ c) % pieces) * 16 + (h & 1) * 8) = o;
+    };
+    auto laid = [&]() __attribute__((always_inline)) {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0)
+      __builtin_amdgcn_wave_barrier();
+    };
+    if constexpr (WALK) {
+      static_assert(!WALK || WTN % 64 == 0, "64 columns at a time");
+      uint8_t* area = lds + NST * STAGE + wave * AREA;
+      // (an output of 256 rows lies within 2^31 bytes of its first)
+      const Buffer ybuf = __builtin_amdgcn_make_buffer_rsrc(y + mb * N + nb, 0, 0x7fffffff, 0x00020000);
+      static_for<0, TM>([&](auto j_c) __attribute__((always_inline)) {
+        static_for<0, WTN / 64>([&](auto half) __attribute__((always_inline)) {
+          static_for<0, 4>([&](auto i_c) __attribute__((always_inline)) {
+            lay(area, std::integral_constant<int, 4 * decltype(half)::value + decltype(i_c)::value>{}, j_c, 8);
+          });
+          laid();
+#pragma unroll
+          for (int r = 0; r < 16; r += 8) {
+            const int row = r + lane / 8, piece = lane % 8;
+            const u32x4 v = *reinterpret_cast<const u32x4*>(area + row * 128 + ((piece ^ row) % 8) * 16);
+            const uint32_t m = wm * WTM + 16 * decltype(j_c)::value + row, n = wn * WTN + 64 * decltype(half)::value + 8 * piece;
+            const uint32_t off = m < m_left && n < n_left ? (m * (uint32_t)N + n) * 2 : 0x80000000u;
+            __builtin_amdgcn_raw_buffer_store_b128(v, ybuf, (int)off, 0, 2);
+          }
+          laid();
+        });
+      });
+    } else {
+      constexpr int PIECES = WTN / 8, ROWS = 64 / PIECES, REGION = WTM * WTN * 2;
+      static_assert(REGION * WGM * WGN <= NST * STAGE, "outputs fit the stages");
+      asm volatile("" ::: "memory");
+      wait_loads<0>();                                      // nothing lands in LDS behind this
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      uint8_t* region = lds + wave * REGION;
+      static_for<0, TM>([&](auto j_c) __attribute__((always_inline)) {
+        static_for<0, TN>([&](auto i_c) __attribute__((always_inline)) { lay(region + 16 * decltype(j_c)::value * WTN * 2, i_c, j_c, PIECES); });
+      });
+      laid();
+      const int piece = lane % PIECES;
+#pragma unroll
+      for (int r = 0; r < WTM; r += ROWS) {
+        const int row = r + lane / PIECES;
+        const uint32_t m = wm * WTM + row, n = wn * WTN + 8 * piece;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(region + row * (WTN * 2) + ((piece ^ (row % 16)) % PIECES) * 16);
+        if (m < m_left && n < n_left) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y + (mb + m) * N + nb + n));
+      }
+    }
+  };
+
+  if (WALK && !bias) {                                     // (seen by all behind the first stage's barrier)
+    for (int i = tid; i < 2 * BIAS / 4; i += NT) *reinterpret_cast<uint32_t*>(lds + NST * STAGE + WGM * WGN * AREA + 4 * i) = 0;
+  }
+  aim(load_at);
+  int64_t mb = load_m, nb = load_n;                       // the tile that is multiplied
+  const float* swp = load_sw;
+#pragma unroll
+  for (int b = 0; b < NST; ++b) {
+    static_for<0, LOADS>([&](auto t_c) __attribute__((always_inline)) { issue_one(t_c, b); });
+    load_b = min(b + 1, blocks - 1);                      // (past the last block: that one again, not used)
+    if (b == NST - 2) landed();
+  }
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int j = 0; j < TM; ++j) by[j] = 0.0f, raw[j] = read_s(0, j), xr[j] = read_x(0, j);
+  for (int j = 0; j < TM; ++j) raw[j] = read_s(0, j), xr[j] = read_x(0, j);
   wr[0] = read_w(0, 0);
   wr[1] = read_w(0, 1);
-  float sb = swp[0];
-  int now = 0;                                            // buffer of stage b
-  for (int b = 0; b < blocks; ++b) {
-    const int then = now + 1 == NST ? 0 : now + 1;
-    const float sb_next = swp[min(b + 1, blocks - 1)];
-    static_for<0, P>([&](auto u_c) __attribute__((always_inline)) {
-      constexpr int u = decltype(u_c)::value, i = u / TM, j = u % TM, t = u - (P - kTail);
-      if constexpr (t == 0) landed();
-      __builtin_amdgcn_sched_barrier(0);
-      part[u % kParts] = mfma128(wr[i % 4], xr[j]);
-      if constexpr (u < kLag) {
-        add(std::integral_constant<int, P - kLag + u>{}, by[TM - kLag + u]);
-      } else {
-        if constexpr (u - kLag < TM) by[u - kLag] = raw[u - kLag] * sb;
-        add(std::integral_constant<int, u - kLag>{}, by[(u - kLag) % TM]);
-      }
-      if constexpr (j == 0) wr[(i + 2) % 4] = i < TN - 2 ? read_w(now, i + 2) : read_w(then, i + 2 - TN);
-      if constexpr (i == TN - 1) xr[j] = read_x(then, j), raw[j] = read_s(then, j);
-      if constexpr (t >= 0)
-        static_for<t * LOADS / kTail, (t + 1) * LOADS / kTail>([&](auto l_c) __attribute__((always_inline)) { issue_one(l_c, b + NST, now); });
-    });
-    sb = sb_next;
-    now = then;
-  }
-  static_for<0, kLag>([&](auto u_c) __attribute__((always_inline)) {
-    constexpr int u = decltype(u_c)::value;
-    add(std::integral_constant<int, P - kLag + u>{}, by[TM - kLag + u]);
-  });
-
-  // Outputs through LDS: a product leaves 8 bytes of each of 16 rows a store, so a wave lays its rows out first, pieces of 16 bytes at c
-  // ^ row, and stores runs of whole row segments.
-  constexpr int PIECES = WTN / 8, ROWS = 64 / PIECES, REGION = WTM * WTN * 2;
-  static_assert(REGION * WGM * WGN <= NST * STAGE, "outputs fit the stages");
-  float bias4[TN][4];
-#pragma unroll
-  for (int i = 0; i < TN; ++i) {
-    const int64_t n = min(nb + wn * WTN + 16 * i + 4 * h, N - 4);
-    if (bias) bf16x4(*reinterpret_cast<const uint2*>(bias + n), bias4[i]);
-    else bias4[i][0] = bias4[i][1] = bias4[i][2] = bias4[i][3] = 0.0f;
-  }
-  asm volatile("" ::: "memory");
-  wait_loads<0>();                                        // nothing lands in LDS behind this
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  uint8_t* region = lds + wave * REGION;
-#pragma unroll
-  for (int j = 0; j < TM; ++j)
-#pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      const f32x4 v = acc[i][j];
-      const uint2 o = make_uint2(bf16x2_rne(v[0] + bias4[i][0], v[1] + bias4[i][1]), bf16x2_rne(v[2] + bias4[i][2], v[3] + bias4[i][3]));
-      *reinterpret_cast<uint2*>(region + (16 * j + c) * (WTN * 2) + (((2 * i + (h >> 1)) ^ (c % PIECES)) * 16) + (h & 1) * 8) = o;
+  float sb = uniform_load(swp);
+  int now = 0;                                            // buffer of the stage that is multiplied
+  clear();
+  for (int tile = 0;; ++tile) {
+    // the loads are NST blocks ahead: of this tile, then of the next, or its last block again where there is none
+    int b = 0, load_step = 1;
+#pragma clang loop unroll(disable)
+    for (int part_of = 0; part_of < 2; ++part_of) {
+    const int stop = part_of == 0 ? blocks - NST : blocks;
+    if (part_of == 1) {
+      if (WALK && load_at + step < end) load_at += step, load_b = 0, aim(load_at);
+      else load_b = blocks - 1, load_step = 0;
     }
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0)
-  __builtin_amdgcn_wave_barrier();
-  const int piece = lane % PIECES;
-#pragma unroll
-  for (int r = 0; r < WTM; r += ROWS) {
-    const int row = r + lane / PIECES;
-    const int64_t m = mb + wm * WTM + row, n = nb + wn * WTN + 8 * piece;
-    const u32x4 v = *reinterpret_cast<const u32x4*>(region + row * (WTN * 2) + ((piece ^ (row % 16 % PIECES)) * 16));
-    if (m < M && n < N) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y + m * N + n));
+#pragma clang loop unroll(disable)
+    for (; b < stop; ++b) {
+      const int then = now + 1 == NST ? 0 : now + 1;
+      const float sb_next = uniform_load(swp + min(b + 1, blocks - 1));
+      static_for<0, P>([&](auto u_c) __attribute__((always_inline)) {
+        constexpr int u = decltype(u_c)::value, i = u / TM, j = u % TM, t = u - (P - kTail);
+        if constexpr (t == 0) {
+          landed();
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        part[u % kParts] = mfma128(wr[i % 4], xr[j]);
+        if constexpr (u < kLag) {
+          add(std::integral_constant<int, P - kLag + u>{}, by[TM - kLag + u]);
+        } else {
+          if constexpr (u - kLag < TM) by[u - kLag] = raw[u - kLag] * sb;
+          add(std::integral_constant<int, u - kLag>{}, by[(u - kLag) % TM]);
+        }
+        if constexpr (j == 0) wr[(i + 2) % 4] = i < TN - 2 ? read_w(now, i + 2) : read_w(then, i + 2 - TN);
+        if constexpr (i == TN - 1) xr[j] = read_x(then, j), raw[j] = read_s(then, j);
+        if constexpr (t >= 0)
+          static_for<t * LOADS / kTail, (t + 1) * LOADS / kTail>([&](auto l_c) __attribute__((always_inline)) { issue_one(l_c, now); });
+      });
+      load_b += load_step;
+      sb = sb_next;
+      now = then;
+    }
+    }
+    static_for<0, kLag>([&](auto u_c) __attribute__((always_inline)) {
+      constexpr int u = decltype(u_c)::value;
+      add(std::integral_constant<int, P - kLag + u>{}, by[TM - kLag + u]);
+    });
+    outputs(mb, nb, tile);
+    if constexpr (!WALK) break;
+    at += step;
+    if (at >= end) break;
+    mb = load_m, nb = load_n, swp = load_sw;
+    sb = uniform_load(swp);
+    clear();
   }
+  wait_loads<0>();                                        // nothing lands in LDS behind the workgroup's end
 }
 
-template <int BM, int BN, int WGM, int WGN, int NST>
+template <int BM, int BN, int WGM, int WGN, int NST, bool WALK>
 hipError_t launch(const uint8_t* q, const float* s, const uint8_t* w, const float* sw, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N,
                   int64_t K, hipStream_t stream) {
   const int64_t tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;   // (fewer than 2^27 together)
-  return in_launches(tiles_m * tiles_n, 1, 64 * WGM * WGN, [&](int64_t first, int64_t count) {
-    hipLaunchKernelGGL((block_tile<BM, BN, WGM, WGN, NST>), dim3((unsigned)count), dim3(64 * WGM * WGN), 0, stream, q, s, w, sw, bias, y, M, N, (int)K,
-                       (uint32_t)tiles_m, (uint32_t)tiles_n, (uint32_t)first);
+  auto run = [&](int64_t first, int64_t count) {
+    hipLaunchKernelGGL((block_tile<BM, BN, WGM, WGN, NST, WALK>), dim3((unsigned)count), dim3(64 * WGM * WGN), 0, stream, q, s, w, sw, bias, y, M,
+                       N, (int)K, (uint32_t)tiles_m, (uint32_t)tiles_n, (uint32_t)first);
     return hipGetLastError();
-  });
+  };
+  if (WALK) return run(0, std::min<int64_t>((tiles_m * tiles_n + 7) / 8, kCus / 8) * 8);
+  return in_launches(tiles_m * tiles_n, 1, 64 * WGM * WGN, run);
 }
 
 }  // namespace
@@ -256,8 +369,8 @@ hipError_t launch_block_gemm(const uint8_t* q, const float* s, const uint8_t* w,
                              int64_t N, int64_t K, hipStream_t stream) {
   if (M <= kFewTokens) return launch_block_few(q, s, w, sw, bias, y, M, N, K, stream);
   auto tiles = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((N + bn - 1) / bn); };
-  if (tiles(256, 256) >= kCus) return launch<256, 256, 4, 2, 2>(q, s, w, sw, bias, y, M, N, K, stream);
-  return launch<128, 128, 1, 2, 2>(q, s, w, sw, bias, y, M, N, K, stream);
+  if (tiles(256, 256) >= kCus) return launch<256, 256, 4, 2, 2, true>(q, s, w, sw, bias, y, M, N, K, stream);
+  return launch<128, 256, 2, 4, 3, false>(q, s, w, sw, bias, y, M, N, K, stream);
 }
 
 }  // namespace w8a8
