@@ -479,13 +479,15 @@ w8a8_status w8a8_quantize_weight_block(const uint16_t* w, int64_t N, int64_t K, 
  * the E4M3 matrix instructions, which drop what lies 2^-13 below the largest of a group of their products (1.4e-5 of
  * the output's rms on normal values, 4e-5 with outliers of 20 times); the sum over blocks is fp32, rounded once.
  * Which form multiplies, and with it the order of the sum over blocks, depends on M, N and K.
- * M * N <= 2^40, N <= 2^28 - 32, M <= 2^30; a token that is not finite spoils its own row only. */
+ * M * N <= 2^40, N <= 2^28 - 32, M <= 2^30; a token that is not finite spoils its own row only.  The workspace holds fp32
+ * partial sums where the shape is short of tiles, so that K is cut; its size is 0, and workspace may be NULL, where it is not. */
+size_t w8a8_fp8_block_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);   /* 0 also outside the limits */
 w8a8_status w8a8_fp8_block_gemm_packed(const uint8_t* q_packed, const float* s, const uint8_t* w_packed, const float* s_w,
-                                       const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K,
-                                       hipStream_t stream);
+                                       const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K, void* workspace,
+                                       size_t workspace_bytes, hipStream_t stream);
 
-/* x is quantized into the workspace, then multiplied.  The workspace holds the packed codes and their scales. */
-size_t w8a8_fp8_block_workspace_bytes(int64_t M, int64_t K);   /* 0 for M <= 0 or K <= 0 */
+/* x is quantized into the workspace (packed codes and scales; a short call may leave it unused), then multiplied. */
+size_t w8a8_fp8_block_workspace_bytes(int64_t M, int64_t N, int64_t K);        /* 0 for M <= 0 and outside the limits */
 w8a8_status w8a8_fp8_block_linear_packed(const uint16_t* x, const uint8_t* w_packed, const float* s_w, const uint16_t* bias,
                                          uint16_t* y, int64_t M, int64_t N, int64_t K, void* workspace,
                                          size_t workspace_bytes, hipStream_t stream);

@@ -47,12 +47,43 @@ def weight_codes(w):
     return q, s
 
 
-def check(y, q, s, w, sw, bias, what=""):
-    want, dropped, spread = plain.block_product(q, s, w, sw, bias)
+def check(y, q, s, w, sw, bias, what="", rows=None, cols=None):
+    """Against 64 bits; `rows` and `cols`: these of y only."""
+    if rows is not None:
+        y, q, s = y[rows], q[rows], s[rows]
+    if cols is not None:
+        assert (np.diff(cols) > 0).all()
+        block = cols // 128
+        want, dropped, spread = (np.zeros((q.shape[0], len(cols))) for _ in range(3))
+        for b in np.unique(block):
+            at = block == b
+            want[:, at], dropped[:, at], spread[:, at] = plain.block_product(q, s, w[cols[at]], sw[b:b + 1], None if bias is None else bias[cols[at]])
+        y = y[:, cols]
+    else:
+        want, dropped, spread = plain.block_product(q, s, w, sw, bias)
     blocks = q.shape[1] // 128
     off = np.abs(plain.f64(y) - want)
     by = dropped + spread * (2.0 ** -20 + (blocks + 3) * 2.0 ** -24) + (np.abs(want) + dropped) * 2.0 ** -8 + 2.0 ** -134
     assert np.isfinite(plain.f64(y)).all() and (off <= by).all(), f"{what}: off by {np.max(off / by)} of what it may be"
+
+
+def near(y, x, w, bias):
+    """Every output, loosely: against fp32 products of the values."""
+    (q, s), (wq, sw) = x, w
+    (M, K), N = q.shape, wq.shape[0]
+    v = (q.view(torch.float8_e4m3fn).float().view(M, -1, 128) * s[:, :, None]).view(M, K)
+    ref = v @ (wq.view(torch.float8_e4m3fn).float().view(N, -1, 128) * sw.repeat_interleave(128, 0)[:N, :, None]).view(N, K).t()
+    if bias is not None:
+        ref = ref + bias.float()
+    rms = ref.square().mean(1, keepdim=True).sqrt()          # a token's own: tokens differ by powers of two
+    assert ((y.float() - ref).abs() <= ref.abs() * 2.0 ** -7 + rms * 2.0 ** -7).all()
+
+
+def some(n, seed):
+    """Some of n places: both ends, around every border of a tile, others."""
+    rng = np.random.default_rng(seed)
+    at = {0, n - 1, n // 2} | {b + d for b in (16, 32, 64, 128, 256, n // 64 * 64, n // 128 * 128, n // 256 * 256) for d in (-1, 0)} | set(rng.integers(0, n, 12).tolist())
+    return np.array(sorted(i for i in at if 0 <= i < n))
 
 
 @pytest.mark.parametrize("M,K", ((1, 128), (3, 256), (37, 1024), (300, 640), (2, 131072)))
@@ -81,7 +112,10 @@ def test_quantize_weights(lib, N, K):
     assert np.array_equal(lib.w8a8_pack_weight(gq).cpu().numpy(), plain.pack(q))
 
 
-SHAPES = ((1, 8, 128), (1, 64, 256), (2, 136, 1024), (5, 24, 2176), (16, 256, 512), (17, 200, 384), (31, 128, 640), (33, 392, 256),
+# every form: few tokens (16 and 32 weight rows a workgroup; 1, 2 and 4 blocks of tokens; fused), tiles of each size, parts of K, workgroups
+# that walk over tiles; ragged last tiles, and blocks of columns fewer than the stages
+SHAPES = ((7, 4360, 2048), (16, 8, 4096), (20, 4360, 256), (40, 4360, 384), (64, 40, 8192), (70, 8, 128), (66, 72, 4096), (100, 264, 5120), (130, 1032, 17408),
+          (17, 8200, 6272), (70, 34824, 128), (129, 34824, 384), (300, 1032, 4096), (258, 5128, 2048), (520, 4104, 640), (1030, 8200, 256), (1, 8, 128), (1, 64, 256), (2, 136, 1024), (5, 24, 2176), (16, 256, 512), (17, 200, 384), (31, 128, 640), (33, 392, 256),
           (48, 264, 128), (64, 128, 1024), (65, 136, 512), (100, 520, 256), (129, 256, 384), (200, 72, 256), (257, 264, 128), (300, 136, 256))
 
 
@@ -95,12 +129,17 @@ def test_linear(lib, M, N, K, bias):
     bc = None if b is None else b.cuda()
     y = lib.w8a8_fp8_block_linear_packed(x.cuda(), wp, N, sw, bc)
     q, s = act_codes(x)
-    check(y, q, s, wq.cpu().numpy(), sw.cpu().numpy(), b, "linear")
+    if M * N * K <= 1 << 25:
+        check(y, q, s, wq.cpu().numpy(), sw.cpu().numpy(), b, "linear")
+    else:
+        check(y, q, s, wq.cpu().numpy(), sw.cpu().numpy(), b, "linear", some(M, N), some(N, M))
+    near(y, lib.w8a8_quantize_act_block(x.cuda()), (wq, sw), bc)
     qp, sp = lib.w8a8_quantize_act_block_packed(x.cuda())
     assert torch.equal(lib.w8a8_fp8_block_gemm_packed(qp, sp, wp, sw, M, N, K, bc), y)
 
 
-@pytest.mark.parametrize("M,N,K", ((1, 5120, 17408), (5, 5120, 17408), (64, 2056, 5120), (1502, 4096, 4096), (2270, 1160, 5120), (700, 17408, 1024)))
+@pytest.mark.parametrize("M,N,K", ((1, 5120, 17408), (5, 5120, 17408), (64, 2056, 5120), (64, 5120, 17408), (100, 5120, 17408), (1502, 4096, 4096), (2270, 1160, 5120),
+                                   (700, 17408, 1024), (4370, 4360, 640), (300, 65544, 512), (513, 33000, 1152)))
 def test_large(lib, M, N, K):
     """Sampled rows and columns of larger products."""
     say(f"block linear {M} x {K} x {N}")
@@ -109,18 +148,8 @@ def test_large(lib, M, N, K):
     wq, sw = lib.w8a8_quantize_weight_block((torch.randn(N, K, generator=g, device="cuda") * 0.02).to(torch.bfloat16))
     y = lib.w8a8_fp8_block_linear_packed(x, lib.w8a8_pack_weight(wq), N, sw)
     q, s = lib.w8a8_quantize_act_block(x)
-    rng = np.random.default_rng(M)
-    rows = np.unique(np.concatenate(([0, M - 1, M // 2], rng.integers(0, M, 6))))
-    block = np.unique(np.concatenate(([0, -(-N // 128) - 1], rng.integers(0, N // 128, 3))))
-    for b in block:
-        cols = slice(128 * b, min(N, 128 * b + 128))
-        check(y[rows][:, cols], q.cpu().numpy()[rows], s.cpu().numpy()[rows], wq.cpu().numpy()[cols], sw.cpu().numpy()[b:b + 1], None, "large")
-    # every output, loosely: against fp32 products of the values
-    v = (q.view(torch.float8_e4m3fn).float().view(M, -1, 128) * s[:, :, None]).view(M, K)
-    u = wq.view(torch.float8_e4m3fn).float().view(N, -1, 128) * sw.repeat_interleave(128, 0)[:N, :, None]
-    ref = v @ u.view(N, K).t()
-    rms = ref.square().mean().sqrt()
-    assert ((y.float() - ref).abs() <= ref.abs() * 2.0 ** -7 + rms * 2.0 ** -9).all()
+    check(y, q.cpu().numpy(), s.cpu().numpy(), wq.cpu().numpy(), sw.cpu().numpy(), None, "large", some(M, N)[::3], some(N, M)[::2])
+    near(y, (q, s), (wq, sw), None)
 
 
 @pytest.mark.parametrize("M", (3, 40, 200))
@@ -190,7 +219,7 @@ def test_captured_on_another_stream_and_outputs_given(lib, M):
     wq, sw = lib.w8a8_quantize_weight_block(w.cuda())
     wp = lib.w8a8_pack_weight(wq)
     want = lib.w8a8_fp8_block_linear_packed(x, wp, N, sw, b)
-    ws = torch.empty(lib.fp8_block_workspace_bytes(M, K), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(lib.fp8_block_workspace_bytes(M, N, K), dtype=torch.uint8, device="cuda")
     out = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
     torch.cuda.synchronize()
     side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()

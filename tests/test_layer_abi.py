@@ -29,8 +29,8 @@ def lib():
         "w8a8_block_scale_stride": (I64, [I64]),
         "w8a8_quantize_act_block": (I, [P, I64, I64, P, P, P]), "w8a8_quantize_act_block_packed": (I, [P, I64, I64, P, P, P]),
         "w8a8_quantize_weight_block": (I, [P, I64, I64, P, P, P]),
-        "w8a8_fp8_block_gemm_packed": (I, [P, P, P, P, P, P, I64, I64, I64, P]),
-        "w8a8_fp8_block_workspace_bytes": (SZ, [I64, I64]),
+        "w8a8_fp8_block_gemm_packed": (I, [P, P, P, P, P, P, I64, I64, I64, P, SZ, P]),
+        "w8a8_fp8_block_gemm_workspace_bytes": (SZ, [I64, I64, I64]), "w8a8_fp8_block_workspace_bytes": (SZ, [I64, I64, I64]),
         "w8a8_fp8_block_linear_packed": (I, [P, P, P, P, P, I64, I64, I64, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
@@ -46,8 +46,12 @@ def gone():
 
 def test_sizes(lib):
     assert [lib.w8a8_block_scale_stride(m) for m in (-1, 0, 1, 32, 33, 1 << 62)] == [0, 0, 32, 32, 64, 0]
-    assert lib.w8a8_fp8_block_workspace_bytes(33, 256) == 64 * 256 + 512
-    assert lib.w8a8_fp8_block_workspace_bytes(0, 256) == 0 and lib.w8a8_fp8_block_workspace_bytes(1, 0) == 0
+    size, sums = lib.w8a8_fp8_block_workspace_bytes, lib.w8a8_fp8_block_gemm_workspace_bytes
+    assert size(33, 16, 256) == 64 * 256 + 512 and sums(33, 16, 256) == 0
+    for bad in ((0, 16, 256), (1, 16, 0), (1, 12, 256), (-5, 16, 256), (1, 16, 192)):
+        assert size(*bad) == 0 and sums(*bad) == 0
+    assert sums(100, 5120, 17408) % (100 * 5120 * 4) < 256 and sums(100, 5120, 17408) >= 2 * 100 * 5120 * 4   # few tiles, long K: parts
+    assert sums(4096, 17408, 5120) == 0 and size(100, 5120, 17408) == 128 * 17408 + 136 * 512 + sums(100, 5120, 17408)
 
 
 def test_norm_refusals(lib):
@@ -106,8 +110,8 @@ def test_block_refusals(lib):
         assert f(None, 4, 128, A, A, None) == NULLP and f(A, 4, 128, None, A, None) == NULLP and f(A, 4, 128, A, None, None) == NULLP
         assert f(U, 4, 128, A, A, None) == MISALIGNED and f(A, 4, 128, A, U, None) == MISALIGNED
 
-    def gemm(q=A, s=A, w=A, sw=A, b=None, y=A, m=4, n=16, k=256):
-        return lib.w8a8_fp8_block_gemm_packed(q, s, w, sw, b, y, m, n, k, None)
+    def gemm(q=A, s=A, w=A, sw=A, b=None, y=A, m=4, n=16, k=256, ws=None, size=0):
+        return lib.w8a8_fp8_block_gemm_packed(q, s, w, sw, b, y, m, n, k, ws, size, None)
 
     def linear(x=A, w=A, sw=A, b=None, y=A, m=4, n=16, k=256, ws=A, size=1 << 20):
         return lib.w8a8_fp8_block_linear_packed(x, w, sw, b, y, m, n, k, ws, size, None)
@@ -120,9 +124,12 @@ def test_block_refusals(lib):
             assert f(**{name: None}) == NULLP and f(**{name: U}) == MISALIGNED
         assert f(b=U) == MISALIGNED
     assert gemm(q=None) == NULLP and gemm(s=U) == MISALIGNED and linear(x=None) == NULLP and linear(ws=None) == NULLP and linear(ws=U) == MISALIGNED
-    assert linear(size=lib.w8a8_fp8_block_workspace_bytes(4, 256) - 1) == BADARG
+    assert linear(size=lib.w8a8_fp8_block_workspace_bytes(4, 16, 256) - 1) == BADARG
+    need = lib.w8a8_fp8_block_gemm_workspace_bytes(100, 5120, 17408)
+    assert gemm(m=100, n=5120, k=17408, ws=A, size=need - 1) == BADARG and gemm(m=100, n=5120, k=17408, size=need) == NULLP
+    assert gemm(m=100, n=5120, k=17408, ws=U, size=need) == MISALIGNED
     if gone() == DEVICE:
-        assert gemm() == DEVICE and linear(size=lib.w8a8_fp8_block_workspace_bytes(4, 256)) == DEVICE
+        assert gemm() == DEVICE and linear(size=lib.w8a8_fp8_block_workspace_bytes(4, 16, 256)) == DEVICE
 
 
 STUBS = r'''
@@ -137,7 +144,8 @@ hipError_t launch_quantize_weight_block(const uint16_t*, int64_t, int64_t, uint8
 bool block_fused_fits(int64_t m, int64_t, int64_t) { return m == 1; }
 hipError_t launch_block_fused(const uint16_t*, const uint8_t*, const float*, const uint16_t*, uint16_t*, int64_t, int64_t, int64_t, hipStream_t) { return hipErrorUnknown; }
 hipError_t launch_block_gemm(const uint8_t*, const float*, const uint8_t*, const float*, const uint16_t*, uint16_t*, int64_t, int64_t, int64_t,
-                             hipStream_t) { return hipErrorUnknown; }
+                             float*, hipStream_t) { return hipErrorUnknown; }
+size_t block_gemm_workspace(int64_t m, int64_t n, int64_t) { return (size_t)m * (size_t)n; }
 }
 '''
 
@@ -168,9 +176,9 @@ int main() {
       w8a8_quantize_act_block_packed(a, m, k, b, f, nullptr);
       w8a8_quantize_weight_block(a, m, k, b, f, nullptr);
       w8a8_block_scale_stride(m);
-      w8a8_fp8_block_workspace_bytes(m, k);
       for (int64_t n : values) {
-        w8a8_fp8_block_gemm_packed(b, f, b, f, a, a, m, n, k, nullptr);
+        w8a8_fp8_block_gemm_packed(b, f, b, f, a, a, m, n, k, a, (size_t)-1, nullptr);
+        w8a8_fp8_block_workspace_bytes(m, n, k);
         w8a8_fp8_block_linear_packed(a, b, f, a, a, m, n, k, a, (size_t)-1, nullptr);
         w8a8_rope(a, n, a, k, reinterpret_cast<uint64_t*>(a), 64, 0, 1.0f, reinterpret_cast<int32_t*>(a), m, n, 4, 2, 64, a, n, a, k, nullptr);
         w8a8_rope(a, 1024, a, 1024, reinterpret_cast<uint64_t*>(a), k, 1, 1.0f, reinterpret_cast<int32_t*>(a), 1, 1, m, n, k, a, 1024, a, 1024, nullptr);

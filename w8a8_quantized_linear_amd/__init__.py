@@ -42,7 +42,7 @@ __all__ = [
     "w8a8_rmsnorm_quantize_fp8_packed", "w8a8_rmsnorm_quantize_block", "w8a8_rmsnorm_quantize_block_packed",
     "Rope", "rope_frequencies", "rope", "w8a8_rope",
     "block_scale_stride", "w8a8_quantize_act_block", "w8a8_quantize_act_block_packed", "w8a8_quantize_weight_block",
-    "fp8_block_workspace_bytes", "w8a8_fp8_block_gemm_packed", "w8a8_fp8_block_linear_packed",
+    "fp8_block_workspace_bytes", "fp8_block_gemm_workspace_bytes", "w8a8_fp8_block_gemm_packed", "w8a8_fp8_block_linear_packed",
 ]
 
 LIB_PATH = Path(__file__).resolve().parent / "libw8a8.so"
@@ -101,8 +101,9 @@ _SIGS = {
     "w8a8_quantize_act_block": (_I, [_P, _I64, _I64, _P, _P, _P]),
     "w8a8_quantize_act_block_packed": (_I, [_P, _I64, _I64, _P, _P, _P]),
     "w8a8_quantize_weight_block": (_I, [_P, _I64, _I64, _P, _P, _P]),
-    "w8a8_fp8_block_workspace_bytes": (_SZ, [_I64, _I64]),
-    "w8a8_fp8_block_gemm_packed": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
+    "w8a8_fp8_block_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "w8a8_fp8_block_gemm_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "w8a8_fp8_block_gemm_packed": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -756,7 +757,11 @@ def w8a8_quantize_weight_block(w: torch.Tensor):
     return q, s
 
 
-def w8a8_fp8_block_gemm_packed(q_packed, s, w_packed, s_w, M: int, N: int, K: int, bias=None, out=None):
+def fp8_block_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_lib.w8a8_fp8_block_gemm_workspace_bytes(M, N, K))
+
+
+def w8a8_fp8_block_gemm_packed(q_packed, s, w_packed, s_w, M: int, N: int, K: int, bias=None, workspace=None, out=None):
     """y bf16 [M, N] from packed E4M3FN codes of M tokens and N weight rows and their block scales."""
     _want(q_packed, torch.uint8, "q_packed", 1)
     _want(w_packed, torch.uint8, "w_packed", 1)
@@ -770,14 +775,15 @@ def w8a8_fp8_block_gemm_packed(q_packed, s, w_packed, s_w, M: int, N: int, K: in
         raise ValueError("inconsistent shapes")
     if bias is not None and bias.shape[0] != N:
         raise ValueError("bias length must equal N")
+    ws = _workspace(workspace, fp8_block_gemm_workspace_bytes(M, N, K), q_packed.device)
     y = _out(out, torch.bfloat16, M * N, "out", q_packed.device, shape=(M, N))
     _check(_lib.w8a8_fp8_block_gemm_packed(_ptr(q_packed), _ptr(s), _ptr(w_packed), _ptr(s_w), _ptr(bias), _ptr(y), M, N, K,
-                                           _stream()), "w8a8_fp8_block_gemm_packed")
+                                           _ptr(ws), ws.numel() * ws.element_size(), _stream()), "w8a8_fp8_block_gemm_packed")
     return y
 
 
-def fp8_block_workspace_bytes(M: int, K: int) -> int:
-    return int(_lib.w8a8_fp8_block_workspace_bytes(M, K))
+def fp8_block_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_lib.w8a8_fp8_block_workspace_bytes(M, N, K))
 
 
 def w8a8_fp8_block_linear_packed(x, w_packed, N: int, s_w, bias=None, workspace=None, out=None):

@@ -420,7 +420,7 @@ PyObject* fp8_block_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (b.size(0) != N) fail(PyExc_ValueError, "bias length must equal N");
       bias = bf16(b);
     }
-    const at::Tensor ws = workspace(a[5], w8a8_fp8_block_workspace_bytes(M, K), device);
+    const at::Tensor ws = workspace(a[5], w8a8_fp8_block_workspace_bytes(M, N, K), device);
     const at::Tensor y = output(a[6], "out", {M, N}, device);
     w8a8_status st;
     Py_BEGIN_ALLOW_THREADS

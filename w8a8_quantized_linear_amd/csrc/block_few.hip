@@ -160,11 +160,13 @@ hipError_t launch(const uint16_t* x, const uint8_t* q, const float* s, const uin
 
 }  // namespace
 
+// Up to 16 tokens this form reads the weight about as fast as memory gives it.  For more, whose codes every workgroup reads again, up to
+// weights of 48 Mi: 64 tokens of 5,120 x 7,168 11.4 us (12.7 with tiles), but 17,408 x 5,120 34.4 (22.8 with tiles).
+bool block_few_fits(int64_t M, int64_t N, int64_t K) { return M <= 16 || (M <= 64 && N * K <= (48 << 20)); }
+
 // Weight rows of a workgroup: 16 while that gives one workgroup a CU at most (12 tokens of 4,096 x 4,096 5.7 us, 6.2 with 32 rows;
 // 24 tokens 5.7 and 6.6; 48 tokens 7.4 and 8.7) and, up to 16 tokens, where it gives many (8 tokens of 5,120 x 34,816 31.1 and 33.1 us); 32
-// between, where 16 leave a second round of CUs half empty (5 tokens of 17,408 x 5,120 22.4 and 18.6 us; 32 tokens 34.7 and 25.5) and
-// for more tokens, whose codes every workgroup reads from the L2; 64 for more than 32 tokens and many rows (64 tokens of 5,120 x
-// 34,816 56.4 and 46.4 us).
+// between, where 16 leave a second round of CUs half empty (5 tokens of 17,408 x 5,120 22.4 and 18.6 us) and for more tokens.
 hipError_t launch_block_few(const uint8_t* q, const float* s, const uint8_t* w, const float* sw, const uint16_t* bias, uint16_t* y, int64_t M,
                             int64_t N, int64_t K, hipStream_t stream) {
   const int64_t blocks = (N + 15) / 16;
@@ -172,14 +174,13 @@ hipError_t launch_block_few(const uint8_t* q, const float* s, const uint8_t* w, 
     if (blocks > 256 && blocks <= 384) return launch<8, 2, 1, 2, false>(nullptr, q, s, w, sw, bias, y, M, N, K, stream);
     return launch<8, 1, 1, 6, false>(nullptr, q, s, w, sw, bias, y, M, N, K, stream);
   }
+  if (M > 64) return hipErrorInvalidValue;
   if (M <= 32) {
     if (blocks <= 256) return launch<4, 1, 2, 3, false>(nullptr, q, s, w, sw, bias, y, M, N, K, stream);
     return launch<4, 2, 2, 3, false>(nullptr, q, s, w, sw, bias, y, M, N, K, stream);
   }
-  if (M > kFewTokens) return hipErrorInvalidValue;
   if (blocks <= 256) return launch<4, 1, 4, 3, false>(nullptr, q, s, w, sw, bias, y, M, N, K, stream);
-  if (blocks <= 1536) return launch<4, 2, 4, 2, false>(nullptr, q, s, w, sw, bias, y, M, N, K, stream);
-  return launch<2, 4, 4, 2, false>(nullptr, q, s, w, sw, bias, y, M, N, K, stream);
+  return launch<4, 2, 4, 2, false>(nullptr, q, s, w, sw, bias, y, M, N, K, stream);
 }
 
 // A launch less (2 us) against quantizing in every workgroup: 1 token of 1,024 x 1,024 3.9 us in all, 5,120 x 5,120 8.8 against 6.6 and the

@@ -84,7 +84,8 @@ __device__ __forceinline__ int lds_piece(int r, int c) { return r * 128 + ((c ^ 
 template <int BM, int BN, int WGM, int WGN, int NST, bool WALK>
 __global__ void __launch_bounds__(64 * WGM * WGN)
 block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uint8_t* __restrict__ w, const float* __restrict__ sw,
-           const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, int64_t M, int64_t N, int K, uint32_t tiles_m, uint32_t tiles_n, uint32_t first) {
+           const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, int64_t M, int64_t N, int K, uint32_t tiles_m, uint32_t tiles_n, uint32_t first,
+           int split_blocks, float* __restrict__ sums) {
   constexpr int NT = 64 * WGM * WGN, WTM = BM / WGM, WTN = BN / WGN, TM = WTM / 16, TN = WTN / 16;
   constexpr int A_LOADS = BM * 8 / NT, B_LOADS = BN * 8 / NT, SCALES = (BM + BN) * 128;
   constexpr int STAGE = SCALES + BM * 4, LOADS = A_LOADS + B_LOADS + 1, AREA = WALK ? 2048 : 0, BIAS = WALK ? BN * 2 : 0;
@@ -94,33 +95,37 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, h = lane >> 4;
   const int wm = wave % WGM, wn = wave / WGM;
   const int64_t s_ld = block_scale_stride(M);
-  const int blocks = K / kScaleBlock;
 
-  // this workgroup's tiles: `at`, at + step, ... below `end`
+  // this workgroup's tiles: `at`, at + step, ... below `end`, and its blocks of columns: `blocks` from `block0` on
   uint32_t at, end, step = 1;
+  const int all_blocks = K / kScaleBlock;
+  int block0 = 0, blocks = all_blocks;
   if constexpr (WALK) {
     const uint32_t tiles = tiles_m * tiles_n, q8 = tiles / 8, r8 = tiles % 8, xcd = blockIdx.x % 8, begin = xcd * q8 + min(xcd, r8);
     at = begin + blockIdx.x / 8, end = begin + q8 + (xcd < r8 ? 1 : 0), step = gridDim.x / 8;
     if (at >= end) return;
   } else {
-    at = first + (uint32_t)xcd_order(blockIdx.x, gridDim.x), end = at + 1;
+    const uint32_t id = first + (uint32_t)xcd_order(blockIdx.x, gridDim.x), tiles = tiles_m * tiles_n, split = id / tiles;
+    at = __builtin_amdgcn_readfirstlane(id - split * tiles), end = at + 1;
+    block0 = __builtin_amdgcn_readfirstlane(split) * split_blocks, blocks = min(split_blocks, all_blocks - block0);
   }
   // Loads of a tile: thread t of round i fills the 16 bytes at LDS place 16 (i NT + t), piece (t % 8) ^ key of row (i NT + t) / 8; rows
   // past the last one are the last one again (their sums are not stored).  And the tokens' scales, 64 a wave (of waves beyond
   // the tokens the same ones again: every wave issues as many loads).
-  Buffer abuf, bbuf, sbuf;
+  Buffer abuf, bbuf;
+  const float* load_s;                                    // the tokens' scales of the block to load (64 bits: they may lie far apart)
   uint32_t a_at[A_LOADS], b_at[B_LOADS], s_at;
   int64_t load_m, load_n;                                 // its first token and weight row
   const float* load_sw;                                   // the scales of its weight rows of this wave, by block of columns
   int aimed = 0;                                          // tiles aimed at
-  const int s_wave = wave % (BM / 64), bias_wave = wave % (BN / 128);
+  const int s_wave = wave % (BM / 64), bias_wave = wave % (BN < 128 ? 1 : BN / 128);
   auto place = [&](uint32_t r, int p) -> uint32_t { return r / 32 * 32 * (uint32_t)K + r % 32 * 64 + (p >> 2) * 2048 + (p & 3) * 16; };
   auto aim = [&](uint32_t t) __attribute__((always_inline)) {
     uint32_t tm, tn;
     tile_of(t, tiles_m, tiles_n, tm, tn);
     load_m = (int64_t)__builtin_amdgcn_readfirstlane(tm) * BM, load_n = (int64_t)__builtin_amdgcn_readfirstlane(tn) * BN;
-    abuf = buffer(q + load_m * K), bbuf = buffer(w + load_n * K), sbuf = buffer(s + load_m);
-    load_sw = sw + min(load_n + wn * WTN, N - 1) / kScaleBlock * blocks;
+    abuf = buffer(q + load_m * K + block0 * 4096), bbuf = buffer(w + load_n * K + block0 * 4096), load_s = s + block0 * s_ld + load_m;
+    load_sw = sw + min(load_n + wn * WTN, N - 1) / kScaleBlock * all_blocks + block0;
     const uint32_t m_last = (uint32_t)min(M - 1 - load_m, (int64_t)BM), n_last = (uint32_t)min(N - 1 - load_n, (int64_t)BN);
     int id = tid;
     if constexpr (WALK) asm volatile("" : "+v"(id));      // (what follows from it is computed again, not kept in registers)
@@ -150,7 +155,7 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
     if constexpr (t < A_LOADS) lds_load16(abuf, a_at[t], (uint32_t)load_b * 4096, to + wave * 1024 + t * NT * 16);
     else if constexpr (t < A_LOADS + B_LOADS)
       lds_load16(bbuf, b_at[t - A_LOADS], (uint32_t)load_b * 4096, to + BM * 128 + wave * 1024 + (t - A_LOADS) * NT * 16);
-    else lds_load4(sbuf, s_at, (uint32_t)(load_b * s_ld) * 4, to + SCALES + s_wave * 256);
+    else lds_load4(buffer(load_s), s_at, 0, to + SCALES + s_wave * 256);
   };
 
   auto read = [&](int stage, int row, int part) __attribute__((always_inline)) -> i32x8 {
@@ -166,8 +171,8 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
   };
   // Product u of a stage (weight operand u / TM, token operand u % TM) is added to the sums behind product u + kLag: an instruction that
   // reads a product's result too early waits for it.  The last kLag of a stage are added in the next.
-  constexpr int P = TM * TN, kLag = 3, kParts = 4, kTail = 2 * TM;
-  static_assert(TN >= 4 && TN % 4 == 0 && TM > kLag, "products in flight, weight operands two ahead");
+  constexpr int P = TM * TN, kLag = TM > 3 ? 3 : TM - 1, kParts = 4, kTail = 2 * TM;
+  static_assert(TN >= 4 && TN % 4 == 0 && TM >= 2, "products in flight, weight operands two ahead");
   f32x4 acc[TN][TM], part[kParts];
   i32x8 xr[TM], wr[4];
   float by[TM], raw[TM];
@@ -202,6 +207,18 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
   // stores runs of whole row segments.  Walking, in 16 rows x 64 columns of an area of its own; otherwise all at once in the stages' place.
   auto outputs = [&](int64_t mb, int64_t nb, int tile) __attribute__((always_inline)) {
     const uint32_t m_left = (uint32_t)min(M - mb, (int64_t)BM), n_left = (uint32_t)min(N - nb, (int64_t)BN);
+    if (!WALK && sums) {                                  // a part of K: its sums [part][M][N], for add_splits
+      const int h = lane >> 4, c = lane & 15;
+      float* to = sums + (int64_t)(block0 / split_blocks) * M * N;
+      static_for<0, TM>([&](auto j_c) __attribute__((always_inline)) {
+        static_for<0, TN>([&](auto i_c) __attribute__((always_inline)) {
+          constexpr int i = decltype(i_c)::value, j = decltype(j_c)::value;
+          const uint32_t m = wm * WTM + 16 * j + c, n = wn * WTN + 16 * i + 4 * h;
+          if (m < m_left && n < n_left) *reinterpret_cast<f32x4*>(to + (mb + m) * N + nb + n) = acc[i][j];
+        });
+      });
+      return;
+    }
     float bias4[WALK ? 1 : TN][4];
     if constexpr (!WALK) {
       const int h = lane >> 4;
@@ -287,7 +304,7 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
 #pragma unroll
   for (int b = 0; b < NST; ++b) {
     static_for<0, LOADS>([&](auto t_c) __attribute__((always_inline)) { issue_one(t_c, b); });
-    load_b = min(b + 1, blocks - 1);                      // (past the last block: that one again, not used)
+    if (b + 1 < blocks) ++load_b, load_s += s_ld;         // (past the last block: that one again, not used)
     if (b == NST - 2) landed();
   }
   __builtin_amdgcn_sched_barrier(0);
@@ -306,7 +323,7 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
     const int stop = part_of == 0 ? blocks - NST : blocks;
     if (part_of == 1) {
       if (WALK && load_at + step < end) load_at += step, load_b = 0, aim(load_at);
-      else load_b = blocks - 1, load_step = 0;
+      else load_step = 0, load_s -= load_b == blocks ? s_ld : 0, load_b = blocks - 1;
     }
 #pragma clang loop unroll(disable)
     for (; b < stop; ++b) {
@@ -330,7 +347,7 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
         if constexpr (t >= 0)
           static_for<t * LOADS / kTail, (t + 1) * LOADS / kTail>([&](auto l_c) __attribute__((always_inline)) { issue_one(l_c, now); });
       });
-      load_b += load_step;
+      load_b += load_step, load_s += load_step ? s_ld : 0;
       sb = sb_next;
       now = then;
     }
@@ -350,27 +367,114 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
   wait_loads<0>();                                        // nothing lands in LDS behind the workgroup's end
 }
 
+// y = the sums of the parts of K, in their order, and the bias: 8 columns a thread.
+__global__ void __launch_bounds__(256)
+add_splits(const float* __restrict__ sums, int splits, const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, int64_t values, int64_t N,
+           int64_t first) {
+  const int64_t at = ((first + blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (at >= values) return;
+  float v[8], b[8];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) *reinterpret_cast<f32x4*>(v + 4 * i) = *reinterpret_cast<const f32x4*>(sums + at + 4 * i);
+  for (int k = 1; k < splits; ++k)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f32x4 u = *reinterpret_cast<const f32x4*>(sums + k * values + at + 4 * i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * i + e] += u[e];
+    }
+  if (bias) {
+    widen8(*reinterpret_cast<const u32x4*>(bias + at % N), b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += b[e];
+  }
+  *reinterpret_cast<u32x4*>(y + at) = narrow8(v);
+}
+
+struct Call {
+  const uint8_t* q;
+  const float* s;
+  const uint8_t* w;
+  const float* sw;
+  const uint16_t* bias;
+  uint16_t* y;
+  int64_t M, N, K;
+  hipStream_t stream;
+};
+
 template <int BM, int BN, int WGM, int WGN, int NST, bool WALK>
-hipError_t launch(const uint8_t* q, const float* s, const uint8_t* w, const float* sw, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N,
-                  int64_t K, hipStream_t stream) {
-  const int64_t tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;   // (fewer than 2^27 together)
+hipError_t launch(const Call& c, int splits, float* sums) {
+  const int64_t tiles_m = (c.M + BM - 1) / BM, tiles_n = (c.N + BN - 1) / BN;   // (fewer than 2^27 tiles)
+  const int blocks = (int)(c.K / kScaleBlock), split_blocks = (blocks + splits - 1) / splits;
   auto run = [&](int64_t first, int64_t count) {
-    hipLaunchKernelGGL((block_tile<BM, BN, WGM, WGN, NST, WALK>), dim3((unsigned)count), dim3(64 * WGM * WGN), 0, stream, q, s, w, sw, bias, y, M,
-                       N, (int)K, (uint32_t)tiles_m, (uint32_t)tiles_n, (uint32_t)first);
+    hipLaunchKernelGGL((block_tile<BM, BN, WGM, WGN, NST, WALK>), dim3((unsigned)count), dim3(64 * WGM * WGN), 0, c.stream, c.q, c.s, c.w, c.sw,
+                       c.bias, c.y, c.M, c.N, (int)c.K, (uint32_t)tiles_m, (uint32_t)tiles_n, (uint32_t)first, split_blocks,
+                       splits > 1 ? sums : nullptr);
     return hipGetLastError();
   };
   if (WALK) return run(0, std::min<int64_t>((tiles_m * tiles_n + 7) / 8, kCus / 8) * 8);
-  return in_launches(tiles_m * tiles_n, 1, 64 * WGM * WGN, run);
+  const hipError_t e = in_launches(tiles_m * tiles_n * splits, 1, 64 * WGM * WGN, run);
+  if (e != hipSuccess || splits == 1) return e;
+  return in_launches((c.M * c.N + 2047) / 2048, 1, 256, [&](int64_t first, int64_t count) {
+    hipLaunchKernelGGL(add_splits, dim3((unsigned)count), dim3(256), 0, c.stream, sums, splits, c.bias, c.y, c.M * c.N, c.N, first);
+    return hipGetLastError();
+  });
+}
+
+// Tile and parts of K.  A launch takes its rounds (workgroups over what the CUs hold) times its stages times what a stage takes:
+// measured, in us, where a CU holds one workgroup and where it holds all it can; parts cost a launch and the sums' way through
+// memory.  Over 18 shapes of 24 to 1,502 tokens what is chosen is the fastest of 29 forms or within 4% of it, once 14%: 100 tokens of 17,408 x
+// 5,120 30 us in 6 parts (53 in one), 512 of 4,096 x 4,096 15.5 with 64 x 128 (26 with 128 x 256), 1,502 29 with 128 x 256 (45 with 256 x 256).
+struct Tile {
+  int bm, bn, per_cu;
+  double one, full;
+};
+constexpr Tile kTiles[] = {{256, 256, 1, 1.40, 1.76}, {128, 256, 1, 0.82, 0.95}, {64, 256, 1, 0.60, 0.75}, {64, 128, 2, 0.45, 0.60}, {64, 64, 3, 0.41, 0.60}};
+struct Choice {
+  int tile, splits;
+};
+Choice choose(int64_t M, int64_t N, int64_t K) {
+  const int blocks = (int)(K / kScaleBlock);
+  Choice best{0, 1};
+  double least = 1e30;
+  for (int t = 0; t < 5; ++t) {
+    const Tile& c = kTiles[t];
+    const int64_t tiles = (M + c.bm - 1) / c.bm * ((N + c.bn - 1) / c.bn);
+    const int room = kCus * c.per_cu;
+    // (walking needs a few blocks of columns, and rows of outputs within 2^31 bytes of a tile's first)
+    if (t == 0 && (blocks < 4 || N > (1 << 21))) continue;
+    for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (splits > 1 && (t == 0 || blocks < 4 * splits || tiles * splits > 2 * room)) break;
+      const int stages = (blocks + splits - 1) / splits;
+      if (splits > 1 && (splits - 1) * stages >= blocks) continue;   // (a part without a block)
+      const int64_t groups = tiles * splits, rounds = groups <= room ? 1 : (groups + room - 1) / room;
+      const double time = (double)rounds * stages * (groups <= kCus ? c.one : c.full) + (splits > 1 ? 4.0 + splits * 2.2e-6 * M * N : 0.0);
+      if (time < least) least = time, best = {t, splits};
+    }
+  }
+  return best;
 }
 
 }  // namespace
 
+size_t block_gemm_workspace(int64_t M, int64_t N, int64_t K) {
+  if (block_few_fits(M, N, K)) return 0;
+  const int splits = choose(M, N, K).splits;
+  return splits == 1 ? 0 : (size_t)splits * M * N * sizeof(float);
+}
+
 hipError_t launch_block_gemm(const uint8_t* q, const float* s, const uint8_t* w, const float* sw, const uint16_t* bias, uint16_t* y, int64_t M,
-                             int64_t N, int64_t K, hipStream_t stream) {
-  if (M <= kFewTokens) return launch_block_few(q, s, w, sw, bias, y, M, N, K, stream);
-  auto tiles = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((N + bn - 1) / bn); };
-  if (tiles(256, 256) >= kCus) return launch<256, 256, 4, 2, 2, true>(q, s, w, sw, bias, y, M, N, K, stream);
-  return launch<128, 256, 2, 4, 3, false>(q, s, w, sw, bias, y, M, N, K, stream);
+                             int64_t N, int64_t K, float* sums, hipStream_t stream) {
+  if (block_few_fits(M, N, K)) return launch_block_few(q, s, w, sw, bias, y, M, N, K, stream);
+  const Choice c = choose(M, N, K);
+  const Call call{q, s, w, sw, bias, y, M, N, K, stream};
+  switch (c.tile) {
+    case 0: return launch<256, 256, 4, 2, 2, true>(call, 1, nullptr);
+    case 1: return launch<128, 256, 2, 4, 3, false>(call, c.splits, sums);
+    case 2: return launch<64, 256, 2, 4, 3, false>(call, c.splits, sums);
+    case 3: return launch<64, 128, 2, 2, 3, false>(call, c.splits, sums);
+    default: return launch<64, 64, 2, 1, 3, false>(call, c.splits, sums);
+  }
 }
 
 }  // namespace w8a8

@@ -48,15 +48,17 @@ hipError_t launch_rope(const Rope& r, hipStream_t stream);
 hipError_t launch_quantize_block(const uint16_t* x, int64_t M, int64_t K, bool packed, uint8_t* q, float* s, hipStream_t stream);
 hipError_t launch_quantize_weight_block(const uint16_t* w, int64_t N, int64_t K, uint8_t* q, float* s, hipStream_t stream);
 
-// Packed codes and their block scales, y bf16 [M, N].  block_few.hip: up to kFewTokens tokens, or x bf16 itself where
-// block_fused_fits(); block_gemm.hip: any number.
-constexpr int64_t kFewTokens = 64;
+// Packed codes and their block scales, y bf16 [M, N].  block_few.hip: where block_few_fits(), or x bf16 itself where
+// block_fused_fits(); block_gemm.hip: any shape.
+bool block_few_fits(int64_t M, int64_t N, int64_t K);
 hipError_t launch_block_few(const uint8_t* q, const float* s, const uint8_t* w, const float* sw, const uint16_t* bias, uint16_t* y,
                             int64_t M, int64_t N, int64_t K, hipStream_t stream);
 bool block_fused_fits(int64_t M, int64_t N, int64_t K);
 hipError_t launch_block_fused(const uint16_t* x, const uint8_t* w, const float* sw, const uint16_t* bias, uint16_t* y, int64_t M,
                               int64_t N, int64_t K, hipStream_t stream);
+// Bytes of the sums that launch_block_gemm needs where it cuts K (0 elsewhere).
+size_t block_gemm_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_block_gemm(const uint8_t* q, const float* s, const uint8_t* w, const float* sw, const uint16_t* bias, uint16_t* y,
-                             int64_t M, int64_t N, int64_t K, hipStream_t stream);
+                             int64_t M, int64_t N, int64_t K, float* sums, hipStream_t stream);
 
 }  // namespace w8a8

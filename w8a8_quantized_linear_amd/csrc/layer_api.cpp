@@ -52,6 +52,12 @@ w8a8_status check_block_shape(int64_t M, int64_t N, int64_t K) {
   return W8A8_OK;
 }
 
+// The packed codes of M tokens and their scales in a workspace.
+size_t code_bytes(int64_t M, int64_t K) {
+  const size_t rows = (size_t)w8a8::block_scale_stride(M);
+  return align256(rows * (size_t)K) + align256((size_t)(K / kScaleBlock) * rows * sizeof(float));
+}
+
 bool ld_ok(int64_t ld, int64_t least) { return ld >= least && ld % 8 == 0 && ld <= ((int64_t)1 << 40); }
 
 }  // namespace
@@ -133,23 +139,28 @@ w8a8_status w8a8_quantize_weight_block(const uint16_t* w, int64_t N, int64_t K, 
   return launched(w8a8::launch_quantize_weight_block(w, N, K, q, s, stream));
 }
 
+size_t w8a8_fp8_block_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return M <= 0 || check_block_shape(M, N, K) != W8A8_OK ? 0 : align256(w8a8::block_gemm_workspace(M, N, K));
+}
+
 w8a8_status w8a8_fp8_block_gemm_packed(const uint8_t* q_packed, const float* s, const uint8_t* w_packed, const float* s_w,
-                                       const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K,
-                                       hipStream_t stream) {
+                                       const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K, void* workspace,
+                                       size_t workspace_bytes, hipStream_t stream) {
   w8a8_status st = check_block_shape(M, N, K);
   if (st != W8A8_OK) return st;
   if (M == 0) return W8A8_OK;
-  if (!q_packed || !s || !w_packed || !s_w || !y) return W8A8_ERR_NULL_POINTER;
-  if (!aligned16(q_packed) || !aligned16(s) || !aligned16(w_packed) || !aligned16(s_w) || !aligned16(bias) || !aligned16(y))
+  const size_t need = w8a8_fp8_block_gemm_workspace_bytes(M, N, K);
+  if (workspace_bytes < need) return W8A8_ERR_BAD_ARGUMENT;
+  if (!q_packed || !s || !w_packed || !s_w || !y || (need && !workspace)) return W8A8_ERR_NULL_POINTER;
+  if (!aligned16(q_packed) || !aligned16(s) || !aligned16(w_packed) || !aligned16(s_w) || !aligned16(bias) || !aligned16(y) ||
+      (need && !aligned16(workspace)))
     return W8A8_ERR_MISALIGNED;
   if ((st = check_device()) != W8A8_OK) return st;
-  return launched(w8a8::launch_block_gemm(q_packed, s, w_packed, s_w, bias, y, M, N, K, stream));
+  return launched(w8a8::launch_block_gemm(q_packed, s, w_packed, s_w, bias, y, M, N, K, static_cast<float*>(workspace), stream));
 }
 
-size_t w8a8_fp8_block_workspace_bytes(int64_t M, int64_t K) {
-  if (M <= 0 || K <= 0 || K > W8A8_MAX_K || M > ((int64_t)1 << 30)) return 0;
-  const size_t rows = (size_t)w8a8::block_scale_stride(M);
-  return align256(rows * (size_t)K) + align256((size_t)(K / kScaleBlock) * rows * sizeof(float));
+size_t w8a8_fp8_block_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return M <= 0 || check_block_shape(M, N, K) != W8A8_OK ? 0 : code_bytes(M, K) + w8a8_fp8_block_gemm_workspace_bytes(M, N, K);
 }
 
 w8a8_status w8a8_fp8_block_linear_packed(const uint16_t* x, const uint8_t* w_packed, const float* s_w, const uint16_t* bias,
@@ -159,7 +170,7 @@ w8a8_status w8a8_fp8_block_linear_packed(const uint16_t* x, const uint8_t* w_pac
   if (st != W8A8_OK) return st;
   if (M > kMaxValues / K) return W8A8_ERR_BAD_SHAPE;
   if (M == 0) return W8A8_OK;
-  if (workspace_bytes < w8a8_fp8_block_workspace_bytes(M, K)) return W8A8_ERR_BAD_ARGUMENT;
+  if (workspace_bytes < w8a8_fp8_block_workspace_bytes(M, N, K)) return W8A8_ERR_BAD_ARGUMENT;
   if (!x || !w_packed || !s_w || !y || !workspace) return W8A8_ERR_NULL_POINTER;
   if (!aligned16(x) || !aligned16(w_packed) || !aligned16(s_w) || !aligned16(bias) || !aligned16(y) || !aligned16(workspace))
     return W8A8_ERR_MISALIGNED;
@@ -169,7 +180,7 @@ w8a8_status w8a8_fp8_block_linear_packed(const uint16_t* x, const uint8_t* w_pac
   float* s = reinterpret_cast<float*>(q + align256((size_t)w8a8::block_scale_stride(M) * (size_t)K));
   st = launched(w8a8::launch_quantize_block(x, M, K, true, q, s, stream));
   if (st != W8A8_OK) return st;
-  return launched(w8a8::launch_block_gemm(q, s, w_packed, s_w, bias, y, M, N, K, stream));
+  return launched(w8a8::launch_block_gemm(q, s, w_packed, s_w, bias, y, M, N, K, reinterpret_cast<float*>(q + code_bytes(M, K)), stream));
 }
 
 }  // extern "C"
