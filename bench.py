@@ -339,10 +339,7 @@ def decode(torch, lib, prompt=1502, steps=64, page=64, layers=3):
     their weights do not stay in the last-level cache."""
     from w8a8_quantized_linear_amd.decode import random_layer
     hidden, q_heads, heads, dim, ffn, group = 5120, 40, 8, 128, 17408, 64
-    stack = [random_layer(hidden, q_heads, heads, dim, ffn, group, seed=i) for i in range(layers)]
     gen = torch.Generator(device="cuda").manual_seed(1)
-    weight_bytes = sum(p.N * (k // 2 + 2 * k // group) for p, k in
-                       ((stack[0].qkv, hidden), (stack[0].o, q_heads * dim), (stack[0].gateup, hidden), (stack[0].down, ffn)))
 
     def timed(run, n):
         torch.cuda.synchronize()
@@ -354,38 +351,51 @@ def decode(torch, lib, prompt=1502, steps=64, page=64, layers=3):
         torch.cuda.synchronize()
         return e0.elapsed_time(e1) / (n * layers)
 
-    for seqs in (1, 8, 32):
-        width = -(-(prompt + steps) // page)
-        caches = [lib.kv_cache(seqs * width, heads, page, dim) for _ in stack]
-        table = torch.randperm(seqs * width, generator=gen, device="cuda").view(seqs, width).to(torch.int32)
-        lens = torch.full((seqs,), prompt, dtype=torch.int32, device="cuda")
-        x = torch.randn(seqs, prompt, hidden, generator=gen, device="cuda").to(torch.bfloat16)
-        one = x[:, -1:].contiguous()
+    for what, norms, blocks in (("one decoder layer", False, False), ("with norms and rotary positions", True, False),
+                                ("with norms, rotary positions and E4M3 block scales", True, True)):
+        stack = [random_layer(hidden, q_heads, heads, dim, ffn, group, seed=i, norms=norms, blocks=blocks) for i in range(layers)]
+        rotate = lib.rope(dim) if norms else None
+        weight_bytes = sum(p.N * (k + 4 * k // (128 * 128) if blocks else k // 2 + 2 * k // group) for p, k in
+                           ((stack[0].qkv, hidden), (stack[0].o, q_heads * dim), (stack[0].gateup, hidden), (stack[0].down, ffn)))
+        for seqs in (1, 8, 32):
+            width = -(-(prompt + steps) // page)
+            caches = [lib.kv_cache(seqs * width, heads, page, dim) for _ in stack]
+            table = torch.randperm(seqs * width, generator=gen, device="cuda").view(seqs, width).to(torch.int32)
+            lens = torch.full((seqs,), prompt, dtype=torch.int32, device="cuda")
+            x = torch.randn(seqs, prompt, hidden, generator=gen, device="cuda").to(torch.bfloat16)
+            one = x[:, -1:].contiguous()
 
-        def run(x):
-            for layer, cache in zip(stack, caches):
-                x = layer(x, cache, table, lens)
-            return x
-        prompt_ms = min([timed(lambda: run(x), 1) for _ in range(4)][1:])
-        run(one)
-        torch.cuda.synchronize()
-        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
-        with torch.cuda.graph(graph, stream=side):
-            lens.add_(1)
-            y = run(one)
-        step = []
-        for _ in range(4):
-            lens.fill_(prompt)
-            step.append(timed(graph.replay, steps))
-        step_us = min(step[1:]) * 1e3
-        if not torch.isfinite(y.float()).all():
-            raise RuntimeError("a step's output is not finite")
-        cache_bytes = 2 * seqs * heads * dim * (prompt + steps // 2)
-        print(json.dumps({"decode": "one decoder layer", "sequences": seqs, "prompt_tokens": prompt,
-                          "prompt_ms": prompt_ms, "step_us": step_us, "weight_bytes": weight_bytes,
-                          "cache_bytes": cache_bytes, "step_gbs": (weight_bytes + cache_bytes) / step_us / 1e3,
-                          "config": {"hidden": hidden, "q_heads": q_heads, "heads": heads, "dim": dim, "ffn": ffn,
-                                     "group": group, "page": page, "layers_in_turn": layers}}), flush=True)
+            def run(x):
+                if not norms:
+                    for layer, cache in zip(stack, caches):
+                        x = layer(x, cache, table, lens)
+                    return x
+                residual = None
+                for layer, cache in zip(stack, caches):
+                    x, residual = layer.step(x, residual, cache, table, lens, rotate=rotate)
+                return x + residual
+            prompt_ms = min([timed(lambda: run(x), 1) for _ in range(4)][1:])
+            run(one)
+            torch.cuda.synchronize()
+            graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+            with torch.cuda.graph(graph, stream=side):
+                lens.add_(1)
+                y = run(one)
+            step = []
+            for _ in range(4):
+                lens.fill_(prompt)
+                step.append(timed(graph.replay, steps))
+            step_us = min(step[1:]) * 1e3
+            if not torch.isfinite(y.float()).all():
+                raise RuntimeError("a step's output is not finite")
+            cache_bytes = 2 * seqs * heads * dim * (prompt + steps // 2)
+            print(json.dumps({"decode": what, "sequences": seqs, "prompt_tokens": prompt,
+                              "prompt_ms": prompt_ms, "step_us": step_us, "weight_bytes": weight_bytes,
+                              "cache_bytes": cache_bytes, "step_gbs": (weight_bytes + cache_bytes) / step_us / 1e3,
+                              "config": {"hidden": hidden, "q_heads": q_heads, "heads": heads, "dim": dim, "ffn": ffn,
+                                         "group": group, "page": page, "layers_in_turn": layers}}), flush=True)
+            del graph, caches
+        del stack
 
 
 def lds_patterns(torch, blocks=512, iters=4096, launches=5):
