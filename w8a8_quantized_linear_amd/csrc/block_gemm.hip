@@ -63,8 +63,9 @@ __device__ __forceinline__ void wait_loads() {
 }
 
 // Tiles are walked in groups of kGroupM token tiles, a contiguous range of them on each XCD, so that the workgroups that
-// run at once on an XCD share panels in its L2.
-constexpr int kGroupM = 4;
+// run at once on an XCD share panels in its L2.  (Groups of 4, 6, 8 and 16 differ by up to 5%: 12,016 x 17,408 x 5,120 930, 903, 935 and
+// 947 us, 2,270 x 5,120 x 34,816 348, 350, 354 and 352.)
+constexpr int kGroupM = 6;
 __device__ __forceinline__ void tile_of(uint32_t t, uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm, uint32_t& tn) {
   const uint32_t per_group = kGroupM * tiles_n, group = t / per_group, first = group * kGroupM, in = t - group * per_group;
   const uint32_t size = min((uint32_t)kGroupM, tiles_m - first);
@@ -91,6 +92,7 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
   constexpr int STAGE = SCALES + BM * 4, LOADS = A_LOADS + B_LOADS + 1, AREA = WALK ? 2048 : 0, BIAS = WALK ? BN * 2 : 0;
   static_assert(A_LOADS * NT == BM * 8 && B_LOADS * NT == BN * 8, "whole loads");
   static_assert(WTN <= 128 && 128 % WTN == 0, "a wave's weight rows have one scale");
+  static_assert(!WALK || NST == 2, "walking, a stage waits for every load, the bias and the last tile's stores among them");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NST * STAGE + WGM * WGN * AREA + 2 * BIAS];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, h = lane >> 4;
   const int wm = wave % WGM, wn = wave / WGM;

@@ -47,14 +47,15 @@ __device__ __forceinline__ void cos_sin(uint32_t turn, float& c, float& s) {
 // turn.
 template <bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads)
-rope_rows(Rope r, int64_t first, int64_t rows, int parts, int slots) {
-  const int units = r.dim / 16, slot = threadIdx.x / units, unit = threadIdx.x % units;
+rope_rows(Rope r, int64_t first, int64_t rows, uint32_t parts, uint32_t slots) {
+  const uint32_t units = r.dim / 16, slot = threadIdx.x / units, unit = threadIdx.x % units;
   if (slot >= slots) return;
-  const int64_t row = first + ((int64_t)blockIdx.x * slots + slot) / parts;
-  const int part = (int)(((int64_t)blockIdx.x * slots + slot) % parts);
+  const uint32_t id = blockIdx.x * slots + slot, part = id % parts;   // (below 2^32, as a launch's threads are)
+  const int64_t row = first + id / parts;
   if (row >= rows) return;
-  const int64_t seq = row / r.tokens, p = max(r.lens[seq], 0) - r.tokens + row % r.tokens;
-  const bool turned = unit < r.rotary / 16 && p >= 0;
+  const uint32_t seq = (uint32_t)row / (uint32_t)r.tokens, token = (uint32_t)row % (uint32_t)r.tokens;
+  const int64_t p = max(r.lens[seq], 0) - r.tokens + token;
+  const bool turned = (int)unit < r.rotary / 16 && p >= 0;
   float c[8], s[8];
   if (turned) {
 #pragma unroll
@@ -65,9 +66,9 @@ rope_rows(Rope r, int64_t first, int64_t rows, int parts, int slots) {
     }
   }
   // the unit's two pieces of a head: of the halves, or side by side (also behind the rotated part)
-  const bool halves = !INTERLEAVED && unit < r.rotary / 16;
-  const int lo = halves ? 8 * unit : 16 * unit, hi = halves ? lo + r.rotary / 2 : lo + 8;
-  for (int head = part; head < r.q_heads + r.heads; head += parts) {
+  const bool halves = !INTERLEAVED && (int)unit < r.rotary / 16;
+  const int lo = (int)(halves ? 8 * unit : 16 * unit), hi = halves ? lo + r.rotary / 2 : lo + 8;
+  for (int head = (int)part; head < r.q_heads + r.heads; head += (int)parts) {
     const bool is_q = head < r.q_heads;
     const int h = is_q ? head : head - r.q_heads;
     const uint16_t* x = (is_q ? r.q + row * r.ldq : r.k + row * r.ldk) + h * r.dim;
@@ -115,9 +116,9 @@ hipError_t launch_rope(const Rope& r, hipStream_t stream) {
     const int64_t left = (rows - first * slots) * parts, here = count * parts;
     const unsigned grid = (unsigned)(here * slots < left ? here : (left + slots - 1) / slots);
     if (r.interleaved)
-      hipLaunchKernelGGL(rope_rows<true>, dim3(grid), dim3(kThreads), 0, stream, r, first * slots, rows, parts, slots);
+      hipLaunchKernelGGL(rope_rows<true>, dim3(grid), dim3(kThreads), 0, stream, r, first * slots, rows, (uint32_t)parts, (uint32_t)slots);
     else
-      hipLaunchKernelGGL(rope_rows<false>, dim3(grid), dim3(kThreads), 0, stream, r, first * slots, rows, parts, slots);
+      hipLaunchKernelGGL(rope_rows<false>, dim3(grid), dim3(kThreads), 0, stream, r, first * slots, rows, (uint32_t)parts, (uint32_t)slots);
     return hipGetLastError();
   });
 }
