@@ -141,6 +141,20 @@ def test_a_row_that_is_not_finite_spoils_itself_only(lib, form):
     assert not torch.isfinite(values[1]).any() and not torch.isfinite(values[3]).all()
 
 
+def test_in_place_rows_read_twice(lib):
+    x, res, w = cuda(*inputs(3, 131072, 15))
+    y, h = lib.w8a8_rmsnorm(x, w, res)
+    for at in (0, 1):
+        x2, r2 = x.clone(), res.clone()
+        place = (x2, r2)[at]
+        assert torch.equal(lib.w8a8_rmsnorm(x2, w, r2, h=place)[0], y) and torch.equal(place, h)
+    x2, r2 = x.clone(), res.clone()
+    lib.w8a8_rmsnorm(x2, w, r2, h=r2, out=x2)
+    assert torch.equal(x2, y) and torch.equal(r2, h)
+    lib.w8a8_rmsnorm(h, w, out=h)
+    assert torch.equal(h, lib.w8a8_rmsnorm(lib.w8a8_rmsnorm(x, w, res)[1], w)[0])
+
+
 def test_in_place_and_given_outputs(lib):
     x, res, w = cuda(*inputs(37, 640, 11))
     y, h = lib.w8a8_rmsnorm(x, w, res)

@@ -616,7 +616,7 @@ def _norm(name, form, packed, x, weight, residual, eps, rot_block, h, out, scale
 
 def w8a8_rmsnorm(x, weight, residual=None, eps: float = 1e-6, out=None, h=None):
     """(y, h): h = x + residual (bf16 [M, K]; None without a residual), y = h / sqrt(mean(h^2) + eps) * weight bf16 [M, K].
-    h may be given: a tensor of its own, or the residual itself (updated in place)."""
+    h may be given: a tensor of its own, or the residual or x itself (updated in place)."""
     got = _norm("w8a8_rmsnorm", 0, False, x, weight, residual, eps, 0, h, out, None)
     return got[0], got[2]
 

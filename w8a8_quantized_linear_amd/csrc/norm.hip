@@ -42,14 +42,98 @@ __device__ __forceinline__ void rotate128(float (&v)[8], int lane) {
   }
 }
 
+// bf16(x + residual) of a piece of 8 columns.
+__device__ __forceinline__ u32x4 sum_of(u32x4 x, u32x4 r) {
+  float a[8], b[8];
+  widen8(x, a);
+  widen8(r, b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] += b[i];
+  return narrow8(a);
+}
+
+// z of a piece, rotated where asked; adds the squares of h to sum.  Columns past the row's end count as zeros.  (16 lanes of a block of 128 are
+// in or out together.)
+template <bool ROT>
+__device__ __forceinline__ void scaled(u32x4 h4, u32x4 w4, bool in, int lane, float (&z)[8], float (&sum)[4]) {
+  float h[8], w[8];
+  widen8(h4, h);
+  widen8(w4, w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    h[i] = in ? h[i] : 0.0f;
+    sum[i & 3] = __builtin_fmaf(h[i], h[i], sum[i & 3]);
+    z[i] = h[i] * w[i];
+  }
+  if constexpr (ROT) rotate128(z, lane);
+}
+
+__device__ __forceinline__ float top_of(const float (&z)[8], float top) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(z[i]));
+  return top;
+}
+
+// Sum (and maximum) over the row's waves, the same in all of them.
+template <bool MAX>
+__device__ __forceinline__ void meet(float& total, float& top) {
+  __shared__ float red[2][16];
+  const int tid = threadIdx.x, waves = blockDim.x >> 6;
+  total = sum64(total);
+  if constexpr (MAX) top = max64(top);
+  if (waves == 1) return;
+  if ((tid & 63) == 0) {
+    red[0][tid >> 6] = total;
+    red[1][tid >> 6] = top;
+  }
+  __syncthreads();
+  total = 0.0f;
+  for (int w = 0; w < waves; ++w) {
+    total += red[0][w];
+    top = fmaxf(top, red[1][w]);
+  }
+}
+
+// What a row's pieces are written with: r, and the scale of z where the row has one.
+template <NormOut OUT>
+struct Out {
+  float r;
+  qm::QuotientScale qs;
+  __device__ __forceinline__ Out(const Norm& n, int64_t row, float total, float top) : r(1.0f / sqrtf(total / (float)n.K + n.eps)) {
+    if constexpr (OUT == NormOut::kI8 || OUT == NormOut::kFp8) {
+      const float s = top / (OUT == NormOut::kI8 ? 127.0f : 448.0f);
+      if (threadIdx.x == 0) n.scales[row] = s * r;
+      qs = qm::quotient_scale(s);
+    }
+  }
+  // the piece at column e (whole rows of 16 lanes call it)
+  __device__ __forceinline__ void write(const Norm& n, int64_t row, int64_t e, bool in, int lane, float (&z)[8]) {
+    if constexpr (OUT == NormOut::kBf16) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] *= r;
+      if (in) *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(n.out) + row * n.K + e) = narrow8(z);
+    } else {
+      if constexpr (OUT == NormOut::kBlock) {
+        const float s = max16(top_of(z, 0.0f)) / 448.0f;
+        qs = qm::quotient_scale(s);
+        const int64_t s_ld = n.packed ? block_scale_stride(n.M) : n.K / kScaleBlock;
+        if (in && (lane & 15) == 0) n.scales[n.packed ? e / kScaleBlock * s_ld + row : row * s_ld + e / kScaleBlock] = s * r;
+      }
+      qm::apply_prefactor(z, qs);
+      const u32x2 c = OUT == NormOut::kI8 ? int8_codes8(z, qs) : e4m3_codes8(z, qs);
+      if (in) *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(n.out) + code_at(row, e, n.K, n.packed)) = c;
+    }
+  }
+};
+
 // A workgroup of T threads for each row; a thread holds V pieces of 8 columns, T * 8 columns apart, so that every load
 // and store of a wave is one run of memory and 16 lanes hold a block of 128 columns.
 template <int V, NormOut OUT, bool ROT>
 __global__ void __launch_bounds__(1024)
 norm_rows(Norm n, int64_t first) {
+  constexpr bool TOKEN = OUT == NormOut::kI8 || OUT == NormOut::kFp8;
   const int tid = threadIdx.x, T = blockDim.x, lane = tid & 63;
-  const int64_t K = n.K, row = first + xcd_order(blockIdx.x, gridDim.x);
-  const int64_t at = row * K;
+  const int64_t K = n.K, row = first + xcd_order(blockIdx.x, gridDim.x), at = row * K;
   u32x4 hv[V], wv[V];
   float z[V][8];
   bool in[V];
@@ -62,14 +146,7 @@ norm_rows(Norm n, int64_t first) {
 #pragma unroll
     for (int j = 0; j < V; ++j) rv[j] = *reinterpret_cast<const u32x4*>(n.residual + at + (in[j] ? (j * T + tid) * 8 : 0));
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      float a[8], b[8];
-      widen8(hv[j], a);
-      widen8(rv[j], b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] += b[i];
-      hv[j] = narrow8(a);
-    }
+    for (int j = 0; j < V; ++j) hv[j] = sum_of(hv[j], rv[j]);
   }
 #pragma unroll
   for (int j = 0; j < V; ++j) wv[j] = *reinterpret_cast<const u32x4*>(n.weight + (in[j] ? (j * T + tid) * 8 : 0));
@@ -78,94 +155,72 @@ norm_rows(Norm n, int64_t first) {
     for (int j = 0; j < V; ++j)
       if (in[j]) *reinterpret_cast<u32x4*>(n.h + at + (j * T + tid) * 8) = hv[j];
   }
-
   float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f}, top = 0.0f;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    float h[8], w[8];
-    widen8(hv[j], h);
-    widen8(wv[j], w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      h[i] = in[j] ? h[i] : 0.0f;                       // (16 lanes of a block of 128 are in or out together)
-      sum[i & 3] = __builtin_fmaf(h[i], h[i], sum[i & 3]);
-      z[j][i] = h[i] * w[i];
-    }
-    if constexpr (ROT) rotate128(z[j], lane);
-    if constexpr (OUT == NormOut::kI8 || OUT == NormOut::kFp8) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(z[j][i]));
-    }
+    scaled<ROT>(hv[j], wv[j], in[j], lane, z[j], sum);
+    if constexpr (TOKEN) top = top_of(z[j], top);
   }
-  __shared__ float red[2][16];
-  float total = sum64((sum[0] + sum[1]) + (sum[2] + sum[3]));
-  if constexpr (OUT == NormOut::kI8 || OUT == NormOut::kFp8) top = max64(top);
-  if (T > 64) {
-    if (lane == 0) {
-      red[0][tid >> 6] = total;
-      red[1][tid >> 6] = top;
-    }
-    __syncthreads();
-    total = 0.0f;
-    for (int w = 0; w < T >> 6; ++w) {
-      total += red[0][w];
-      top = fmaxf(top, red[1][w]);
-    }
-  }
-  const float r = 1.0f / sqrtf(total / (float)K + n.eps);
+  float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  meet<TOKEN>(total, top);
+  Out<OUT> out(n, row, total, top);
+#pragma unroll
+  for (int j = 0; j < V; ++j) out.write(n, row, (int64_t)(j * T + tid) * 8, in[j], lane, z[j]);
+}
 
-  if constexpr (OUT == NormOut::kBf16) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[j][i] *= r;
-      if (in[j]) *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(n.out) + at + (j * T + tid) * 8) = narrow8(z[j]);
-    }
-  } else {
-    uint8_t* q = static_cast<uint8_t*>(n.out);
-    qm::QuotientScale qs;
-    if constexpr (OUT != NormOut::kBlock) {
-      const float s = top / (OUT == NormOut::kI8 ? 127.0f : 448.0f);
-      if (tid == 0) n.scales[row] = s * r;
-      qs = qm::quotient_scale(s);
-    }
-    const int64_t s_ld = n.packed ? block_scale_stride(n.M) : K / kScaleBlock;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int64_t e = (int64_t)(j * T + tid) * 8;
-      if constexpr (OUT == NormOut::kBlock) {
-        float m = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(z[j][i]));
-        const float s = max16(m) / 448.0f;
-        qs = qm::quotient_scale(s);
-        if (in[j] && (lane & 15) == 0) n.scales[n.packed ? e / kScaleBlock * s_ld + row : row * s_ld + e / kScaleBlock] = s * r;
-      }
-      qm::apply_prefactor(z[j], qs);
-      const u32x2 c = OUT == NormOut::kI8 ? int8_codes8(z[j], qs) : e4m3_codes8(z[j], qs);
-      if (in[j]) *reinterpret_cast<u32x2*>(q + code_at(row, e, K, n.packed)) = c;
-    }
+// Rows of more columns than a workgroup's registers hold (K > 65,536): each piece is read twice, the second time out of a cache.
+// 300 x 131,072 with a residual: 81 us (3.9 TB/s of what must move); with 16 pieces a thread in norm_rows, which spill, 250 us.
+template <NormOut OUT, bool ROT>
+__global__ void __launch_bounds__(1024)
+norm_wide(Norm n, int64_t first) {
+  constexpr bool TOKEN = OUT == NormOut::kI8 || OUT == NormOut::kFp8;
+  const int tid = threadIdx.x, T = blockDim.x, lane = tid & 63, K = (int)n.K;
+  const int64_t row = first + xcd_order(blockIdx.x, gridDim.x), at = row * n.K;
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f}, top = 0.0f;
+  auto load = [&](const uint16_t* p, int e) __attribute__((always_inline)) { return *reinterpret_cast<const u32x4*>(p + (e < K ? e : 0)); };
+  for (int base = 0; base < K; base += T * 8) {
+    const int e = base + tid * 8;
+    u32x4 h = load(n.x + at, e);
+    if (n.residual) h = sum_of(h, load(n.residual + at, e));
+    if (n.h && e < K) *reinterpret_cast<u32x4*>(n.h + at + e) = h;
+    float z[8];
+    scaled<ROT>(h, load(n.weight, e), e < K, lane, z, sum);
+    if constexpr (TOKEN) top = top_of(z, top);
   }
+  float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  meet<TOKEN>(total, top);
+  Out<OUT> out(n, row, total, top);
+  // h where it was written (it may have taken x's or the residual's place), by this thread itself; otherwise from x again
+  for (int base = 0; base < K; base += T * 8) {
+    const int e = base + tid * 8;
+    u32x4 h = load((n.h ? n.h : n.x) + at, e);
+    if (!n.h && n.residual) h = sum_of(h, load(n.residual + at, e));
+    float z[8], again[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    scaled<ROT>(h, load(n.weight, e), e < K, lane, z, again);
+    out.write(n, row, e, e < K, lane, z);
+  }
+}
+
+// V pieces a thread, or norm_wide (V = 0).
+template <int V, NormOut OUT, bool ROT>
+hipError_t launch_kernel(const Norm& n, int T, hipStream_t stream) {
+  return in_launches(n.M, 1, T, [&](int64_t first, int64_t count) {
+    const dim3 grid((unsigned)count), block((unsigned)T);
+    if constexpr (V == 0) hipLaunchKernelGGL((norm_wide<OUT, ROT>), grid, block, 0, stream, n, first);
+    else hipLaunchKernelGGL((norm_rows<V, OUT, ROT>), grid, block, 0, stream, n, first);
+    return hipGetLastError();
+  });
 }
 
 template <int V>
 hipError_t launch_v(const Norm& n, int T, hipStream_t stream) {
-  return in_launches(n.M, 1, T, [&](int64_t first, int64_t count) {
-    const dim3 grid((unsigned)count), block((unsigned)T);
-    switch (n.kind) {
-      case NormOut::kBf16: hipLaunchKernelGGL((norm_rows<V, NormOut::kBf16, false>), grid, block, 0, stream, n, first); break;
-      case NormOut::kI8:
-        if (n.rotate) hipLaunchKernelGGL((norm_rows<V, NormOut::kI8, true>), grid, block, 0, stream, n, first);
-        else hipLaunchKernelGGL((norm_rows<V, NormOut::kI8, false>), grid, block, 0, stream, n, first);
-        break;
-      case NormOut::kFp8:
-        if (n.rotate) hipLaunchKernelGGL((norm_rows<V, NormOut::kFp8, true>), grid, block, 0, stream, n, first);
-        else hipLaunchKernelGGL((norm_rows<V, NormOut::kFp8, false>), grid, block, 0, stream, n, first);
-        break;
-      case NormOut::kBlock: hipLaunchKernelGGL((norm_rows<V, NormOut::kBlock, false>), grid, block, 0, stream, n, first); break;
-    }
-    return hipGetLastError();
-  });
+  switch (n.kind) {
+    case NormOut::kBf16: return launch_kernel<V, NormOut::kBf16, false>(n, T, stream);
+    case NormOut::kI8: return n.rotate ? launch_kernel<V, NormOut::kI8, true>(n, T, stream) : launch_kernel<V, NormOut::kI8, false>(n, T, stream);
+    case NormOut::kFp8: return n.rotate ? launch_kernel<V, NormOut::kFp8, true>(n, T, stream) : launch_kernel<V, NormOut::kFp8, false>(n, T, stream);
+    case NormOut::kBlock: return launch_kernel<V, NormOut::kBlock, false>(n, T, stream);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
@@ -173,7 +228,8 @@ hipError_t launch_v(const Norm& n, int T, hipStream_t stream) {
 // As few pieces a thread as fit: 12,016 x 5,120 with a residual and block scales 80.7 us with one piece in 640 threads, 87.6 with three
 // in 256; 2,270 x 17,408 56.6 with three in 768, 63.1 with four in 576.  A row that is read alone and is no residual's is in flight
 // for too short a time for that: 2,270 x 5,120 to E4M3 13.7 us with one piece in 640 threads, 10.6 with two in 320 (bf16, 4,000 x
-// 8,192: 26.8 and 27.8).
+// 8,192: 26.8 and 27.8).  Eight pieces spill up to ten registers and still are the faster form: 300 x 65,536 with a residual 30.4 us,
+// 32.4 in norm_wide.
 hipError_t launch_norm(const Norm& n, hipStream_t stream) {
   const int64_t pieces = (n.K + 7) / 8;
   const int64_t most = n.residual || n.M <= 256 ? 1024 : 512;
@@ -185,7 +241,7 @@ hipError_t launch_norm(const Norm& n, hipStream_t stream) {
   if (least <= 3) return launch_v<3>(n, threads(3), stream);
   if (least <= 4) return launch_v<4>(n, threads(4), stream);
   if (least <= 8) return launch_v<8>(n, threads(8), stream);
-  return launch_v<16>(n, threads(16), stream);
+  return launch_v<0>(n, 1024, stream);
 }
 
 }  // namespace w8a8
