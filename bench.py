@@ -120,7 +120,8 @@ def parse():
                     help="instead of the workload line: a decoder layer (5,120 wide, 40 query and 8 cache heads "
                          "of 128, 17,408 in the MLP) on 1, 8 and 32 sequences: a prompt of 1,502 tokens each "
                          "through the 8-bit projections, then steps of one token through the 4-bit ones, "
-                         "the paged 8-bit cache and its attention, captured into a HIP graph")
+                         "the paged 8-bit cache and its attention, captured into a HIP graph; then the same with "
+                         "norms and rotary positions, and with E4M3 projections with block scales for all tokens")
     ap.add_argument("--pmc-summary", nargs=2, metavar=("FETCH_DIR", "WRITE_DIR"),
                     help="summarize rocprofv3 FETCH_SIZE / WRITE_SIZE runs of this script into "
                          "profiles/traffic_<workload>.json and exit")
@@ -335,7 +336,7 @@ def stream_peak(torch, W, lib, names, launches=50):
 
 def decode(torch, lib, prompt=1502, steps=64, page=64, layers=3):
     """Time of a prompt and of a captured single-token step of one decoder layer, beside the bytes that a step
-    cannot do without (4-bit weights and scales, the cache's codes).  Several layers take turns, so that
+    cannot do without (weights and scales, 4-bit or E4M3, the cache's codes).  Several layers take turns, so that
     their weights do not stay in the last-level cache."""
     from w8a8_quantized_linear_amd.decode import random_layer
     hidden, q_heads, heads, dim, ffn, group = 5120, 40, 8, 128, 17408, 64

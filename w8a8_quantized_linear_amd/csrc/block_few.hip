@@ -4,8 +4,12 @@
 //
 // A workgroup owns 16 RB weight rows and up to 16 TB tokens; its W waves take the blocks of 128 columns in turn, operands
 // straight from memory into registers (each weight byte is used by one wave, the tokens' codes stay in the L2), D steps
-// ahead.  Nothing is shared and nothing waits for another wave before the end, where the 8 sums meet in LDS in the order
+// ahead.  Nothing is shared and nothing waits for another wave before the end, where the W sums meet in LDS in the order
 // of the waves.  One workgroup reads all of K, so there is no second launch and no workspace for the sums.
+//
+// 5 tokens of 17,408 x 5,120 take 15.5 to 16.6 us (89 MB, 5.4 to 5.7 TB/s; a kernel that only reads does 5.4 over 96
+// MiB), 8 of 5,120 x 34,816 31 us (5.7 TB/s): the weight's bytes are what bounds it.  A small weight is three dependent
+// trips to memory and the joining of the sums: 1 token of 1,024 x 1,024 3.8 us.
 //
 // FUSED: x comes as bf16 and every workgroup quantizes the tokens itself, in operand layout: a lane holds a quarter of a
 // block of one token.  That saves a launch (about 2 us) and costs about a thousand cycles a step, so it is for weights of
@@ -160,13 +164,15 @@ hipError_t launch(const uint16_t* x, const uint8_t* q, const float* s, const uin
 
 }  // namespace
 
-// Up to 16 tokens this form reads the weight about as fast as memory gives it.  For more, whose codes every workgroup reads again, up to
-// weights of 48 Mi: 64 tokens of 5,120 x 7,168 11.4 us (12.7 with tiles), but 17,408 x 5,120 34.4 (22.8 with tiles).
+// Up to 16 tokens this form reads the weight about as fast as memory gives it.  For more, whose codes every workgroup
+// reads again, up to weights of 48 Mi: 64 tokens of 5,120 x 7,168 11.4 us (12.7 with tiles), but 17,408 x 5,120 34.4
+// (22.8 with tiles).
 bool block_few_fits(int64_t M, int64_t N, int64_t K) { return M <= 16 || (M <= 64 && N * K <= (48 << 20)); }
 
-// Weight rows of a workgroup: 16 while that gives one workgroup a CU at most (12 tokens of 4,096 x 4,096 5.7 us, 6.2 with 32 rows;
-// 24 tokens 5.7 and 6.6; 48 tokens 7.4 and 8.7) and, up to 16 tokens, where it gives many (8 tokens of 5,120 x 34,816 31.1 and 33.1 us); 32
-// between, where 16 leave a second round of CUs half empty (5 tokens of 17,408 x 5,120 22.4 and 18.6 us) and for more tokens.
+// Weight rows of a workgroup: 16 while that gives one workgroup a CU at most (12 tokens of 4,096 x 4,096 5.7 us, 6.2
+// with 32 rows; 24 tokens 5.7 and 6.6; 48 tokens 7.4 and 8.7) and, up to 16 tokens, where it gives many (8 tokens of
+// 5,120 x 34,816 31.1 and 33.1 us); 32 between, where 16 leave a second round of CUs half empty (5 tokens of 17,408 x
+// 5,120 22.4 and 18.6 us) and for more tokens.
 hipError_t launch_block_few(const uint8_t* q, const float* s, const uint8_t* w, const float* sw, const uint16_t* bias, uint16_t* y, int64_t M,
                             int64_t N, int64_t K, hipStream_t stream) {
   const int64_t blocks = (N + 15) / 16;
@@ -183,8 +189,8 @@ hipError_t launch_block_few(const uint8_t* q, const float* s, const uint8_t* w, 
   return launch<4, 2, 4, 2, false>(nullptr, q, s, w, sw, bias, y, M, N, K, stream);
 }
 
-// A launch less (2 us) against quantizing in every workgroup: 1 token of 1,024 x 1,024 3.9 us in all, 5,120 x 5,120 8.8 against 6.6 and the
-// quantizer.
+// A launch less (2 us) against quantizing in every workgroup: 1 token of 1,024 x 1,024 3.9 us in all, 5,120 x 5,120 8.8
+// against 6.6 and the quantizer.
 bool block_fused_fits(int64_t M, int64_t N, int64_t K) { return M <= 16 && (N + 15) / 16 * (K / kScaleBlock) <= 4096; }
 
 hipError_t launch_block_fused(const uint16_t* x, const uint8_t* w, const float* sw, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N,

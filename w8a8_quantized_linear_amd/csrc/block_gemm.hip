@@ -3,17 +3,25 @@
 // What it computes: y[m][n] = bf16(sum over blocks b of 128 columns of s[b][m] * sw[n / 128][b] * (sum over the block of
 // q[m][k] * w[n][k]) + bias[n]): the inner sums on the E4M3 matrix instructions (block_math.h), the outer one in fp32.
 //
-// A workgroup of WGM x WGN waves owns BM tokens x BN weight rows; a wave accumulates 16 TM tokens x 16 TN rows.  One stage is
-// one block of 128 columns of both operands, 128 bytes a row, and the tokens' scales, which NST LDS buffers take in turn by direct-to-LDS
-// loads;
-// each product starts from zero and is multiplied into the sums by s * sw, four multiply-adds a lane beside 32 cycles
-// of the matrix unit.
+// A workgroup of WGM x WGN waves owns BM tokens x BN weight rows; a wave accumulates 16 TM tokens x 16 TN rows.  One
+// stage is one block of 128 columns of both operands, 128 bytes a row, and the tokens' scales, which NST LDS buffers take
+// in turn by direct-to-LDS loads; each product starts from zero and is multiplied into the sums by s * sw, four
+// multiply-adds a lane beside 32 cycles of the matrix unit.
 //
 // A stage's products run over the weight operands, each with all token operands of the wave, which stay in registers;
-// weight operands are read two ahead.  Two weight operands before its end the wave has read all of the stage: there it waits until
-// the next stage has landed and every wave is as far (one barrier a stage), then issues the loads of the stage behind it into
-// the buffer that is free now, one or two beside each product (in one go, both waves of a SIMD left the matrix unit idle meanwhile), and
-// replaces each token operand by the next stage's behind its last product.
+// weight operands are read two ahead.  Two weight operands before its end the wave has read all of the stage: there it
+// waits until the next stage has landed and every wave is as far (one barrier a stage), then issues the loads of the
+// stage behind it into the buffer that is free now, one or two beside each product (in one go, both waves of a SIMD left
+// the matrix unit idle meanwhile), and replaces each token operand by the next stage's behind its last product.
+//
+// What bounds it: 256 x 256 tiles the chip's power.  2,270 x 5,120 x 34,816 takes 350 to 372 us (2.2 to 2.3 PFLOP/s),
+// 8,192 x 8,192 x 8,192 435 (2.5), at 1.85 to 1.97 GHz of the 2.4 that 5 PFLOP/s need, the matrix unit busy for 66% of
+// the cycles.  The same products and multiply-adds on operands that stay in registers reach 3.45 PFLOP/s at whatever
+// clock that leaves, this kernel without its loads from memory 2.98; its barriers and the loads' latency are 0 to 3%.  A
+// matrix instruction of 32 x 32 outputs, 192 x 256 tiles and other wave priorities were no faster; a wave of 128 x 128
+// outputs, which would read a third less from LDS, has more sums than the 256 registers that vector instructions reach.
+// Smaller tiles: 1,502 x 4,096 x 4,096 29 us, one round of 192 workgroups on 256 CUs, the matrix unit of those busy for
+// 54%; 64 x 5,120 x 34,816 37 us, the weight's bytes at 4.8 TB/s.
 #include <algorithm>
 #include <type_traits>
 
@@ -28,7 +36,8 @@ using namespace lm;
 
 constexpr int kCus = 256;
 
-// A read-only value at an address that is uniform over the wave, by a scalar load: it is not counted with the loads of the stages.
+// A read-only value at an address that is uniform over the wave, by a scalar load: it is not counted with the loads of
+// the stages.
 __device__ __forceinline__ float uniform_load(const float* p) {
   const uint64_t u = reinterpret_cast<uint64_t>(p);
   const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(u >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)u);
@@ -63,8 +72,8 @@ __device__ __forceinline__ void wait_loads() {
 }
 
 // Tiles are walked in groups of kGroupM token tiles, a contiguous range of them on each XCD, so that the workgroups that
-// run at once on an XCD share panels in its L2.  (Groups of 4, 6, 8 and 16 differ by up to 5%: 12,016 x 17,408 x 5,120 930, 903, 935 and
-// 947 us, 2,270 x 5,120 x 34,816 348, 350, 354 and 352.)
+// run at once on an XCD share panels in its L2.  (Groups of 4, 6, 8 and 16 differ by up to 5%: 12,016 x 17,408 x 5,120
+// 930, 903, 935 and 947 us, 2,270 x 5,120 x 34,816 348, 350, 354 and 352.)
 constexpr int kGroupM = 6;
 __device__ __forceinline__ void tile_of(uint32_t t, uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm, uint32_t& tn) {
   const uint32_t per_group = kGroupM * tiles_n, group = t / per_group, first = group * kGroupM, in = t - group * per_group;
@@ -73,15 +82,15 @@ __device__ __forceinline__ void tile_of(uint32_t t, uint32_t tiles_m, uint32_t t
   tn = in / size;
 }
 
-// Rows of 128 bytes in LDS, eight pieces of 16: piece c of row r at c ^ (r / 2 % 8).  16 lanes of a read take the same piece of 16
-// consecutive rows in one cycle; even and odd rows lie in the two halves of the 64 banks, and the key spreads each half's
-// eight rows over its eight pieces (with r % 8 as the key, rows r and r + 8 meet and a read takes twice as long: 2,270 x 5,120 x
-// 34,816 378 us).
+// Rows of 128 bytes in LDS, eight pieces of 16: piece c of row r at c ^ (r / 2 % 8).  16 lanes of a read take the same
+// piece of 16 consecutive rows in one cycle; even and odd rows lie in the two halves of the 64 banks, and the key spreads
+// each half's eight rows over its eight pieces.  (With r % 8 as the key, rows r and r + 8 meet and a read takes twice as
+// long, which does not show where the clock is the limit: 2,270 x 5,120 x 34,816 371 us with either.)
 __device__ __forceinline__ int lds_key(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ int lds_piece(int r, int c) { return r * 128 + ((c ^ lds_key(r)) << 4); }
 
-// WALK: a workgroup for each CU, which walks over tiles of its XCD's range; the stages run on from one tile into the next, whose first
-// ones load while this tile's outputs leave.  Otherwise a workgroup for each tile.
+// WALK: a workgroup for each CU, which walks over tiles of its XCD's range; the stages run on from one tile into the
+// next, whose first ones load while this tile's outputs leave.  Otherwise a workgroup for each tile.
 template <int BM, int BN, int WGM, int WGN, int NST, bool WALK>
 __global__ void __launch_bounds__(64 * WGM * WGN)
 block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uint8_t* __restrict__ w, const float* __restrict__ sw,
@@ -111,9 +120,9 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
     at = __builtin_amdgcn_readfirstlane(id - split * tiles), end = at + 1;
     block0 = __builtin_amdgcn_readfirstlane(split) * split_blocks, blocks = min(split_blocks, all_blocks - block0);
   }
-  // Loads of a tile: thread t of round i fills the 16 bytes at LDS place 16 (i NT + t), piece (t % 8) ^ key of row (i NT + t) / 8; rows
-  // past the last one are the last one again (their sums are not stored).  And the tokens' scales, 64 a wave (of waves beyond
-  // the tokens the same ones again: every wave issues as many loads).
+  // Loads of a tile: thread t of round i fills the 16 bytes at LDS place 16 (i NT + t), piece (t % 8) ^ key of row (i NT
+  // + t) / 8; rows past the last one are the last one again (their sums are not stored).  And the tokens' scales, 64 a
+  // wave (of waves beyond the tokens the same ones again: every wave issues as many loads).
   Buffer abuf, bbuf;
   const float* load_s;                                    // the tokens' scales of the block to load (64 bits: they may lie far apart)
   uint32_t a_at[A_LOADS], b_at[B_LOADS], s_at;
@@ -171,8 +180,8 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
   auto read_s = [&](int stage, int j) __attribute__((always_inline)) {
     return *reinterpret_cast<const float*>(lds + stage * STAGE + SCALES + (wm * WTM + 16 * j + c) * 4);
   };
-  // Product u of a stage (weight operand u / TM, token operand u % TM) is added to the sums behind product u + kLag: an instruction that
-  // reads a product's result too early waits for it.  The last kLag of a stage are added in the next.
+  // Product u of a stage (weight operand u / TM, token operand u % TM) is added to the sums behind product u + kLag: an
+  // instruction that reads a product's result too early waits for it.  The last kLag of a stage are added in the next.
   constexpr int P = TM * TN, kLag = TM > 3 ? 3 : TM - 1, kParts = 4, kTail = 2 * TM;
   static_assert(TN >= 4 && TN % 4 == 0 && TM >= 2, "products in flight, weight operands two ahead");
   f32x4 acc[TN][TM], part[kParts];
@@ -194,8 +203,8 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
     for (int e = 0; e < 4; ++e) acc[u / TM][u % TM][e] = __builtin_fmaf(part[u % kParts][e], f, acc[u / TM][u % TM][e]);
   };
 
-  // The next stage has landed (the stages behind it may still be on their way) and this wave's LDS reads are done, and so for every
-  // wave.
+  // The next stage has landed (the stages behind it may still be on their way) and this wave's LDS reads are done, and
+  // so for every wave.
   auto landed = [&]() __attribute__((always_inline)) {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
@@ -205,8 +214,9 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
     asm volatile("" ::: "memory");
   };
 
-  // Outputs: a product leaves 8 bytes of each of 16 rows a store, so a wave lays rows out in LDS first, pieces of 16 bytes at c ^ row, and
-  // stores runs of whole row segments.  Walking, in 16 rows x 64 columns of an area of its own; otherwise all at once in the stages' place.
+  // Outputs: a product leaves 8 bytes of each of 16 rows a store, so a wave lays rows out in LDS first, pieces of 16
+  // bytes at c ^ row, and stores runs of whole row segments.  Walking, in 16 rows x 64 columns of an area of its own;
+  // otherwise all at once in the stages' place.
   auto outputs = [&](int64_t mb, int64_t nb, int tile) __attribute__((always_inline)) {
     const uint32_t m_left = (uint32_t)min(M - mb, (int64_t)BM), n_left = (uint32_t)min(N - nb, (int64_t)BN);
     if (!WALK && sums) {                                  // a part of K: its sums [part][M][N], for add_splits
@@ -322,37 +332,35 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
     int b = 0, load_step = 1;
 #pragma clang loop unroll(disable)
     for (int part_of = 0; part_of < 2; ++part_of) {
-    const int stop = part_of == 0 ? blocks - NST : blocks;
-    if (part_of == 1) {
-      if (WALK && load_at + step < end) load_at += step, load_b = 0, aim(load_at);
-      else load_step = 0, load_s -= load_b == blocks ? s_ld : 0, load_b = blocks - 1;
-    }
+      const int stop = part_of == 0 ? blocks - NST : blocks;
+      if (part_of == 1) {
+        if (WALK && load_at + step < end) load_at += step, load_b = 0, aim(load_at);
+        else load_step = 0, load_s -= load_b == blocks ? s_ld : 0, load_b = blocks - 1;
+      }
 #pragma clang loop unroll(disable)
-    for (; b < stop; ++b) {
-      const int then = now + 1 == NST ? 0 : now + 1;
-      const float sb_next = uniform_load(swp + min(b + 1, blocks - 1));
-      static_for<0, P>([&](auto u_c) __attribute__((always_inline)) {
-        constexpr int u = decltype(u_c)::value, i = u / TM, j = u % TM, t = u - (P - kTail);
-        if constexpr (t == 0) {
-          landed();
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        part[u % kParts] = mfma128(wr[i % 4], xr[j]);
-        if constexpr (u < kLag) {
-          add(std::integral_constant<int, P - kLag + u>{}, by[TM - kLag + u]);
-        } else {
-          if constexpr (u - kLag < TM) by[u - kLag] = raw[u - kLag] * sb;
-          add(std::integral_constant<int, u - kLag>{}, by[(u - kLag) % TM]);
-        }
-        if constexpr (j == 0) wr[(i + 2) % 4] = i < TN - 2 ? read_w(now, i + 2) : read_w(then, i + 2 - TN);
-        if constexpr (i == TN - 1) xr[j] = read_x(then, j), raw[j] = read_s(then, j);
-        if constexpr (t >= 0)
-          static_for<t * LOADS / kTail, (t + 1) * LOADS / kTail>([&](auto l_c) __attribute__((always_inline)) { issue_one(l_c, now); });
-      });
-      load_b += load_step, load_s += load_step ? s_ld : 0;
-      sb = sb_next;
-      now = then;
-    }
+      for (; b < stop; ++b) {
+        const int then = now + 1 == NST ? 0 : now + 1;
+        const float sb_next = uniform_load(swp + min(b + 1, blocks - 1));
+        static_for<0, P>([&](auto u_c) __attribute__((always_inline)) {
+          constexpr int u = decltype(u_c)::value, i = u / TM, j = u % TM, t = u - (P - kTail);
+          if constexpr (t == 0) landed();
+          __builtin_amdgcn_sched_barrier(0);
+          part[u % kParts] = mfma128(wr[i % 4], xr[j]);
+          if constexpr (u < kLag) {
+            add(std::integral_constant<int, P - kLag + u>{}, by[TM - kLag + u]);
+          } else {
+            if constexpr (u - kLag < TM) by[u - kLag] = raw[u - kLag] * sb;
+            add(std::integral_constant<int, u - kLag>{}, by[(u - kLag) % TM]);
+          }
+          if constexpr (j == 0) wr[(i + 2) % 4] = i < TN - 2 ? read_w(now, i + 2) : read_w(then, i + 2 - TN);
+          if constexpr (i == TN - 1) xr[j] = read_x(then, j), raw[j] = read_s(then, j);
+          if constexpr (t >= 0)
+            static_for<t * LOADS / kTail, (t + 1) * LOADS / kTail>([&](auto l_c) __attribute__((always_inline)) { issue_one(l_c, now); });
+        });
+        load_b += load_step, load_s += load_step ? s_ld : 0;
+        sb = sb_next;
+        now = then;
+      }
     }
     static_for<0, kLag>([&](auto u_c) __attribute__((always_inline)) {
       constexpr int u = decltype(u_c)::value;
@@ -423,10 +431,11 @@ hipError_t launch(const Call& c, int splits, float* sums) {
   });
 }
 
-// Tile and parts of K.  A launch takes its rounds (workgroups over what the CUs hold) times its stages times what a stage takes:
-// measured, in us, where a CU holds one workgroup and where it holds all it can; parts cost a launch and the sums' way through
-// memory.  Over 18 shapes of 24 to 1,502 tokens what is chosen is the fastest of 29 forms or within 4% of it, once 14%: 100 tokens of 17,408 x
-// 5,120 30 us in 6 parts (53 in one), 512 of 4,096 x 4,096 15.5 with 64 x 128 (26 with 128 x 256), 1,502 29 with 128 x 256 (45 with 256 x 256).
+// Tile and parts of K.  A launch takes its rounds (workgroups over what the CUs hold) times its stages times what a
+// stage takes: measured, in us, where a CU holds one workgroup and where it holds all it can; parts cost a launch and
+// the sums' way through memory.  Over 18 shapes of 24 to 1,502 tokens what is chosen is the fastest of 29 forms or
+// within 4% of it, once 14%: 100 tokens of 17,408 x 5,120 30 us in 6 parts (53 in one), 512 of 4,096 x 4,096 15.5 with
+// 64 x 128 (26 with 128 x 256), 1,502 29 with 128 x 256 (45 with 256 x 256).
 struct Tile {
   int bm, bn, per_cu;
   double one, full;

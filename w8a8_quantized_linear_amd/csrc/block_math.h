@@ -16,22 +16,22 @@ namespace lm {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// 128 columns of 16 weight rows and 16 tokens: lane l holds 32 columns of row l % 16 of both, l / 16 the same quarter of them, and gets
-// token l % 16, weight rows 4 (l / 16) .. + 3.
+// 128 columns of 16 weight rows and 16 tokens: lane l holds 32 columns of row l % 16 of both, l / 16 the same quarter of
+// them, and gets token l % 16, weight rows 4 (l / 16) .. + 3.
 __device__ __forceinline__ f32x4 mfma128(i32x8 w, i32x8 x) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
 }
 
-// Memory from `base` on, for loads of a scalar and a 32-bit lane offset (the scalar part stays out of the lanes' registers).
-// The range is left open: what is read is the caller's to keep inside.
+// Memory from `base` on, for loads of a scalar and a 32-bit lane offset (the scalar part stays out of the lanes'
+// registers). The range is left open: what is read is the caller's to keep inside.
 typedef __amdgpu_buffer_rsrc_t Buffer;
 __device__ __forceinline__ Buffer buffer(const void* base) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, -1, 0x00020000);
 }
-// Packed rows' operand at lane offset `at` (row's place + 16 h), scalar offset `from`: columns 16 h .. + 15 and 64 + 16 h ..
-// + 15 of a block, so that each load of a wave is one run of 1 KiB.  (Which columns meet in which lanes is free as long as
-// both operands agree.  32 columns a lane in order leave every load half of twice as many lines: 64 tokens of 5,120 x
-// 34,816 took 2 to 5% longer that way.)
+// Packed rows' operand at lane offset `at` (row's place + 16 h), scalar offset `from`: columns 16 h .. + 15 and 64 + 16
+// h .. + 15 of a block, so that each load of a wave is one run of 1 KiB.  (Which columns meet in which lanes is free as
+// long as both operands agree.  32 columns a lane in order leave every load half of twice as many lines: 64 tokens of
+// 5,120 x 34,816 took 2 to 5% longer that way.)
 __device__ __forceinline__ i32x8 load_operand(Buffer p, uint32_t at, uint32_t from) {
   const u32x4 a = __builtin_amdgcn_raw_buffer_load_b128(p, (int)at, (int)from, 0);
   const u32x4 b = __builtin_amdgcn_raw_buffer_load_b128(p, (int)at + 2048, (int)from, 0);
@@ -39,11 +39,6 @@ __device__ __forceinline__ i32x8 load_operand(Buffer p, uint32_t at, uint32_t fr
 }
 __device__ __forceinline__ float load_scale(Buffer p, uint32_t at, uint32_t from) {
   return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(p, (int)at, (int)from, 0));
-}
-
-__device__ __forceinline__ i32x8 load_operand(const uint8_t* at) {
-  const u32x4 a = reinterpret_cast<const u32x4*>(at)[0], b = reinterpret_cast<const u32x4*>(at)[128];
-  return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
 // Largest of lanes l, l ^ 16, l ^ 32 and l ^ 48.

@@ -11,9 +11,10 @@ using namespace lm;
 
 constexpr int kThreads = 256;   // of the weight's quantizer
 
-// A workgroup of T threads for each row, V pieces of 8 columns a thread, T * 8 columns apart, so that 16 lanes hold a block of 128: two
-// bytes read and one written a value, nothing shared between waves.  (Threads dealt over rows and columns alike need a division each,
-// which takes longer than the rest for few rows: 5 x 17,408 5.0 us.)
+// A workgroup of T threads for each row, V pieces of 8 columns a thread, T * 8 columns apart, so that 16 lanes hold a
+// block of 128: two bytes read and one written a value, nothing shared between waves.  (Threads dealt over rows and
+// columns alike need a division each, which takes longer than the rest for few rows: 5 x 17,408 5.0 us, 3.6 this way.)
+// Bound by memory for many rows, 4,000 x 16,384 37.6 us (5.2 TB/s), and by three dependent steps for few.
 template <int V>
 __global__ void __launch_bounds__(1024)
 quantize_block(const uint16_t* __restrict__ x, int64_t M, int K, bool packed, uint8_t* __restrict__ q, float* __restrict__ s_out, int64_t first) {

@@ -8,6 +8,11 @@
 //   int8, E4M3: scale (amax / 127, amax / 448) r over the row or over each 128 columns, codes of z over amax / 127
 //   (448).  r is in the scale alone: it is common to a row, so codes of z are codes of y, and y is not rounded on
 //   the way.  That also leaves one reduction: sum of squares and amax of z meet in one exchange.
+//
+// A workgroup for each row, whose pieces stay in registers between the reduction and the output: everything is read and
+// written once, and that is what bounds it.  12,016 x 5,120 with a residual and block scales 77 us (433 MB, 5.6 TB/s),
+// 2,270 x 5,120 to E4M3 10.0 us (35 MB, 3.5 TB/s: one round, whose beginning and end nothing hides); a single row is a
+// load, two exchanges and a store one behind the other, 2.0 us in the kernel.
 #include "decode.h"
 #include "layer.h"
 #include "layer_math.h"
@@ -52,8 +57,8 @@ __device__ __forceinline__ u32x4 sum_of(u32x4 x, u32x4 r) {
   return narrow8(a);
 }
 
-// z of a piece, rotated where asked; adds the squares of h to sum.  Columns past the row's end count as zeros.  (16 lanes of a block of 128 are
-// in or out together.)
+// z of a piece, rotated where asked; adds the squares of h to sum.  Columns past the row's end count as zeros.  (16
+// lanes of a block of 128 are in or out together.)
 template <bool ROT>
 __device__ __forceinline__ void scaled(u32x4 h4, u32x4 w4, bool in, int lane, float (&z)[8], float (&sum)[4]) {
   float h[8], w[8];
@@ -168,8 +173,9 @@ norm_rows(Norm n, int64_t first) {
   for (int j = 0; j < V; ++j) out.write(n, row, (int64_t)(j * T + tid) * 8, in[j], lane, z[j]);
 }
 
-// Rows of more columns than a workgroup's registers hold (K > 65,536): each piece is read twice, the second time out of a cache.
-// 300 x 131,072 with a residual: 81 us (3.9 TB/s of what must move); with 16 pieces a thread in norm_rows, which spill, 250 us.
+// Rows of more columns than a workgroup's registers hold (K > 65,536): each piece is read twice, the second time out of
+// a cache. 300 x 131,072 with a residual: 81 us (3.9 TB/s of what must move); with 16 pieces a thread in norm_rows,
+// which spill, 250 us.
 template <NormOut OUT, bool ROT>
 __global__ void __launch_bounds__(1024)
 norm_wide(Norm n, int64_t first) {
@@ -225,11 +231,11 @@ hipError_t launch_v(const Norm& n, int T, hipStream_t stream) {
 
 }  // namespace
 
-// As few pieces a thread as fit: 12,016 x 5,120 with a residual and block scales 80.7 us with one piece in 640 threads, 87.6 with three
-// in 256; 2,270 x 17,408 56.6 with three in 768, 63.1 with four in 576.  A row that is read alone and is no residual's is in flight
-// for too short a time for that: 2,270 x 5,120 to E4M3 13.7 us with one piece in 640 threads, 10.6 with two in 320 (bf16, 4,000 x
-// 8,192: 26.8 and 27.8).  Eight pieces spill up to ten registers and still are the faster form: 300 x 65,536 with a residual 30.4 us,
-// 32.4 in norm_wide.
+// As few pieces a thread as fit: 12,016 x 5,120 with a residual and block scales 80.7 us with one piece in 640 threads,
+// 87.6 with three in 256; 2,270 x 17,408 56.6 with three in 768, 63.1 with four in 576.  A row that is read alone and is
+// no residual's is in flight for too short a time for that: 2,270 x 5,120 to E4M3 13.7 us with one piece in 640 threads,
+// 10.6 with two in 320 (bf16, 4,000 x 8,192: 26.8 and 27.8).  Eight pieces spill up to ten registers and still are the
+// faster form: 300 x 65,536 with a residual 30.4 us, 32.4 in norm_wide.
 hipError_t launch_norm(const Norm& n, hipStream_t stream) {
   const int64_t pieces = (n.K + 7) / 8;
   const int64_t most = n.residual || n.M <= 256 ? 1024 : 512;

@@ -1,8 +1,8 @@
 // Rotary positions of queries and keys.
 //
-// What it computes: pairs (a, b) of the first `rotary` values of every head become A (a cos t - b sin t, b cos t + a sin t),
-// t = p f_i for pair i of a token at position p; the rest of the head is copied, and so is a token that has no position
-// (p < 0).  Pairs are the halves' (i, i + rotary / 2) or neighbours (2i, 2i + 1).
+// What it computes: pairs (a, b) of the first `rotary` values of every head become A (a cos t - b sin t, b cos t + a sin
+// t), t = p f_i for pair i of a token at position p; the rest of the head is copied, and so is a token that has no
+// position (p < 0).  Pairs are the halves' (i, i + rotary / 2) or neighbours (2i, 2i + 1).
 //
 // Angles: f_i comes as a 64-bit fraction of a turn, so that the low 64 bits of p * turns_i are the exact fraction of the
 // angle of whole turns, at any position; its upper 32 bits are taken (2^-32 of a turn), split into the nearest quarter
@@ -10,8 +10,8 @@
 // it.  Nothing is read but 64 bits a pair, and no table bounds the positions.
 //
 // A thread keeps one unit of 8 pairs (16 values, two 16-byte pieces) of a token, computes its 8 sines and cosines once,
-// and turns that unit of one head after another.  Bound by memory: 8 x 1,502 tokens, 40 and 8 heads of 128, 295 MB in 55.9 us (5.3 TB/s); few
-// tokens by the launch (4.2 us).
+// and turns that unit of one head after another.  Bound by memory: 8 x 1,502 tokens, 40 and 8 heads of 128, 295 MB in
+// 55.9 us (5.3 TB/s); few tokens by the launch (4.2 us).
 #include "decode.h"
 #include "layer.h"
 #include "layer_math.h"
@@ -108,8 +108,8 @@ rope_rows(Rope r, int64_t first, int64_t rows, uint32_t parts, uint32_t slots) {
 hipError_t launch_rope(const Rope& r, hipStream_t stream) {
   const int all = r.q_heads + r.heads, slots = kThreads / (r.dim / 16);
   const int64_t rows = r.seqs * r.tokens;
-  // One head a thread, two where there are many rows: 298 tokens of 48 heads of 128 4.2 us (5.8 with six heads a thread), 1 x 1,502 8.2 (9.3
-  // with one, 8.5 with six), 8 x 1,502 55.9 (56.3 with one, 60.1 with six, 4.9 TB/s then).
+  // One head a thread, two where there are many rows: 298 tokens of 48 heads of 128 4.2 us (5.8 with six heads a
+  // thread), 1 x 1,502 8.2 (9.3 with one, 8.5 with six), 8 x 1,502 55.9 (56.3 with one, 60.1 with six, 4.9 TB/s then).
   const int parts = rows >= 1024 ? (all + 1) / 2 : all;
   // (a launch begins at a row: `parts` workgroups for every `slots` rows)
   return in_launches((rows + slots - 1) / slots, parts, kThreads, [&](int64_t first, int64_t count) {
