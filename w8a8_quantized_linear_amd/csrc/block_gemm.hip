@@ -17,12 +17,15 @@
 // What bounds it: 256 x 256 tiles the chip's power.  2,270 x 5,120 x 34,816 takes 350 to 372 us (2.2 to 2.3 PFLOP/s),
 // 8,192 x 8,192 x 8,192 435 (2.5), at 1.85 to 1.97 GHz of the 2.4 that 5 PFLOP/s need, the matrix unit busy for 66% of
 // the cycles.  The same products and multiply-adds on operands that stay in registers reach 3.45 PFLOP/s at whatever
-// clock that leaves, this kernel without its loads from memory 2.98; its barriers and the loads' latency are 0 to 3%.  A
-// matrix instruction of 32 x 32 outputs, 192 x 256 tiles and other wave priorities were no faster; a wave of 128 x 128
-// outputs, which would read a third less from LDS, has more sums than the 256 registers that vector instructions reach.
-// Smaller tiles: 1,502 x 4,096 x 4,096 29 us, one round of 192 workgroups on 256 CUs, the matrix unit of those busy for
-// 54%; 64 x 5,120 x 34,816 37 us, the weight's bytes at 4.8 TB/s.
+// clock that leaves, this kernel without its loads from memory 2.98; its barriers and the loads' latency are 0 to 3% at
+// that clock (10% where few workgroups run).  A matrix instruction of 32 x 32 outputs and other wave priorities were no
+// faster; a wave of 128 x 128 outputs, which would read a third less from LDS, has more sums than the 256 registers that
+// vector instructions reach.  Smaller tiles are for what fills the CUs better with them.  One wave a SIMD with twice the
+// outputs (192 x 128, 192 x 256 and 128 x 128 by four waves) takes as long as two for the same area or less: the barrier
+// has fewer to wait for.  1,502 x 4,096 x 4,096 26 us, one round of 256 workgroups; 64 x 5,120 x 34,816 37 us, the
+// weight's bytes at 4.8 TB/s.
 #include <algorithm>
+#include <iterator>
 #include <type_traits>
 
 #include "block_math.h"
@@ -431,16 +434,28 @@ hipError_t launch(const Call& c, int splits, float* sums) {
   });
 }
 
-// Tile and parts of K.  A launch takes its rounds (workgroups over what the CUs hold) times its stages times what a
-// stage takes: measured, in us, where a CU holds one workgroup and where it holds all it can; parts cost a launch and
-// the sums' way through memory.  Over 18 shapes of 24 to 1,502 tokens what is chosen is the fastest of 29 forms or
-// within 4% of it, once 14%: 100 tokens of 17,408 x 5,120 30 us in 6 parts (53 in one), 512 of 4,096 x 4,096 15.5 with
-// 64 x 128 (26 with 128 x 256), 1,502 29 with 128 x 256 (45 with 256 x 256).
+// Tile and parts of K.  A launch takes, in us, `begin`, `again` for each further round (workgroups over what the CUs
+// hold), and for each stage of a round from `one`, where there is a workgroup for each CU or fewer, to `full`, where
+// they hold all they can or take turns; parts cost a launch and the sums' way through memory.  Fitted to 141 shapes of
+// 24 to 5,729 tokens, weights of 512 x 1,024 to 34,816 x 17,408: of the forms measured for each (every tile in one part,
+// for 60 of the shapes in up to 16) the one that is chosen is the fastest or, on the mean, 0.4% behind it, 8% at most.
+// 1,502 x 4,096 x 4,096 26.1 us with 192 x 128, 27.9 with 128 x 256, 45 with 256 x 256; 2,270 x 5,120 x 5,120 53 with
+// 192 x 256, 57 with 256 x 256; 1,024 x 4,096 x 4,096 20.3 with 128 x 128, 21.7 with 64 x 256; 512 x 4,096 x 4,096 15.2
+// with 64 x 128, 22.9 with 192 x 128; 100 x 5,120 x 17,408 26.5 with 128 x 128, 31.7 with 64 x 256; 64 x 5,120 x 34,816
+// 38.1 with 64 x 256, 43 with 64 x 64.
 struct Tile {
   int bm, bn, per_cu;
-  double one, full;
+  double begin, again, one, full;
 };
-constexpr Tile kTiles[] = {{256, 256, 1, 1.40, 1.76}, {128, 256, 1, 0.82, 0.95}, {64, 256, 1, 0.60, 0.75}, {64, 128, 2, 0.45, 0.60}, {64, 64, 3, 0.41, 0.60}};
+constexpr Tile kTiles[] = {{256, 256, 1, 7.7, 4.2, 1.279, 1.385}, {192, 256, 1, 6.7, 5.0, 1.113, 1.152}, {128, 256, 1, 4.9, 3.6, 0.755, 0.839},
+                           {64, 256, 1, 4.7, 2.7, 0.524, 0.593},  {192, 128, 1, 5.0, 3.3, 0.610, 0.636}, {128, 128, 1, 4.6, 2.6, 0.469, 0.506},
+                           {64, 128, 2, 4.0, 1.8, 0.319, 0.617},  {64, 64, 3, 3.3, 1.4, 0.310, 0.591}};
+double time_of(const Tile& c, int64_t groups, int stages) {
+  const int64_t room = (int64_t)kCus * c.per_cu, rounds = groups <= room ? 1 : (groups + room - 1) / room;
+  const int64_t held = std::min<int64_t>((groups + kCus - 1) / kCus, c.per_cu);
+  const double busy = c.per_cu == 1 ? groups > kCus : (double)(held - 1) / (c.per_cu - 1);
+  return c.begin + c.again * (rounds - 1) + (double)rounds * stages * (c.one + (c.full - c.one) * busy);
+}
 struct Choice {
   int tile, splits;
 };
@@ -448,18 +463,16 @@ Choice choose(int64_t M, int64_t N, int64_t K) {
   const int blocks = (int)(K / kScaleBlock);
   Choice best{0, 1};
   double least = 1e30;
-  for (int t = 0; t < 5; ++t) {
+  for (int t = 0; t < (int)std::size(kTiles); ++t) {
     const Tile& c = kTiles[t];
     const int64_t tiles = (M + c.bm - 1) / c.bm * ((N + c.bn - 1) / c.bn);
-    const int room = kCus * c.per_cu;
     // (walking needs a few blocks of columns, and rows of outputs within 2^31 bytes of a tile's first)
     if (t == 0 && (blocks < 4 || N > (1 << 21))) continue;
     for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
-      if (splits > 1 && (t == 0 || blocks < 4 * splits || tiles * splits > 2 * room)) break;
+      if (splits > 1 && (t == 0 || blocks < 4 * splits || tiles * splits > 2 * kCus * c.per_cu)) break;
       const int stages = (blocks + splits - 1) / splits;
       if (splits > 1 && (splits - 1) * stages >= blocks) continue;   // (a part without a block)
-      const int64_t groups = tiles * splits, rounds = groups <= room ? 1 : (groups + room - 1) / room;
-      const double time = (double)rounds * stages * (groups <= kCus ? c.one : c.full) + (splits > 1 ? 4.0 + splits * 2.2e-6 * M * N : 0.0);
+      const double time = time_of(c, tiles * splits, stages) + (splits > 1 ? 3.0 + splits * 1.2e-6 * M * N : 0.0);
       if (time < least) least = time, best = {t, splits};
     }
   }
@@ -481,9 +494,12 @@ hipError_t launch_block_gemm(const uint8_t* q, const float* s, const uint8_t* w,
   const Call call{q, s, w, sw, bias, y, M, N, K, stream};
   switch (c.tile) {
     case 0: return launch<256, 256, 4, 2, 2, true>(call, 1, nullptr);
-    case 1: return launch<128, 256, 2, 4, 3, false>(call, c.splits, sums);
-    case 2: return launch<64, 256, 2, 4, 3, false>(call, c.splits, sums);
-    case 3: return launch<64, 128, 2, 2, 3, false>(call, c.splits, sums);
+    case 1: return launch<192, 256, 2, 2, 2, false>(call, c.splits, sums);
+    case 2: return launch<128, 256, 2, 4, 3, false>(call, c.splits, sums);
+    case 3: return launch<64, 256, 2, 4, 3, false>(call, c.splits, sums);
+    case 4: return launch<192, 128, 2, 2, 3, false>(call, c.splits, sums);
+    case 5: return launch<128, 128, 2, 2, 3, false>(call, c.splits, sums);
+    case 6: return launch<64, 128, 2, 2, 3, false>(call, c.splits, sums);
     default: return launch<64, 64, 2, 1, 3, false>(call, c.splits, sums);
   }
 }
