@@ -4,7 +4,7 @@
 // q[m][k] * w[n][k]) + bias[n]): the inner sums on the E4M3 matrix instructions (block_math.h), the outer one in fp32.
 //
 // A workgroup of WGM x WGN waves owns BM tokens x BN weight rows; a wave accumulates 16 TM tokens x 16 TN rows.  One
-// stage is one block of 128 columns of both operands, 128 bytes a row, and the tokens' scales, which NST LDS buffers take
+// stage is one block of 128 columns of both operands, 128 bytes a row, and the scales of both, which NST LDS buffers take
 // in turn by direct-to-LDS loads; each product starts from zero and is multiplied into the sums by s * sw, four
 // multiply-adds a lane beside 32 cycles of the matrix unit.
 //
@@ -14,16 +14,20 @@
 // stage behind it into the buffer that is free now, one or two beside each product (in one go, both waves of a SIMD left
 // the matrix unit idle meanwhile), and replaces each token operand by the next stage's behind its last product.
 //
-// What bounds it: 256 x 256 tiles the chip's power.  2,270 x 5,120 x 34,816 takes 350 to 372 us (2.2 to 2.3 PFLOP/s),
-// 8,192 x 8,192 x 8,192 435 (2.5), at 1.85 to 1.97 GHz of the 2.4 that 5 PFLOP/s need, the matrix unit busy for 66% of
-// the cycles.  The same products and multiply-adds on operands that stay in registers reach 3.45 PFLOP/s at whatever
-// clock that leaves, this kernel without its loads from memory 2.98; its barriers and the loads' latency are 0 to 3% at
-// that clock (10% where few workgroups run).  A matrix instruction of 32 x 32 outputs and other wave priorities were no
-// faster; a wave of 128 x 128 outputs, which would read a third less from LDS, has more sums than the 256 registers that
-// vector instructions reach.  Smaller tiles are for what fills the CUs better with them.  One wave a SIMD with twice the
-// outputs (192 x 128, 192 x 256 and 128 x 128 by four waves) takes as long as two for the same area or less: the barrier
-// has fewer to wait for.  1,502 x 4,096 x 4,096 26 us, one round of 256 workgroups; 64 x 5,120 x 34,816 37 us, the
-// weight's bytes at 4.8 TB/s.
+// What bounds it: a product takes the matrix unit for 32 cycles and leaves room for four vector instructions beside it;
+// each further one, and with one wave a SIMD each instruction of any kind, costs four cycles.  Four are the
+// multiply-adds, so the loop has little else: the scales of both operands come with the stage (a scalar load would be
+// waited for together with all LDS reads), places in LDS are stepped.  512 x 17,408 x 4,096, 32 tiles of 256 x 256 with
+// a CU each, takes 1.18 us a stage of 0.85 in products (1.23 with places computed anew and the weight's scales by scalar
+// loads), 0.09 of it at the barrier. With all CUs at work the clock is what limits: 8,192 x 8,192 x 8,192 takes 412 us
+// (2.67 PFLOP/s), 2,270 x 5,120 x 34,816 330 to 360 (2.3 to 2.5), at 1.85 to 1.97 GHz of the 2.4 that 5 PFLOP/s need.
+// The same products and multiply-adds on operands that stay in registers reach 3.45 PFLOP/s at whatever clock that
+// leaves, products alone 4.1; without its loads from memory the kernel is 14% faster then, without the barrier 1%.  A
+// matrix instruction of 32 x 32 outputs and other wave priorities were no faster; a wave of 128 x 128 outputs, which
+// would read a third less from LDS, has more sums than the 256 registers that vector instructions reach.
+//
+// Smaller tiles are for what fills the CUs better with them: 1,502 x 4,096 x 4,096 26 us, one round of 256 workgroups;
+// 64 x 5,120 x 34,816 38 us, the weight's bytes at 4.7 TB/s.
 #include <algorithm>
 #include <iterator>
 #include <type_traits>
@@ -38,14 +42,6 @@ namespace {
 using namespace lm;
 
 constexpr int kCus = 256;
-
-// A read-only value at an address that is uniform over the wave, by a scalar load: it is not counted with the loads of
-// the stages.
-__device__ __forceinline__ float uniform_load(const float* p) {
-  const uint64_t u = reinterpret_cast<uint64_t>(p);
-  const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(u >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)u);
-  return *reinterpret_cast<const __attribute__((address_space(4))) float*>(at);
-}
 
 template <int B, int E, typename F>
 __device__ __forceinline__ void static_for(F&& f) {
@@ -101,9 +97,10 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
            int split_blocks, float* __restrict__ sums) {
   constexpr int NT = 64 * WGM * WGN, WTM = BM / WGM, WTN = BN / WGN, TM = WTM / 16, TN = WTN / 16;
   constexpr int A_LOADS = BM * 8 / NT, B_LOADS = BN * 8 / NT, SCALES = (BM + BN) * 128;
-  constexpr int STAGE = SCALES + BM * 4, LOADS = A_LOADS + B_LOADS + 1, AREA = WALK ? 2048 : 0, BIAS = WALK ? BN * 2 : 0;
+  constexpr int STAGE = SCALES + BM * 4 + 256, LOADS = A_LOADS + B_LOADS + 1, AREA = WALK ? 2048 : 0, BIAS = WALK ? BN * 2 : 0;
   static_assert(A_LOADS * NT == BM * 8 && B_LOADS * NT == BN * 8, "whole loads");
   static_assert(WTN <= 128 && 128 % WTN == 0, "a wave's weight rows have one scale");
+  static_assert(WGM * WGN > BM / 64, "a wave for the weight's scales");
   static_assert(!WALK || NST == 2, "walking, a stage waits for every load, the bias and the last tile's stores among them");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NST * STAGE + WGM * WGN * AREA + 2 * BIAS];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, h = lane >> 4;
@@ -124,22 +121,24 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
     block0 = __builtin_amdgcn_readfirstlane(split) * split_blocks, blocks = min(split_blocks, all_blocks - block0);
   }
   // Loads of a tile: thread t of round i fills the 16 bytes at LDS place 16 (i NT + t), piece (t % 8) ^ key of row (i NT
-  // + t) / 8; rows past the last one are the last one again (their sums are not stored).  And the tokens' scales, 64 a
-  // wave (of waves beyond the tokens the same ones again: every wave issues as many loads).
+  // + t) / 8; rows past the last one are the last one again (their sums are not stored).  And one load of scales: the
+  // first waves 64 tokens' each, the others the weight rows', one for 128 rows (all the same: every wave issues as many
+  // loads).
   Buffer abuf, bbuf;
-  const float* load_s;                                    // the tokens' scales of the block to load (64 bits: they may lie far apart)
+  const bool token_scales = wave < BM / 64;
+  const float* load_s;                                    // the scales of the block to load (64 bits: they may lie far apart)
+  const int64_t s_step = token_scales ? s_ld : 1;         // from one block to the next
   uint32_t a_at[A_LOADS], b_at[B_LOADS], s_at;
   int64_t load_m, load_n;                                 // its first token and weight row
-  const float* load_sw;                                   // the scales of its weight rows of this wave, by block of columns
   int aimed = 0;                                          // tiles aimed at
-  const int s_wave = wave % (BM / 64), bias_wave = wave % (BN < 128 ? 1 : BN / 128);
+  const int bias_wave = wave % (BN < 128 ? 1 : BN / 128);
   auto place = [&](uint32_t r, int p) -> uint32_t { return r / 32 * 32 * (uint32_t)K + r % 32 * 64 + (p >> 2) * 2048 + (p & 3) * 16; };
   auto aim = [&](uint32_t t) __attribute__((always_inline)) {
     uint32_t tm, tn;
     tile_of(t, tiles_m, tiles_n, tm, tn);
     load_m = (int64_t)__builtin_amdgcn_readfirstlane(tm) * BM, load_n = (int64_t)__builtin_amdgcn_readfirstlane(tn) * BN;
-    abuf = buffer(q + load_m * K + block0 * 4096), bbuf = buffer(w + load_n * K + block0 * 4096), load_s = s + block0 * s_ld + load_m;
-    load_sw = sw + min(load_n + wn * WTN, N - 1) / kScaleBlock * all_blocks + block0;
+    abuf = buffer(q + load_m * K + block0 * 4096), bbuf = buffer(w + load_n * K + block0 * 4096);
+    load_s = token_scales ? s + block0 * s_ld + load_m : sw + load_n / kScaleBlock * all_blocks + block0;
     const uint32_t m_last = (uint32_t)min(M - 1 - load_m, (int64_t)BM), n_last = (uint32_t)min(N - 1 - load_n, (int64_t)BN);
     int id = tid;
     if constexpr (WALK) asm volatile("" : "+v"(id));      // (what follows from it is computed again, not kept in registers)
@@ -154,7 +153,7 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
       b_at[i] = place(min(r, n_last), (id & 7) ^ lds_key(r));
     }
     const int lane = id & 63;
-    s_at = min((uint32_t)(64 * s_wave + lane), m_last) * 4;
+    s_at = (token_scales ? min((uint32_t)(64 * wave + lane), m_last) : min((uint32_t)lane, n_last / kScaleBlock) * all_blocks) * 4;
     // walking, the tile's bias goes to LDS too (two places in turn; pairs of columns, those past N the last pair)
     if (WALK && bias)
       lds_load4(buffer(bias + load_n), min((uint32_t)(128 * bias_wave + 2 * lane), n_last - 1) * 2, 0,
@@ -162,26 +161,29 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
     ++aimed;
   };
   uint32_t load_at = at;
-  int load_b = 0;                                         // the block to load, of tile load_at
-  auto issue_one = [&](auto t_c, int to_stage) __attribute__((always_inline)) {   // load t of that stage
+  uint32_t load_k = 0;                                    // the block to load, of tile load_at: its place, 4096 a block
+  auto issue_one = [&](auto t_c, uint32_t to_stage) __attribute__((always_inline)) {   // load t of the stage at that place
     constexpr int t = decltype(t_c)::value;
-    uint8_t* to = lds + to_stage * STAGE;
-    if constexpr (t < A_LOADS) lds_load16(abuf, a_at[t], (uint32_t)load_b * 4096, to + wave * 1024 + t * NT * 16);
-    else if constexpr (t < A_LOADS + B_LOADS)
-      lds_load16(bbuf, b_at[t - A_LOADS], (uint32_t)load_b * 4096, to + BM * 128 + wave * 1024 + (t - A_LOADS) * NT * 16);
-    else lds_load4(buffer(load_s), s_at, 0, to + SCALES + s_wave * 256);
+    uint8_t* to = lds + to_stage;
+    if constexpr (t < A_LOADS) lds_load16(abuf, a_at[t], load_k, to + wave * 1024 + t * NT * 16);
+    else if constexpr (t < A_LOADS + B_LOADS) lds_load16(bbuf, b_at[t - A_LOADS], load_k, to + BM * 128 + wave * 1024 + (t - A_LOADS) * NT * 16);
+    else lds_load4(buffer(load_s), s_at, 0, to + SCALES + min(wave, BM / 64) * 256);
   };
 
-  auto read = [&](int stage, int row, int part) __attribute__((always_inline)) -> i32x8 {
-    // pieces h and 4 + h of the row: columns 16 h .. + 15 and 64 + 16 h .. + 15
-    const uint8_t* p = lds + stage * STAGE + part;
-    const u32x4 u = *reinterpret_cast<const u32x4*>(p + lds_piece(row, h)), v = *reinterpret_cast<const u32x4*>(p + lds_piece(row, 4 + h));
-    return i32x8{(int)u[0], (int)u[1], (int)u[2], (int)u[3], (int)v[0], (int)v[1], (int)v[2], (int)v[3]};
+  // Places in LDS of what this lane reads, which step from stage to stage (an instruction more beside a product is one
+  // too many: up to four vector instructions run in its shadow): pieces h and 4 + h, which are columns 16 h .. + 15 and
+  // 64 + 16 h .. + 15, of the first row of the wave's tokens and weight rows, the first token's scale and the weight
+  // rows'.
+  uint32_t x_at[2], w_at[2], ts_at = SCALES + (wm * WTM + c) * 4, ws_at = SCALES + BM * 4 + wn * WTN / kScaleBlock * 4;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) x_at[i] = lds_piece(wm * WTM + c, h + 4 * i), w_at[i] = BM * 128 + lds_piece(wn * WTN + c, h + 4 * i);
+  auto step_by = [&](uint32_t& at, int by) __attribute__((always_inline)) {
+    at += by;
+    asm volatile("" : "+v"(at));
   };
-  auto read_x = [&](int stage, int j) __attribute__((always_inline)) { return read(stage, wm * WTM + 16 * j + c, 0); };
-  auto read_w = [&](int stage, int i) __attribute__((always_inline)) { return read(stage, wn * WTN + 16 * i + c, BM * 128); };
-  auto read_s = [&](int stage, int j) __attribute__((always_inline)) {
-    return *reinterpret_cast<const float*>(lds + stage * STAGE + SCALES + (wm * WTM + 16 * j + c) * 4);
+  auto read = [&](const uint32_t (&at)[2], int k) __attribute__((always_inline)) -> i32x8 {   // 16 rows further each
+    const u32x4 u = *reinterpret_cast<const u32x4*>(lds + at[0] + 2048 * k), v = *reinterpret_cast<const u32x4*>(lds + at[1] + 2048 * k);
+    return i32x8{(int)u[0], (int)u[1], (int)u[2], (int)u[3], (int)v[0], (int)v[1], (int)v[2], (int)v[3]};
   };
   // Product u of a stage (weight operand u / TM, token operand u % TM) is added to the sums behind product u + kLag: an
   // instruction that reads a product's result too early waits for it.  The last kLag of a stage are added in the next.
@@ -189,7 +191,12 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
   static_assert(TN >= 4 && TN % 4 == 0 && TM >= 2, "products in flight, weight operands two ahead");
   f32x4 acc[TN][TM], part[kParts];
   i32x8 xr[TM], wr[4];
-  float by[TM], raw[TM];
+  float by[TM], raw[TM], raw_w;
+  auto read_scales = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < TM; ++j) raw[j] = *reinterpret_cast<const float*>(lds + ts_at + 64 * j);
+    raw_w = *reinterpret_cast<const float*>(lds + ws_at);
+  };
   auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < TN; ++i)
@@ -315,35 +322,37 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
   }
   aim(load_at);
   int64_t mb = load_m, nb = load_n;                       // the tile that is multiplied
-  const float* swp = load_sw;
 #pragma unroll
   for (int b = 0; b < NST; ++b) {
-    static_for<0, LOADS>([&](auto t_c) __attribute__((always_inline)) { issue_one(t_c, b); });
-    if (b + 1 < blocks) ++load_b, load_s += s_ld;         // (past the last block: that one again, not used)
+    static_for<0, LOADS>([&](auto t_c) __attribute__((always_inline)) { issue_one(t_c, b * STAGE); });
+    if (b + 1 < blocks) load_k += 4096, load_s += s_step;  // (past the last block: that one again, not used)
     if (b == NST - 2) landed();
   }
   __builtin_amdgcn_sched_barrier(0);
+  wr[0] = read(w_at, 0);                                  // (in the loop's order, so that it waits for no more than it needs)
+  wr[1] = read(w_at, 1);
 #pragma unroll
-  for (int j = 0; j < TM; ++j) raw[j] = read_s(0, j), xr[j] = read_x(0, j);
-  wr[0] = read_w(0, 0);
-  wr[1] = read_w(0, 1);
-  float sb = uniform_load(swp);
-  int now = 0;                                            // buffer of the stage that is multiplied
+  for (int j = 0; j < TM; ++j) {
+    xr[j] = read(x_at, j);
+    if (j == 0) read_scales();
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  uint32_t now = 0;                                       // place of the stage that is multiplied
   clear();
   for (int tile = 0;; ++tile) {
     // the loads are NST blocks ahead: of this tile, then of the next, or its last block again where there is none
-    int b = 0, load_step = 1;
+    int b = 0;
+    uint32_t load_step = 4096;
 #pragma clang loop unroll(disable)
     for (int part_of = 0; part_of < 2; ++part_of) {
       const int stop = part_of == 0 ? blocks - NST : blocks;
       if (part_of == 1) {
-        if (WALK && load_at + step < end) load_at += step, load_b = 0, aim(load_at);
-        else load_step = 0, load_s -= load_b == blocks ? s_ld : 0, load_b = blocks - 1;
+        if (WALK && load_at + step < end) load_at += step, load_k = 0, aim(load_at);
+        else load_step = 0, load_s -= load_k == (uint32_t)blocks * 4096 ? s_step : 0, load_k = (uint32_t)(blocks - 1) * 4096;
       }
 #pragma clang loop unroll(disable)
       for (; b < stop; ++b) {
-        const int then = now + 1 == NST ? 0 : now + 1;
-        const float sb_next = uniform_load(swp + min(b + 1, blocks - 1));
+        const int to_next = now == (NST - 1) * STAGE ? -(NST - 1) * STAGE : STAGE;
         static_for<0, P>([&](auto u_c) __attribute__((always_inline)) {
           constexpr int u = decltype(u_c)::value, i = u / TM, j = u % TM, t = u - (P - kTail);
           if constexpr (t == 0) landed();
@@ -352,17 +361,19 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
           if constexpr (u < kLag) {
             add(std::integral_constant<int, P - kLag + u>{}, by[TM - kLag + u]);
           } else {
-            if constexpr (u - kLag < TM) by[u - kLag] = raw[u - kLag] * sb;
+            if constexpr (u - kLag < TM) by[u - kLag] = raw[u - kLag] * raw_w;
             add(std::integral_constant<int, u - kLag>{}, by[(u - kLag) % TM]);
           }
-          if constexpr (j == 0) wr[(i + 2) % 4] = i < TN - 2 ? read_w(now, i + 2) : read_w(then, i + 2 - TN);
-          if constexpr (i == TN - 1) xr[j] = read_x(then, j), raw[j] = read_s(then, j);
+          if constexpr (t == 0) step_by(w_at[0], to_next), step_by(w_at[1], to_next);
+          if constexpr (j == 0) wr[(i + 2) % 4] = read(w_at, (i + 2) % TN);
+          if constexpr (i == TN - 1 && j == 0) step_by(x_at[0], to_next), step_by(x_at[1], to_next), step_by(ts_at, to_next), step_by(ws_at, to_next);
+          if constexpr (i == TN - 1) xr[j] = read(x_at, j);
+          if constexpr (i == TN - 1 && j == 0) read_scales();
           if constexpr (t >= 0)
             static_for<t * LOADS / kTail, (t + 1) * LOADS / kTail>([&](auto l_c) __attribute__((always_inline)) { issue_one(l_c, now); });
         });
-        load_b += load_step, load_s += load_step ? s_ld : 0;
-        sb = sb_next;
-        now = then;
+        load_k += load_step, load_s += load_step ? s_step : 0;
+        now += to_next;
       }
     }
     static_for<0, kLag>([&](auto u_c) __attribute__((always_inline)) {
@@ -373,8 +384,7 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
     if constexpr (!WALK) break;
     at += step;
     if (at >= end) break;
-    mb = load_m, nb = load_n, swp = load_sw;
-    sb = uniform_load(swp);
+    mb = load_m, nb = load_n;
     clear();
   }
   wait_loads<0>();                                        // nothing lands in LDS behind the workgroup's end
@@ -438,18 +448,18 @@ hipError_t launch(const Call& c, int splits, float* sums) {
 // hold), and for each stage of a round from `one`, where there is a workgroup for each CU or fewer, to `full`, where
 // they hold all they can or take turns; parts cost a launch and the sums' way through memory.  Fitted to 141 shapes of
 // 24 to 5,729 tokens, weights of 512 x 1,024 to 34,816 x 17,408: of the forms measured for each (every tile in one part,
-// for 60 of the shapes in up to 16) the one that is chosen is the fastest or, on the mean, 0.4% behind it, 8% at most.
-// 1,502 x 4,096 x 4,096 26.1 us with 192 x 128, 27.9 with 128 x 256, 45 with 256 x 256; 2,270 x 5,120 x 5,120 53 with
-// 192 x 256, 57 with 256 x 256; 1,024 x 4,096 x 4,096 20.3 with 128 x 128, 21.7 with 64 x 256; 512 x 4,096 x 4,096 15.2
-// with 64 x 128, 22.9 with 192 x 128; 100 x 5,120 x 17,408 26.5 with 128 x 128, 31.7 with 64 x 256; 64 x 5,120 x 34,816
-// 38.1 with 64 x 256, 43 with 64 x 64.
+// for 57 of the shapes in up to 16) the one that is chosen is the fastest or, on the mean, 0.4% behind it, 8% at most.
+// 1,502 x 4,096 x 4,096 26.2 us with 192 x 128, 27.4 with 128 x 256, 43.8 with 256 x 256; 2,270 x 5,120 x 5,120 52 with
+// 192 x 256, 57 with 256 x 256; 1,024 x 4,096 x 4,096 20.6 with 128 x 128, 21.7 with 64 x 256; 330 x 4,096 x 4,096 12.8
+// with 64 x 128, 15.1 with 64 x 64; 100 x 5,120 x 17,408 26.7 with 128 x 128, 31.8 with 64 x 256; 64 x 5,120 x 34,816
+// 38.5 with 64 x 256, 43.2 with 64 x 64.
 struct Tile {
   int bm, bn, per_cu;
   double begin, again, one, full;
 };
-constexpr Tile kTiles[] = {{256, 256, 1, 7.7, 4.2, 1.279, 1.385}, {192, 256, 1, 6.7, 5.0, 1.113, 1.152}, {128, 256, 1, 4.9, 3.6, 0.755, 0.839},
-                           {64, 256, 1, 4.7, 2.7, 0.524, 0.593},  {192, 128, 1, 5.0, 3.3, 0.610, 0.636}, {128, 128, 1, 4.6, 2.6, 0.469, 0.506},
-                           {64, 128, 2, 4.0, 1.8, 0.319, 0.617},  {64, 64, 3, 3.3, 1.4, 0.310, 0.591}};
+constexpr Tile kTiles[] = {{256, 256, 1, 7.9, 4.5, 1.241, 1.364}, {192, 256, 1, 6.6, 5.4, 1.080, 1.142}, {128, 256, 1, 5.0, 4.3, 0.681, 0.817},
+                           {64, 256, 1, 4.1, 2.8, 0.489, 0.570},  {192, 128, 1, 4.9, 3.5, 0.564, 0.618}, {128, 128, 1, 4.7, 2.4, 0.433, 0.490},
+                           {64, 128, 2, 4.1, 1.7, 0.274, 0.585},  {64, 64, 3, 3.6, 1.3, 0.258, 0.574}};
 double time_of(const Tile& c, int64_t groups, int stages) {
   const int64_t room = (int64_t)kCus * c.per_cu, rounds = groups <= room ? 1 : (groups + room - 1) / room;
   const int64_t held = std::min<int64_t>((groups + kCus - 1) / kCus, c.per_cu);
@@ -472,7 +482,7 @@ Choice choose(int64_t M, int64_t N, int64_t K) {
       if (splits > 1 && (t == 0 || blocks < 4 * splits || tiles * splits > 2 * kCus * c.per_cu)) break;
       const int stages = (blocks + splits - 1) / splits;
       if (splits > 1 && (splits - 1) * stages >= blocks) continue;   // (a part without a block)
-      const double time = time_of(c, tiles * splits, stages) + (splits > 1 ? 3.0 + splits * 1.2e-6 * M * N : 0.0);
+      const double time = time_of(c, tiles * splits, stages) + (splits > 1 ? 2.9 + splits * 1.4e-6 * M * N : 0.0);
       if (time < least) least = time, best = {t, splits};
     }
   }
@@ -498,7 +508,7 @@ hipError_t launch_block_gemm(const uint8_t* q, const float* s, const uint8_t* w,
     case 2: return launch<128, 256, 2, 4, 3, false>(call, c.splits, sums);
     case 3: return launch<64, 256, 2, 4, 3, false>(call, c.splits, sums);
     case 4: return launch<192, 128, 2, 2, 3, false>(call, c.splits, sums);
-    case 5: return launch<128, 128, 2, 2, 3, false>(call, c.splits, sums);
+    case 5: return launch<128, 128, 4, 2, 3, false>(call, c.splits, sums);
     case 6: return launch<64, 128, 2, 2, 3, false>(call, c.splits, sums);
     default: return launch<64, 64, 2, 1, 3, false>(call, c.splits, sums);
   }
