@@ -117,7 +117,7 @@ def test_quantize_weights(lib, N, K):
 SHAPES = ((7, 4360, 2048), (16, 8, 4096), (20, 4360, 256), (40, 4360, 384), (64, 40, 8192), (70, 8, 128), (66, 72, 4096), (100, 264, 5120), (130, 1032, 17408),
           (17, 8200, 6272), (70, 34824, 128), (129, 34824, 384), (300, 1032, 4096), (258, 5128, 2048), (520, 4104, 640), (1030, 8200, 256), (1, 8, 128), (1, 64, 256), (2, 136, 1024), (5, 24, 2176), (16, 256, 512), (17, 200, 384), (31, 128, 640), (33, 392, 256),
           (48, 264, 128), (64, 128, 1024), (65, 136, 512), (100, 520, 256), (129, 256, 384), (200, 72, 256), (257, 264, 128), (300, 136, 256),
-          (1030, 8200, 128), (1700, 7160, 1152), (1000, 5128, 128), (740, 7160, 512), (834, 4104, 128), (834, 4104, 1024), (65, 17416, 256))
+          (1030, 8200, 128), (1700, 7160, 1152), (1000, 5128, 128), (740, 7160, 512), (834, 4104, 128), (834, 4104, 1024), (65, 17416, 256), (2300, 16392, 1152), (5000, 8200, 640))
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -141,7 +141,7 @@ def test_linear(lib, M, N, K, bias):
 
 @pytest.mark.parametrize("M,N,K", ((1, 5120, 17408), (5, 5120, 17408), (64, 2056, 5120), (64, 5120, 17408), (100, 5120, 17408), (1502, 4096, 4096), (2270, 1160, 5120),
                                    (700, 17408, 1024), (4370, 4360, 640), (300, 65544, 512), (513, 33000, 1152), (189, 7176, 17408),
-                                   (65, 7176, 17408), (17, 17416, 5120), (2270, 5120, 5120), (200, 4104, 17408), (17, 7176, 17408), (64, 34824, 5120)))
+                                   (65, 7176, 17408), (17, 17416, 5120), (2270, 5120, 5120), (200, 4104, 17408), (17, 7176, 17408), (64, 34824, 5120), (65, 5120, 17408)))
 def test_large(lib, M, N, K):
     """Sampled rows and columns of larger products."""
     say(f"block linear {M} x {K} x {N}")

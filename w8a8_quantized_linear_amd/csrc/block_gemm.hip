@@ -9,22 +9,24 @@
 // multiply-adds a lane beside 32 cycles of the matrix unit.
 //
 // A stage's products run over the weight operands, each with all token operands of the wave, which stay in registers;
-// weight operands are read two ahead.  Two weight operands before its end the wave has read all of the stage: there it
-// waits until the next stage has landed and every wave is as far (one barrier a stage), then issues the loads of the
-// stage behind it into the buffer that is free now, one or two beside each product (in one go, both waves of a SIMD left
-// the matrix unit idle meanwhile), and replaces each token operand by the next stage's behind its last product.
+// weight operands are read kAhead ahead.  As many weight operands before its end the wave has read all of the stage:
+// there it waits until the next stage has landed and every wave is as far (one barrier a stage), then issues the loads
+// of the stage behind it into the buffer that is free now, one or two beside each product (in one go, both waves of a
+// SIMD left the matrix unit idle meanwhile), and replaces each token operand by the next stage's behind its last
+// product.
 //
 // What bounds it: a product takes the matrix unit for 32 cycles and leaves room for four vector instructions beside it;
 // each further one, and with one wave a SIMD each instruction of any kind, costs four cycles.  Four are the
 // multiply-adds, so the loop has little else: the scales of both operands come with the stage (a scalar load would be
 // waited for together with all LDS reads), places in LDS are stepped.  512 x 17,408 x 4,096, 32 tiles of 256 x 256 with
-// a CU each, takes 1.18 us a stage of 0.85 in products (1.23 with places computed anew and the weight's scales by scalar
-// loads), 0.09 of it at the barrier. With all CUs at work the clock is what limits: 8,192 x 8,192 x 8,192 takes 412 us
-// (2.67 PFLOP/s), 2,270 x 5,120 x 34,816 330 to 360 (2.3 to 2.5), at 1.85 to 1.97 GHz of the 2.4 that 5 PFLOP/s need.
-// The same products and multiply-adds on operands that stay in registers reach 3.45 PFLOP/s at whatever clock that
-// leaves, products alone 4.1; without its loads from memory the kernel is 14% faster then, without the barrier 1%.  A
-// matrix instruction of 32 x 32 outputs and other wave priorities were no faster; a wave of 128 x 128 outputs, which
-// would read a third less from LDS, has more sums than the 256 registers that vector instructions reach.
+// a CU each, takes 1.14 us a stage of 0.85 in products (1.23 with places computed anew and the weight's scales by scalar
+// loads, 1.18 with the barrier a weight operand later, so that the loads come in shorter runs). With all CUs at work the
+// clock is what limits: 8,192 x 8,192 x 8,192 takes 395 us (2.78 PFLOP/s), 2,270 x 5,120 x 34,816 330 (2.45), at about
+// 1.9 GHz of the 2.4 that 5 PFLOP/s need.  The same products and multiply-adds on operands that stay in registers reach
+// 3.45 PFLOP/s at whatever clock that leaves, products alone 4.1; without its loads from memory the kernel was 14%
+// faster then, without the barrier 1%.  A matrix instruction of 32 x 32 outputs and other wave priorities were no
+// faster; a wave of 128 x 128 outputs, which would read a third less from LDS, has more sums than the 256 registers that
+// vector instructions reach.
 //
 // Smaller tiles are for what fills the CUs better with them: 1,502 x 4,096 x 4,096 26 us, one round of 256 workgroups;
 // 64 x 5,120 x 34,816 38 us, the weight's bytes at 4.7 TB/s.
@@ -187,8 +189,10 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
   };
   // Product u of a stage (weight operand u / TM, token operand u % TM) is added to the sums behind product u + kLag: an
   // instruction that reads a product's result too early waits for it.  The last kLag of a stage are added in the next.
-  constexpr int P = TM * TN, kLag = TM > 3 ? 3 : TM - 1, kParts = 4, kTail = 2 * TM;
-  static_assert(TN >= 4 && TN % 4 == 0 && TM >= 2, "products in flight, weight operands two ahead");
+  // (Two weight operands ahead where few waves have few products each: 512 x 17,408 x 4,096 with 64 x 128 by four waves
+  // 45.4 us, 48.7 with three; 128 x 128 by eight 55 and 51.5, 256 x 256 161 and 156.)
+  constexpr int P = TM * TN, kLag = TM > 3 ? 3 : TM - 1, kParts = 4, kAhead = NT > 256 || TM > 2 ? 3 : 2, kTail = kAhead * TM;
+  static_assert(TN >= 4 && TN % 4 == 0 && TM >= 2, "products in flight, weight operands ahead");
   f32x4 acc[TN][TM], part[kParts];
   i32x8 xr[TM], wr[4];
   float by[TM], raw[TM], raw_w;
@@ -329,8 +333,8 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
     if (b == NST - 2) landed();
   }
   __builtin_amdgcn_sched_barrier(0);
-  wr[0] = read(w_at, 0);                                  // (in the loop's order, so that it waits for no more than it needs)
-  wr[1] = read(w_at, 1);
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) wr[i] = read(w_at, i);  // (in the loop's order, so that it waits for no more than it needs)
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
     xr[j] = read(x_at, j);
@@ -365,7 +369,7 @@ block_tile(const uint8_t* __restrict__ q, const float* __restrict__ s, const uin
             add(std::integral_constant<int, u - kLag>{}, by[(u - kLag) % TM]);
           }
           if constexpr (t == 0) step_by(w_at[0], to_next), step_by(w_at[1], to_next);
-          if constexpr (j == 0) wr[(i + 2) % 4] = read(w_at, (i + 2) % TN);
+          if constexpr (j == 0) wr[(i + kAhead) % 4] = read(w_at, (i + kAhead) % TN);
           if constexpr (i == TN - 1 && j == 0) step_by(x_at[0], to_next), step_by(x_at[1], to_next), step_by(ts_at, to_next), step_by(ws_at, to_next);
           if constexpr (i == TN - 1) xr[j] = read(x_at, j);
           if constexpr (i == TN - 1 && j == 0) read_scales();
@@ -448,18 +452,18 @@ hipError_t launch(const Call& c, int splits, float* sums) {
 // hold), and for each stage of a round from `one`, where there is a workgroup for each CU or fewer, to `full`, where
 // they hold all they can or take turns; parts cost a launch and the sums' way through memory.  Fitted to 141 shapes of
 // 24 to 5,729 tokens, weights of 512 x 1,024 to 34,816 x 17,408: of the forms measured for each (every tile in one part,
-// for 57 of the shapes in up to 16) the one that is chosen is the fastest or, on the mean, 0.4% behind it, 8% at most.
-// 1,502 x 4,096 x 4,096 26.2 us with 192 x 128, 27.4 with 128 x 256, 43.8 with 256 x 256; 2,270 x 5,120 x 5,120 52 with
-// 192 x 256, 57 with 256 x 256; 1,024 x 4,096 x 4,096 20.6 with 128 x 128, 21.7 with 64 x 256; 330 x 4,096 x 4,096 12.8
-// with 64 x 128, 15.1 with 64 x 64; 100 x 5,120 x 17,408 26.7 with 128 x 128, 31.8 with 64 x 256; 64 x 5,120 x 34,816
-// 38.5 with 64 x 256, 43.2 with 64 x 64.
+// for 57 of the shapes in up to 16) the one that is chosen is the fastest or, on the mean, 0.5% behind it, 9% at most.
+// 1,502 x 4,096 x 4,096 25.9 us with 192 x 128, 28.1 with 128 x 256, 42.2 with 256 x 256; 2,270 x 5,120 x 5,120 52 with
+// 192 x 256, 56 with 256 x 256; 1,024 x 4,096 x 4,096 20.0 with 128 x 128, 21.4 with 64 x 256; 330 x 4,096 x 4,096 13.1
+// with 64 x 128, 15.0 with 64 x 64; 100 x 5,120 x 17,408 26.8 with 128 x 128, 31.7 with 64 x 256; 64 x 5,120 x 34,816
+// 38.1 with 64 x 256, 43.2 with 64 x 64.
 struct Tile {
   int bm, bn, per_cu;
   double begin, again, one, full;
 };
-constexpr Tile kTiles[] = {{256, 256, 1, 7.9, 4.5, 1.241, 1.364}, {192, 256, 1, 6.6, 5.4, 1.080, 1.142}, {128, 256, 1, 5.0, 4.3, 0.681, 0.817},
-                           {64, 256, 1, 4.1, 2.8, 0.489, 0.570},  {192, 128, 1, 4.9, 3.5, 0.564, 0.618}, {128, 128, 1, 4.7, 2.4, 0.433, 0.490},
-                           {64, 128, 2, 4.1, 1.7, 0.274, 0.585},  {64, 64, 3, 3.6, 1.3, 0.258, 0.574}};
+constexpr Tile kTiles[] = {{256, 256, 1, 7.6, 4.7, 1.219, 1.336}, {192, 256, 1, 6.5, 5.4, 1.052, 1.129}, {128, 256, 1, 5.0, 4.7, 0.646, 0.798},
+                           {64, 256, 1, 3.8, 2.9, 0.501, 0.566},  {192, 128, 1, 4.9, 3.5, 0.545, 0.614}, {128, 128, 1, 4.3, 2.5, 0.429, 0.486},
+                           {64, 128, 2, 4.0, 1.7, 0.267, 0.594},  {64, 64, 3, 3.5, 1.3, 0.257, 0.571}};
 double time_of(const Tile& c, int64_t groups, int stages) {
   const int64_t room = (int64_t)kCus * c.per_cu, rounds = groups <= room ? 1 : (groups + room - 1) / room;
   const int64_t held = std::min<int64_t>((groups + kCus - 1) / kCus, c.per_cu);
@@ -482,7 +486,7 @@ Choice choose(int64_t M, int64_t N, int64_t K) {
       if (splits > 1 && (t == 0 || blocks < 4 * splits || tiles * splits > 2 * kCus * c.per_cu)) break;
       const int stages = (blocks + splits - 1) / splits;
       if (splits > 1 && (splits - 1) * stages >= blocks) continue;   // (a part without a block)
-      const double time = time_of(c, tiles * splits, stages) + (splits > 1 ? 2.9 + splits * 1.4e-6 * M * N : 0.0);
+      const double time = time_of(c, tiles * splits, stages) + (splits > 1 ? 2.8 + splits * 1.5e-6 * M * N : 0.0);
       if (time < least) least = time, best = {t, splits};
     }
   }
