@@ -462,7 +462,9 @@ w8a8_status w8a8_rope(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t
 /* ---- E4M3 projections with block scales ------------------------------------------
  * Codes E4M3FN; an activation's value is code * s of its token and 128 columns, a weight's code * s of its block of
  * 128 x 128 (rows past N are not counted).  scale = amax / 448 (fp32 IEEE division), code as w8a8_quantize_act_fp8's;
- * a block of zeros has scale 0 and codes 0. */
+ * a block of zeros has scale 0 and codes 0.  A block with a NaN has a NaN for its scale (codes 0), one with an infinity an
+ * infinite scale: a token with either gives no finite output (a NaN: NaNs only), and neither does a weight's block for the
+ * rows that it belongs to; other tokens' and rows' outputs are what they are without it. */
 
 /* Row stride of the scales that go with packed codes of M rows: M rounded up to a multiple of 32 (0 outside 1 .. 2^42). */
 int64_t w8a8_block_scale_stride(int64_t M);
@@ -479,7 +481,7 @@ w8a8_status w8a8_quantize_weight_block(const uint16_t* w, int64_t N, int64_t K, 
  * the E4M3 matrix instructions, which drop what lies 2^-13 below the largest of a group of their products (1.4e-5 of
  * the output's rms on normal values, 4e-5 with outliers of 20 times); the sum over blocks is fp32, rounded once.
  * Which form multiplies, and with it the order of the sum over blocks, depends on M, N and K.
- * M * N <= 2^40, N <= 2^28 - 32, M <= 2^30; a token that is not finite spoils its own row only.  The workspace holds fp32
+ * M * N <= 2^40, N <= 2^28 - 32, M <= 2^30; scales that are not finite as above.  The workspace holds fp32
  * partial sums where the shape is short of tiles, so that K is cut; its size is 0, and workspace may be NULL, where it is not. */
 size_t w8a8_fp8_block_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);   /* 0 also outside the limits */
 w8a8_status w8a8_fp8_block_gemm_packed(const uint8_t* q_packed, const float* s, const uint8_t* w_packed, const float* s_w,

@@ -94,7 +94,7 @@ block_few(const uint16_t* __restrict__ xb, const uint8_t* __restrict__ q, const 
           v[8 * i + 2 * e + 1] = qm::bf16hi(t.raw[i][e]);
         }
 #pragma unroll
-      for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(v[i]));
+      for (int i = 0; i < 32; ++i) m = larger(m, fabsf(v[i]));
       t.sx[0] = max_quarters(m) / 448.0f;
       const qm::QuotientScale qs = qm::quotient_scale(t.sx[0]);
       qm::apply_prefactor(v, qs);

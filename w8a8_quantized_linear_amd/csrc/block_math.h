@@ -41,14 +41,14 @@ __device__ __forceinline__ float load_scale(Buffer p, uint32_t at, uint32_t from
   return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(p, (int)at, (int)from, 0));
 }
 
-// Largest of lanes l, l ^ 16, l ^ 32 and l ^ 48.
+// Largest of lanes l, l ^ 16, l ^ 32 and l ^ 48, as larger().
 __device__ __forceinline__ float max_quarters(float v) {
   uint32_t u = __float_as_uint(v);
   const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  v = larger(__uint_as_float(a[0]), __uint_as_float(a[1]));
   u = __float_as_uint(v);
   const auto b = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+  return larger(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
 // Four sums of token m, rows n .. n + 3 (n % 4 == 0): the bias added, rounded once.

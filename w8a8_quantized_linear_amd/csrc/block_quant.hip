@@ -1,5 +1,6 @@
 // E4M3 codes with block scales: one for each 128 columns of an activation's row, one for each 128 x 128 block of a
-// weight.  scale = amax / 448, code = the nearest E4M3 value to x / scale; a block of zeros has scale 0 and codes 0.
+// weight.  scale = amax / 448, code = the nearest E4M3 value to x / scale; a block of zeros has scale 0 and codes 0, one with
+// a NaN a NaN for its scale.
 #include "decode.h"
 #include "layer.h"
 #include "layer_math.h"
@@ -33,7 +34,7 @@ quantize_block(const uint16_t* __restrict__ x, int64_t M, int K, bool packed, ui
     float v[8], m = 0.0f;
     widen8(raw[j], v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+    for (int i = 0; i < 8; ++i) m = larger(m, fabsf(v[i]));
     const float s = max16(m) / 448.0f;
     const qm::QuotientScale qs = qm::quotient_scale(s);
     qm::apply_prefactor(v, qs);
@@ -54,13 +55,13 @@ quantize_weight_block(const uint16_t* __restrict__ w, int64_t N, int64_t K, uint
   for (int i = 0; i < 8; ++i) {
     widen8(*reinterpret_cast<const u32x4*>(w + min(n0 + 16 * i, N - 1) * K + k0), v[i]);    // (past N: the last row again)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[i][e]));
+    for (int e = 0; e < 8; ++e) m = larger(m, fabsf(v[i][e]));
   }
   __shared__ float red[kThreads / 64];
   m = max64(m);
   if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = m;
   __syncthreads();
-  const float s = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])) / 448.0f;
+  const float s = larger(larger(red[0], red[1]), larger(red[2], red[3])) / 448.0f;
   const qm::QuotientScale qs = qm::quotient_scale(s);
   if (threadIdx.x == 0) s_out[block] = s;
 #pragma unroll

@@ -13,12 +13,16 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 // The value of another lane of the row of 16: i ^ 1, i ^ 2, i ^ 3, 7 - i of its eight, 15 - i, i ^ 8.
 constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kXor3 = 0x1B, kHalfMirror = 0x141, kMirror = 0x140, kXor8 = 0x128;
 
-// Maximum and sum over the 16 lanes of a row, the same in all of them.
+// The larger of two values; a NaN where one is (fmaxf gives the other one): what a scale is made of, so that a NaN shows in
+// all that the scale multiplies.  (One instruction for three values, as for fmaxf.)
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
+// Maximum (as larger()) and sum over the 16 lanes of a row, the same in all of them.
 __device__ __forceinline__ float max16(float v) {
-  v = fmaxf(v, qm::dpp_move<kXor1>(v));
-  v = fmaxf(v, qm::dpp_move<kXor2>(v));
-  v = fmaxf(v, qm::dpp_move<kHalfMirror>(v));
-  return fmaxf(v, qm::dpp_move<kMirror>(v));
+  v = larger(v, qm::dpp_move<kXor1>(v));
+  v = larger(v, qm::dpp_move<kXor2>(v));
+  v = larger(v, qm::dpp_move<kHalfMirror>(v));
+  return larger(v, qm::dpp_move<kMirror>(v));
 }
 __device__ __forceinline__ float sum16(float v) {
   v += qm::dpp_move<kXor1>(v);
@@ -33,10 +37,10 @@ __device__ __forceinline__ float max64(float v) {
   v = max16(v);
   uint32_t u = __float_as_uint(v);
   const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  v = larger(__uint_as_float(a[0]), __uint_as_float(a[1]));
   u = __float_as_uint(v);
   const auto b = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+  return larger(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 __device__ __forceinline__ float sum64(float v) {
   v = sum16(v);
@@ -60,7 +64,7 @@ __device__ __forceinline__ u32x4 narrow8(const float (&f)[8]) {
 }
 
 // E4M3 codes of eight values that carry the scale's pre-factor: the nearest to fl32(v / s) within +-448, the sign of
-// v on a zero (all codes +0 where the scale is zero).
+// v on a zero (all codes +0 where the scale is zero or a NaN).
 __device__ __forceinline__ u32x2 e4m3_codes8(const float (&v)[8], const qm::QuotientScale& q) {
   const uint32_t keep = q.s > 0.0f ? ~0u : 0u;
   u32x2 out;
