@@ -418,7 +418,8 @@ w8a8_status w8a8_kv_attention(const uint16_t* q, int64_t ldq, const int8_t* k_co
  * 128, in fp32.  Row-major codes are [M, K], their block scales [M, K / 128]; the _packed forms write the
  * packed layout (padding rows untouched), with block scales [K / 128][w8a8_block_scale_stride(M)].
  * A row of zeros gives zeros.  A row with a NaN or an infinity, or whose h^2 leave fp32's range
- * (|h| beyond about 2^60), spoils its own row only.
+ * (|h| beyond about 2^60), spoils its own row only.  A weight that is not finite spoils its column of y in bf16, and
+ * every scale over that column, in all rows.
  * 1 <= K <= W8A8_MAX_K, K % 8 == 0 (codes: K % 32 == 0; packed: K % 64 == 0; rot_block or block scales:
  * K % 128 == 0); eps finite and positive (W8A8_ERR_BAD_ARGUMENT otherwise). */
 w8a8_status w8a8_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps, uint16_t* h,

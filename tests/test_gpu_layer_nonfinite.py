@@ -83,3 +83,36 @@ def test_products(lib, M, N, K):
     z = lib.w8a8_fp8_block_linear_packed(x.cuda(), lib.w8a8_pack_weight(wq), N, sw, b)
     first = (N - 1) // 128 * 128
     assert torch.isnan(z[:, first:].float()).all() and torch.equal(z[:, :first], y[:, :first])
+
+
+def norm_inputs(M, K, seed):
+    rng = np.random.default_rng(seed)
+    x, r, w = rng.standard_normal((M, K)), rng.standard_normal((M, K)), 1 + 0.3 * rng.standard_normal(K)
+    return [torch.from_numpy(a.astype(np.float32)).to(torch.bfloat16).cuda() for a in (x, r, w)]
+
+
+# rows of one wave and of several, more than registers hold, threads behind the row's end
+@pytest.mark.parametrize("M,K", ((1, 128), (5, 1152), (300, 5120), (3, 67584)))
+@pytest.mark.parametrize("form,rot", (("int8", 0), ("int8", 128), ("fp8", 0), ("fp8", 128), ("block", 0)))
+@pytest.mark.parametrize("packed", (False, True))
+@pytest.mark.parametrize("value", (NAN, -NAN, INF))
+def test_a_norms_weight(lib, M, K, form, rot, packed, value):
+    """Codes behind a norm's weight with a value that is not finite: no scale over it is; scales of other blocks stay."""
+    say(f"norm {M} x {K} {form}, rotated {rot}, packed {packed}, {value} in its weight")
+    x, res, w = norm_inputs(M, K, K)
+    name = {"int8": "w8a8_rmsnorm_quantize", "fp8": "w8a8_rmsnorm_quantize_fp8", "block": "w8a8_rmsnorm_quantize_block"}[form]
+    f = getattr(lib, name + ("_packed" if packed else ""))
+    more = {} if form == "block" else dict(rot_block=rot)
+    _, s, h = f(x, w, res, **more)
+    at = K - 70 if M > 1 else 3
+    spoiled = w.clone()
+    spoiled[at] = value
+    _, t, g = f(x, spoiled, res, **more)
+    if form == "block":
+        s, t = (s.t()[:M], t.t()[:M]) if packed else (s, t)
+        assert not torch.isfinite(t[:, at // 128]).any() and (value == INF or torch.isnan(t[:, at // 128]).all())
+        keep = torch.arange(K // 128, device="cuda") != at // 128
+        assert torch.equal(t[:, keep], s[:, keep])
+    else:
+        assert not torch.isfinite(t).any() and (value == INF or torch.isnan(t).all())
+    assert torch.equal(g, h)

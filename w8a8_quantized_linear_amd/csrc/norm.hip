@@ -62,11 +62,10 @@ __device__ __forceinline__ u32x4 sum_of(u32x4 x, u32x4 r) {
 template <bool ROT>
 __device__ __forceinline__ void scaled(u32x4 h4, u32x4 w4, bool in, int lane, float (&z)[8], float (&sum)[4]) {
   float h[8], w[8];
-  widen8(h4, h);
-  widen8(w4, w);
+  widen8(in ? h4 : u32x4{0, 0, 0, 0}, h);
+  widen8(in ? w4 : u32x4{0, 0, 0, 0}, w);   // (both: a zero times a weight that is not finite is a NaN)
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    h[i] = in ? h[i] : 0.0f;
     sum[i & 3] = __builtin_fmaf(h[i], h[i], sum[i & 3]);
     z[i] = h[i] * w[i];
   }
@@ -75,7 +74,7 @@ __device__ __forceinline__ void scaled(u32x4 h4, u32x4 w4, bool in, int lane, fl
 
 __device__ __forceinline__ float top_of(const float (&z)[8], float top) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(z[i]));
+  for (int i = 0; i < 8; ++i) top = larger(top, fabsf(z[i]));
   return top;
 }
 
@@ -95,7 +94,7 @@ __device__ __forceinline__ void meet(float& total, float& top) {
   total = 0.0f;
   for (int w = 0; w < waves; ++w) {
     total += red[0][w];
-    top = fmaxf(top, red[1][w]);
+    top = larger(top, red[1][w]);
   }
 }
 
