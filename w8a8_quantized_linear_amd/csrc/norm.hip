@@ -2,7 +2,8 @@
 //
 // What it computes, for a row x of K bf16 values:
 //   h = bf16(x + residual) (fp32 sum; x without a residual), written out for the next addition;
-//   z = h * weight, exact in fp32 (8 + 8 bits), z rotated by the normalized transform in blocks of 128 where asked;
+//   z = h * weight, exact in fp32 (8 + 8 bits; below 2^-126 a multiple of 2^-149), z rotated by the normalized transform
+//   in blocks of 128 where asked;
 //   r = 1 / sqrt(mean(h^2) + eps);
 //   bf16: y = bf16(z r);
 //   int8, E4M3: scale (amax / 127, amax / 448) r over the row or over each 128 columns, codes of z over amax / 127
@@ -105,7 +106,10 @@ struct Out {
   qm::QuotientScale qs;
   __device__ __forceinline__ Out(const Norm& n, int64_t row, float total, float top) : r(1.0f / sqrtf(total / (float)n.K + n.eps)) {
     if constexpr (OUT == NormOut::kI8 || OUT == NormOut::kFp8) {
-      const float s = top / (OUT == NormOut::kI8 ? 127.0f : 448.0f);
+      float s = top / (OUT == NormOut::kI8 ? 127.0f : 448.0f);
+      // int8 codes have no clamp: amax / s is 127 but for half a step of fp32.  A scale below the normal range may be off by half
+      // of itself; one that was rounded down so far goes up instead (1.496 * 2^-149 became 2^-149, and amax the code -66).
+      if (OUT == NormOut::kI8 && 127.25f * s < top) s += 0x1p-149f;
       if (threadIdx.x == 0) n.scales[row] = s * r;
       qs = qm::quotient_scale(s);
     }
