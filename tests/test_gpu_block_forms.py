@@ -1,9 +1,10 @@
-"""Block products whose K is cut into parts, two calls at once."""
+"""Block products in every tile, whole and with K in parts, and calls of the latter at once."""
 import pytest
 import torch
 
+from block_forms import FORMS
 from parity import say
-from test_gpu_fp8_block import inputs, near
+from test_gpu_fp8_block import check, inputs, near, some
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +40,17 @@ def test_two_streams_at_once(lib, M, N, K):
                     g.append(lib.w8a8_fp8_block_gemm_packed(*c, wp, sw, M, N, K, b))
         torch.cuda.synchronize()
         assert all(torch.equal(y, t) for ys, t in zip(got, want) for y in ys)
+
+
+@pytest.mark.parametrize("M,N,K,tile,parts", FORMS)
+def test_forms(lib, M, N, K, tile, parts):
+    say(f"block linear {M} x {K} x {N}: {tile[0]} x {tile[1]} in {parts}")
+    assert lib.fp8_block_gemm_workspace_bytes(M, N, K) // (4 * M * N) == (parts if parts > 1 else 0)
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    x = torch.randn(M, K, generator=g, device="cuda").to(torch.bfloat16)
+    b = torch.randn(N, generator=g, device="cuda").to(torch.bfloat16)
+    wq, sw = lib.w8a8_quantize_weight_block((torch.randn(N, K, generator=g, device="cuda") * 0.02).to(torch.bfloat16))
+    y = lib.w8a8_fp8_block_linear_packed(x, lib.w8a8_pack_weight(wq), N, sw, b)
+    q, s = lib.w8a8_quantize_act_block(x)
+    check(y, q.cpu().numpy(), s.cpu().numpy(), wq.cpu().numpy(), sw.cpu().numpy(), b, "forms", some(M, N)[::3], some(N, M)[::2])
+    near(y, (q, s), (wq, sw), b)

@@ -31,9 +31,9 @@
 // Smaller tiles are for what fills the CUs better with them: 1,502 x 4,096 x 4,096 26 us, one round of 256 workgroups;
 // 64 x 5,120 x 34,816 38 us, the weight's bytes at 4.7 TB/s.
 #include <algorithm>
-#include <iterator>
 #include <type_traits>
 
+#include "block_choice.h"
 #include "block_math.h"
 #include "decode.h"
 #include "layer.h"
@@ -42,8 +42,9 @@ namespace w8a8 {
 namespace {
 
 using namespace lm;
-
-constexpr int kCus = 256;
+using block_choice::choose;
+using block_choice::Choice;
+using block_choice::kCus;
 
 template <int B, int E, typename F>
 __device__ __forceinline__ void static_for(F&& f) {
@@ -446,51 +447,6 @@ hipError_t launch(const Call& c, int splits, float* sums) {
     hipLaunchKernelGGL(add_splits, dim3((unsigned)count), dim3(256), 0, c.stream, sums, splits, c.bias, c.y, c.M * c.N, c.N, first);
     return hipGetLastError();
   });
-}
-
-// Tile and parts of K.  A launch takes, in us, `begin`, `again` for each further round (workgroups over what the CUs
-// hold), and for each stage of a round from `one`, where there is a workgroup for each CU or fewer, to `full`, where
-// they hold all they can or take turns; parts cost a launch and the sums' way through memory.  Fitted to 141 shapes of
-// 24 to 5,729 tokens, weights of 512 x 1,024 to 34,816 x 17,408: of the forms measured for each (every tile in one part,
-// for 57 of the shapes in up to 16) the one that is chosen is the fastest or, on the mean, 0.5% behind it, 9% at most.
-// 1,502 x 4,096 x 4,096 25.9 us with 192 x 128, 28.1 with 128 x 256, 42.2 with 256 x 256; 2,270 x 5,120 x 5,120 52 with
-// 192 x 256, 56 with 256 x 256; 1,024 x 4,096 x 4,096 20.0 with 128 x 128, 21.4 with 64 x 256; 330 x 4,096 x 4,096 13.1
-// with 64 x 128, 15.0 with 64 x 64; 100 x 5,120 x 17,408 26.8 with 128 x 128, 31.7 with 64 x 256; 64 x 5,120 x 34,816
-// 38.1 with 64 x 256, 43.2 with 64 x 64.
-struct Tile {
-  int bm, bn, per_cu;
-  double begin, again, one, full;
-};
-constexpr Tile kTiles[] = {{256, 256, 1, 7.6, 4.7, 1.219, 1.336}, {192, 256, 1, 6.5, 5.4, 1.052, 1.129}, {128, 256, 1, 5.0, 4.7, 0.646, 0.798},
-                           {64, 256, 1, 3.8, 2.9, 0.501, 0.566},  {192, 128, 1, 4.9, 3.5, 0.545, 0.614}, {128, 128, 1, 4.3, 2.5, 0.429, 0.486},
-                           {64, 128, 2, 4.0, 1.7, 0.267, 0.594},  {64, 64, 3, 3.5, 1.3, 0.257, 0.571}};
-double time_of(const Tile& c, int64_t groups, int stages) {
-  const int64_t room = (int64_t)kCus * c.per_cu, rounds = groups <= room ? 1 : (groups + room - 1) / room;
-  const int64_t held = std::min<int64_t>((groups + kCus - 1) / kCus, c.per_cu);
-  const double busy = c.per_cu == 1 ? groups > kCus : (double)(held - 1) / (c.per_cu - 1);
-  return c.begin + c.again * (rounds - 1) + (double)rounds * stages * (c.one + (c.full - c.one) * busy);
-}
-struct Choice {
-  int tile, splits;
-};
-Choice choose(int64_t M, int64_t N, int64_t K) {
-  const int blocks = (int)(K / kScaleBlock);
-  Choice best{0, 1};
-  double least = 1e30;
-  for (int t = 0; t < (int)std::size(kTiles); ++t) {
-    const Tile& c = kTiles[t];
-    const int64_t tiles = (M + c.bm - 1) / c.bm * ((N + c.bn - 1) / c.bn);
-    // (walking needs a few blocks of columns, and rows of outputs within 2^31 bytes of a tile's first)
-    if (t == 0 && (blocks < 4 || N > (1 << 21))) continue;
-    for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
-      if (splits > 1 && (t == 0 || blocks < 4 * splits || tiles * splits > 2 * kCus * c.per_cu)) break;
-      const int stages = (blocks + splits - 1) / splits;
-      if (splits > 1 && (splits - 1) * stages >= blocks) continue;   // (a part without a block)
-      const double time = time_of(c, tiles * splits, stages) + (splits > 1 ? 2.8 + splits * 1.5e-6 * M * N : 0.0);
-      if (time < least) least = time, best = {t, splits};
-    }
-  }
-  return best;
 }
 
 }  // namespace
