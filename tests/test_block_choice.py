@@ -16,6 +16,9 @@ PROGRAM = r'''
 using namespace w8a8::block_choice;
 int main() {
   for (const Tile& t : kTiles) std::printf("tile %d %d\n", t.bm, t.bn);
+  for (long long steps = 1; steps <= 128; steps *= 2)
+    for (long long wide = 8; wide <= 1 << 20; wide *= 2)
+      if (fused_fits(1, wide, 1024 * steps)) std::printf("fused %lld %lld\n", wide, steps);
   long long m, n, k;
   while (std::scanf("%lld %lld %lld", &m, &n, &k) == 3) {
     const Choice c = choose(m, n, k);
@@ -39,14 +42,15 @@ def ask(tmp_path_factory):
         out = subprocess.run([str(d / "choice")], input="\n".join("%d %d %d" % s for s in shapes), capture_output=True, text=True, timeout=60)
         assert out.returncode == 0
         lines = [line.split() for line in out.stdout.splitlines()]
+        fused = [tuple(map(int, line[1:])) for line in lines if line[0] == "fused"]
         tiles = [tuple(map(int, line[1:])) for line in lines if line[0] == "tile"]
-        got = [tuple(map(int, line)) for line in lines if line[0] != "tile"]
-        return tiles, [(g[:3], g[3:5], g[5]) for g in got]
+        got = [tuple(map(int, line)) for line in lines if line[0].isdigit()]
+        return tiles, [(g[:3], g[3:5], g[5]) for g in got], fused
     return ask
 
 
 def test_every_form_is_met(ask):
-    tiles, got = ask([f[:3] for f in FORMS])
+    tiles, got, _ = ask([f[:3] for f in FORMS])
     assert got == [(f[:3], f[3], f[4]) for f in FORMS]
     assert {f[3] for f in FORMS if f[4] == 1} == set(tiles)
     assert {f[3] for f in FORMS if f[4] > 1} == set(tiles) - {(256, 256)}
@@ -63,3 +67,10 @@ def test_parts_have_blocks_and_a_workspace(ask):
         blocks = k // 128
         assert (parts - 1) * -(-blocks // parts) < blocks
         assert size(m, n, k) == (0 if parts == 1 else -(-4 * parts * m * n // 256) * 256)
+
+
+def test_tokens_quantized_in_every_workgroup(ask):
+    """Where each of eight waves has four steps of 128 columns at most; longer rows take a launch of their own, whatever the weight's rows."""
+    fused = ask([])[2]
+    assert {steps for _, steps in fused} == {1, 2, 4}
+    assert {n for n, steps in fused if steps == 1} == {1 << i for i in range(3, 14)}

@@ -54,3 +54,18 @@ def test_forms(lib, M, N, K, tile, parts):
     q, s = lib.w8a8_quantize_act_block(x)
     check(y, q.cpu().numpy(), s.cpu().numpy(), wq.cpu().numpy(), sw.cpu().numpy(), b, "forms", some(M, N)[::3], some(N, M)[::2])
     near(y, (q, s), (wq, sw), b)
+
+
+@pytest.mark.parametrize("M,N,K", ((5, 64, 131072), (20, 136, 131072), (139, 136, 131072), (16, 1032, 4096), (16, 1032, 4224)))
+def test_long_rows(lib, M, N, K):
+    """The longest rows, and rows on both sides of where tokens are quantized in every workgroup."""
+    say(f"block linear {M} x {K} x {N}")
+    x, w, b = inputs(M, N, K, 41)
+    wq, sw = lib.w8a8_quantize_weight_block(w.cuda())
+    wp = lib.w8a8_pack_weight(wq)
+    y = lib.w8a8_fp8_block_linear_packed(x.cuda(), wp, N, sw, b.cuda())
+    q, s = lib.w8a8_quantize_act_block(x.cuda())
+    check(y, q.cpu().numpy(), s.cpu().numpy(), wq.cpu().numpy(), sw.cpu().numpy(), b, "long rows", some(M, N)[::4], some(N, M)[::4])
+    near(y, (q, s), (wq, sw), b.cuda())
+    qp, sp = lib.w8a8_quantize_act_block_packed(x.cuda())
+    assert torch.equal(lib.w8a8_fp8_block_gemm_packed(qp, sp, wp, sw, M, N, K, b.cuda()), y)

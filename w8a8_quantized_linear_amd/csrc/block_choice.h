@@ -1,5 +1,5 @@
-// Which tile multiplies E4M3 codes with block scales (block_gemm.hip), and in how many parts of K: host code by itself, for the launch,
-// the workspace's size and the tests of both.
+// Which form multiplies E4M3 codes with block scales: of few tokens (block_few.hip), or which tile (block_gemm.hip) in how many parts of
+// K.  Host code by itself, for the launches, the workspace's size and the tests of both.
 #pragma once
 
 #include <algorithm>
@@ -12,6 +12,21 @@ namespace w8a8 {
 namespace block_choice {
 
 constexpr int kCus = 256;
+
+// Up to 16 tokens the form of few tokens reads the weight about as fast as memory gives it.  For more, whose codes every
+// workgroup reads again, up to weights of 48 Mi: 64 tokens of 5,120 x 7,168 11.4 us (12.7 with tiles), but 17,408 x 5,120
+// 34.4 (22.8 with tiles).
+inline bool few_fits(int64_t M, int64_t N, int64_t K) { return M <= 16 || (M <= 64 && N * K <= (48 << 20)); }
+
+// Its workgroups quantize x themselves, a launch less, where a wave has four steps at most and the weight few blocks in all.  1 and 16
+// tokens, in us, made so and by a launch of their own: 1,024 x 1,024 3.4 and 3.8, 5.8 and 6.7; 2,048 x 4,096 4.9 and 6.7, 6.5 and 7.4;
+// with four steps 4,096 x 1,024 6.7 and 8.3, 6.3 and 6.9, but 6.8 and 8.5, 8.8 and 8.9 for calls from Python one behind the other, which
+// a second launch holds up; with eight 8,192 x 1,024 11.0 and 13.1, 9.2 and 10.9, and with 128 131,072 x 64 138 and 147, 62 and
+// 77.  (5,120 x 5,120, one token: 8.8 against 6.6 and the quantizer.)
+constexpr int kFusedWaves = 8;
+inline bool fused_fits(int64_t M, int64_t N, int64_t K) {
+  return M <= 16 && K / kScaleBlock <= 4 * kFusedWaves && (N + 15) / 16 * (K / kScaleBlock) <= 4096;
+}
 
 // Tile and parts of K.  A launch takes, in us, `begin`, `again` for each further round (workgroups over what the CUs
 // hold), and for each stage of a round from `one`, where there is a workgroup for each CU or fewer, to `full`, where

@@ -12,11 +12,12 @@
 // trips to memory and the joining of the sums: 1 token of 1,024 x 1,024 3.8 us.
 //
 // FUSED: x comes as bf16 and every workgroup quantizes the tokens itself, in operand layout: a lane holds a quarter of a
-// block of one token.  That saves a launch (about 2 us) and costs about a thousand cycles a step, so it is for weights of
+// block of one token.  That saves a launch (about 2 us) and costs about a thousand cycles a step, so it is for rows of
 // few steps.
+#include "block_choice.h"
+#include "block_math.h"
 #include "decode.h"
 #include "layer.h"
-#include "block_math.h"
 
 namespace w8a8 {
 namespace {
@@ -164,10 +165,7 @@ hipError_t launch(const uint16_t* x, const uint8_t* q, const float* s, const uin
 
 }  // namespace
 
-// Up to 16 tokens this form reads the weight about as fast as memory gives it.  For more, whose codes every workgroup
-// reads again, up to weights of 48 Mi: 64 tokens of 5,120 x 7,168 11.4 us (12.7 with tiles), but 17,408 x 5,120 34.4
-// (22.8 with tiles).
-bool block_few_fits(int64_t M, int64_t N, int64_t K) { return M <= 16 || (M <= 64 && N * K <= (48 << 20)); }
+bool block_few_fits(int64_t M, int64_t N, int64_t K) { return block_choice::few_fits(M, N, K); }
 
 // Weight rows of a workgroup: 16 while that gives one workgroup a CU at most (12 tokens of 4,096 x 4,096 5.7 us, 6.2
 // with 32 rows; 24 tokens 5.7 and 6.6; 48 tokens 7.4 and 8.7) and, up to 16 tokens, where it gives many (8 tokens of
@@ -189,13 +187,11 @@ hipError_t launch_block_few(const uint8_t* q, const float* s, const uint8_t* w, 
   return launch<4, 2, 4, 2, false>(nullptr, q, s, w, sw, bias, y, M, N, K, stream);
 }
 
-// A launch less (2 us) against quantizing in every workgroup: 1 token of 1,024 x 1,024 3.9 us in all, 5,120 x 5,120 8.8
-// against 6.6 and the quantizer.
-bool block_fused_fits(int64_t M, int64_t N, int64_t K) { return M <= 16 && (N + 15) / 16 * (K / kScaleBlock) <= 4096; }
+bool block_fused_fits(int64_t M, int64_t N, int64_t K) { return block_choice::fused_fits(M, N, K); }
 
 hipError_t launch_block_fused(const uint16_t* x, const uint8_t* w, const float* sw, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N,
                               int64_t K, hipStream_t stream) {
-  return launch<8, 1, 1, 2, true>(x, nullptr, nullptr, w, sw, bias, y, M, N, K, stream);
+  return launch<block_choice::kFusedWaves, 1, 1, 2, true>(x, nullptr, nullptr, w, sw, bias, y, M, N, K, stream);
 }
 
 }  // namespace w8a8
