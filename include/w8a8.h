@@ -489,7 +489,7 @@ w8a8_status w8a8_fp8_block_gemm_packed(const uint8_t* q_packed, const float* s, 
                                        const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K, void* workspace,
                                        size_t workspace_bytes, hipStream_t stream);
 
-/* x is quantized into the workspace (packed codes and scales; a short call may leave it unused), then multiplied. */
+/* x is quantized into the workspace (packed codes and scales; a short call may leave it unused), then multiplied. M * K <= 2^42. */
 size_t w8a8_fp8_block_workspace_bytes(int64_t M, int64_t N, int64_t K);        /* 0 for M <= 0 and outside the limits */
 w8a8_status w8a8_fp8_block_linear_packed(const uint16_t* x, const uint8_t* w_packed, const float* s_w, const uint16_t* bias,
                                          uint16_t* y, int64_t M, int64_t N, int64_t K, void* workspace,

@@ -52,6 +52,12 @@ w8a8_status check_block_shape(int64_t M, int64_t N, int64_t K) {
   return W8A8_OK;
 }
 
+// And with x [M, K] to quantize.
+w8a8_status check_linear_shape(int64_t M, int64_t N, int64_t K) {
+  const w8a8_status st = check_block_shape(M, N, K);
+  return st == W8A8_OK && M > kMaxValues / K ? W8A8_ERR_BAD_SHAPE : st;
+}
+
 // The packed codes of M tokens and their scales in a workspace.
 size_t code_bytes(int64_t M, int64_t K) {
   const size_t rows = (size_t)w8a8::block_scale_stride(M);
@@ -160,15 +166,14 @@ w8a8_status w8a8_fp8_block_gemm_packed(const uint8_t* q_packed, const float* s, 
 }
 
 size_t w8a8_fp8_block_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return M <= 0 || check_block_shape(M, N, K) != W8A8_OK ? 0 : code_bytes(M, K) + w8a8_fp8_block_gemm_workspace_bytes(M, N, K);
+  return M <= 0 || check_linear_shape(M, N, K) != W8A8_OK ? 0 : code_bytes(M, K) + w8a8_fp8_block_gemm_workspace_bytes(M, N, K);
 }
 
 w8a8_status w8a8_fp8_block_linear_packed(const uint16_t* x, const uint8_t* w_packed, const float* s_w, const uint16_t* bias,
                                          uint16_t* y, int64_t M, int64_t N, int64_t K, void* workspace,
                                          size_t workspace_bytes, hipStream_t stream) {
-  w8a8_status st = check_block_shape(M, N, K);
+  w8a8_status st = check_linear_shape(M, N, K);
   if (st != W8A8_OK) return st;
-  if (M > kMaxValues / K) return W8A8_ERR_BAD_SHAPE;
   if (M == 0) return W8A8_OK;
   if (workspace_bytes < w8a8_fp8_block_workspace_bytes(M, N, K)) return W8A8_ERR_BAD_ARGUMENT;
   if (!x || !w_packed || !s_w || !y || !workspace) return W8A8_ERR_NULL_POINTER;
