@@ -417,9 +417,9 @@ w8a8_status w8a8_kv_attention(const uint16_t* q, int64_t ldq, const int8_t* k_co
  * rounded to bf16 on the way.  rot_block == 128: codes of y turned by the normalized transform in blocks of
  * 128, in fp32.  Row-major codes are [M, K], their block scales [M, K / 128]; the _packed forms write the
  * packed layout (padding rows untouched), with block scales [K / 128][w8a8_block_scale_stride(M)].
- * A row of zeros gives zeros.  A row with a NaN or an infinity, or whose h^2 leave fp32's range
- * (|h| beyond about 2^60), spoils its own row only.  A weight that is not finite spoils its column of y in bf16, and
- * every scale over that column, in all rows.
+ * A row of zeros gives zeros.  A row with a NaN or an infinity, or whose sum of h^2 leaves fp32's range
+ * (one |h| of 2^64, or all of 2^64 / sqrt(K)), spoils its own row only.  A weight that is not finite spoils its
+ * column of y in bf16, and every scale over that column, in all rows.
  * 1 <= K <= W8A8_MAX_K, K % 8 == 0 (codes: K % 32 == 0; packed: K % 64 == 0; rot_block or block scales:
  * K % 128 == 0); eps finite and positive (W8A8_ERR_BAD_ARGUMENT otherwise). */
 w8a8_status w8a8_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps, uint16_t* h,
@@ -480,7 +480,8 @@ w8a8_status w8a8_quantize_weight_block(const uint16_t* w, int64_t N, int64_t K, 
 
 /* y[m][n] = bf16( sum_b s[b][m] * s_w[n / 128][b] * sum_{k in b} q[m][k] * w[n][k] + bias[n] ).  The inner sums run on
  * the E4M3 matrix instructions, which drop what lies 2^-13 below the largest of a group of their products (1.4e-5 of
- * the output's rms on normal values, 4e-5 with outliers of 20 times); the sum over blocks is fp32, rounded once.
+ * the output's rms on normal values, 4e-5 with outliers of 20 times); the sum over blocks is fp32, rounded once
+ * (and so is s * s_w, each block's factor).
  * Which form multiplies, and with it the order of the sum over blocks, depends on M, N and K.
  * M * N <= 2^40, N <= 2^28 - 32, M <= 2^30; scales that are not finite as above.  The workspace holds fp32
  * partial sums where the shape is short of tiles, so that K is cut; its size is 0, and workspace may be NULL, where it is not. */

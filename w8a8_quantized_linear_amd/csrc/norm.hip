@@ -12,8 +12,9 @@
 //
 // A workgroup for each row, whose pieces stay in registers between the reduction and the output: everything is read and
 // written once, and that is what bounds it.  12,016 x 5,120 with a residual and block scales 77 us (433 MB, 5.6 TB/s),
-// 2,270 x 5,120 to E4M3 10.0 us (35 MB, 3.5 TB/s: one round, whose beginning and end nothing hides); a single row is a
-// load, two exchanges and a store one behind the other, 2.0 us in the kernel.
+// 2,270 x 5,120 to E4M3 10.0 us (35 MB, 3.5 TB/s: a CU holds six workgroups of 320 threads, 1,536 in all, so the rows take
+// one and a half rounds, of which the second is half empty); a single row is a load, two exchanges and a store one behind
+// the other, 2.0 us in the kernel.
 #include "decode.h"
 #include "layer.h"
 #include "layer_math.h"
@@ -235,10 +236,11 @@ hipError_t launch_v(const Norm& n, int T, hipStream_t stream) {
 }  // namespace
 
 // As few pieces a thread as fit: 12,016 x 5,120 with a residual and block scales 80.7 us with one piece in 640 threads,
-// 87.6 with three in 256; 2,270 x 17,408 56.6 with three in 768, 63.1 with four in 576.  A row that is read alone and is
-// no residual's is in flight for too short a time for that: 2,270 x 5,120 to E4M3 13.7 us with one piece in 640 threads,
-// 10.6 with two in 320 (bf16, 4,000 x 8,192: 26.8 and 27.8).  Eight pieces spill up to ten registers and still are the
-// faster form: 300 x 65,536 with a residual 30.4 us, 32.4 in norm_wide.
+// 87.6 with three in 256; 2,270 x 17,408 56.6 with three in 768, 63.1 with four in 576.  Without a residual
+// half the threads with twice the pieces: 2,270 x 5,120 to E4M3 10.2 us with two in 320 threads, 12.4 with one in 640; bf16 9.5 and
+// 10.5; 12,016 x 8,192 bf16 70 and 75, to int8 57 and 74; 300 x 5,120 bf16 3.3 and 3.5, with block scales 4.2 and 4.0 (the one
+// of 49 measured, from 300 x 5,120 to 12,016 x 8,192, that loses).  Eight pieces, of which the block-scaled form spills three
+// registers, still are the faster form: 300 x 65,536 with a residual 30.4 us, 32.4 in norm_wide.
 hipError_t launch_norm(const Norm& n, hipStream_t stream) {
   const int64_t pieces = (n.K + 7) / 8;
   const int64_t most = n.residual || n.M <= 256 ? 1024 : 512;
