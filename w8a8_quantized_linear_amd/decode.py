@@ -125,8 +125,8 @@ class DecoderLayer:
         """What the layer adds, and what it adds it to: (y, residual), bf16 [seqs, tokens, hidden] each, whose sum is the layer's
         output; it takes its input as such a pair too (residual None: x alone), so that the sums are left to the norms."""
         seqs, tokens, hidden = x.shape
-        rows = x.reshape(seqs * tokens, hidden)
-        before = None if residual is None else residual.reshape(seqs * tokens, hidden)
+        rows = x.contiguous().view(seqs * tokens, hidden)                       # (copied where it is a slice: the last tokens of prompts)
+        before = None if residual is None else residual.contiguous().view(seqs * tokens, hidden)
         if isinstance(self.norm1, torch.Tensor):
             qkv, rows = self.qkv.behind_norm(rows, self.norm1, self.eps, before)
         else:
